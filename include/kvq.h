@@ -374,6 +374,123 @@ kvq_status kvq_attend_decode_ref(const uint16_t* q, const uint16_t* k, const uin
                                  uint16_t* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------- pages
+ * A paged cache holds the tokens of many requests of different lengths (not on the pages of
+ * the paper). Layouts, P = page_size tokens per page, a power of two from 16 to 128:
+ *      code pages     u8   [num_pages, Hkv, P, D * bits / 8]
+ *      scale pages    fp16 [num_pages, Hkv, P, D / G]
+ *      block table    int32[B, max_pages]: row b lists the pages of request b, in order;
+ *                     consecutive rows are table_stride (>= max_pages) entries apart
+ *      slot           int32: page * P + place in the page; num_pages * P <= 2^31 - 1
+ * K and V pages share one table. Lengths, tables and slots are device data, so the host
+ * checks cannot see them; what a kernel does with an entry outside its range is said at
+ * each call, and none reads or writes outside the buffers given. Every call is one launch
+ * on `stream` (kvq_encode_paged: one per two jobs) and may be captured into a CUDA graph.
+ */
+
+/*
+ * kvq_page_plan -- the block tables and slot maps of one serving step, built on the GPU:
+ * request b has kv_lens[b] cached tokens and gets q_lens[b] new ones (negative lengths
+ * count as 0). With have = ceil(kv / P), want = ceil((kv + q) / P), need = want - have:
+ *   a request whose `want` exceeds max_pages is refused, and needs nothing; the others are
+ *   served in order while the running total of their needs (upto) fits the free entries
+ *   left, n_free - *free_head; once it does not, every later request with need > 0 is
+ *   refused as well (those that fit their last page are served).
+ *   Served: table entries have .. want - 1 = free_pages[*free_head + upto - need ...],
+ *   kv_lens_out = kv + q. Refused: table row unchanged, kv_lens_out = kv, slots -1.
+ *   kv_lens, q_lens  int32[B];  B <= 16384.
+ *   block_table  in and out; free_pages int32[n_free], read only.
+ *   free_head    int32[1]: entries of the free list taken so far; free_head_out int32[1]
+ *                gets the new value. May be the same address, as kv_lens_out may be kv_lens.
+ *   slots, positions  int32[n_slots], new tokens packed request after request: slot (-1:
+ *                refused) and position kv + j; -1 and -1 behind the last new token. New
+ *                tokens past n_slots get no entry (info[0] > n_slots tells).
+ *   q_starts     int32[B + 1]: exclusive prefix sums of q_lens (saturating at 2^31 - 1).
+ *   info         int32[4]: new tokens, pages taken, requests refused, pages wanted.
+ * Integers only and no atomics on outputs: the same inputs give the same outputs.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+kvq_status kvq_page_plan(const int32_t* kv_lens, const int32_t* q_lens, int B, int32_t* block_table, int max_pages,
+                         int64_t table_stride, const int32_t* free_pages, int n_free, const int32_t* free_head,
+                         int32_t* free_head_out, int page_size, int32_t* slots, int32_t* positions, int n_slots,
+                         int32_t* q_starts, int32_t* kv_lens_out, int32_t* info, void* stream);
+
+/*
+ * kvq_page_release -- finished requests give their pages back: for every row with done[b]
+ * != 0 (u8[B]), in row order, its ceil(kv_lens[b] / P) pages are put in front of the free
+ * list's head (page i of the rows' sequence at entry head - 1 - i), *free_head goes down by
+ * their number and kv_lens[b] becomes 0. Pages beyond the entries in front of the head
+ * (more pages than were ever taken) are dropped. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+kvq_status kvq_page_release(const uint8_t* done, int32_t* kv_lens, const int32_t* block_table, int64_t table_stride,
+                            int B, int max_pages, int page_size, int32_t* free_pages, int n_free, int32_t* free_head,
+                            void* stream);
+
+/*
+ * kvq_encode_paged -- kvq_encode of n tokens (rows of Hkv heads) into pages: token i goes
+ * to slots[i] (int32[n], device), head h of it to row slot % P of pages[slot / P][h]. A
+ * slot outside [0, num_pages * P) (-1: a padded or refused token) is skipped; the rows of
+ * other slots are left as they were. Slots must be distinct: two tokens with the same slot
+ * leave a mixture of the two.
+ *   x      fp16, token i and head h at x + i * token_stride + h * head_stride elements, D
+ *          contiguous (strides multiples of 8, e.g. a part of a fused projection); the
+ *          strides of a dimension of size one are ignored.
+ * The jobs (e.g. K and V) share n, Hkv <= 128, the slots and the page geometry, and the
+ * plans' head_dim, group, transform, code width and device; two share a launch. Always the
+ * dense tensor-core encode (kvq_set_encode_path does not apply).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, DEVICE, CUDA.
+ */
+typedef struct kvq_paged_encode_job {
+  const kvq_plan* plan;
+  const uint16_t* x;
+  uint8_t* codes;    /* u8   [num_pages, Hkv, P, D * bits / 8] */
+  uint16_t* scales;  /* fp16 [num_pages, Hkv, P, D / G] */
+  int64_t token_stride, head_stride;
+} kvq_paged_encode_job;
+
+kvq_status kvq_encode_paged(const kvq_paged_encode_job* jobs, int njobs, int n, int Hkv, int page_size, int num_pages,
+                            const int32_t* slots, void* stream);
+
+/*
+ * kvq_decode_paged -- kvq_decode of the rows at n slots (any order, repeats allowed):
+ * out fp16 [n, Hkv, D]; a slot outside the pages gives zeros. n * Hkv <= 2^31 - 129.
+ * Always the tensor-core decode. Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, DEVICE, CUDA.
+ */
+kvq_status kvq_decode_paged(const kvq_plan* plan, const uint8_t* codes, const uint16_t* scales, int num_pages,
+                            int page_size, int Hkv, const int32_t* slots, int n, uint16_t* out, void* stream);
+
+/*
+ * kvq_attend_paged -- causal attention of ragged queries over the pages, in the rotated
+ * domain as kvq_attend_decode. Request b holds kv_lens[b] tokens in its pages (its queries'
+ * own tokens included) and has the query tokens q_starts[b] .. q_starts[b + 1] - 1 of q;
+ * q_starts NULL: one each, token b. Its j-th of m query tokens stands at position
+ * pos = kv_lens[b] - m + j and attends tokens t <= pos, with window > 0 only t > pos - window.
+ *   q          fp16, token i and head h at q + i * q_token_stride + h * q_head_stride
+ *              (multiples of 8), D contiguous; n_q tokens in all.
+ *   block_table, kv_lens (clamped to max_pages * P), q_starts: device.
+ *   max_q_len  no request has more query tokens (those past it get no output);
+ *   max_kv_len no request holds more tokens than this (longer ones are cut to it).
+ *   softmax_scale  <= 0 selects 1/sqrt(D).
+ *   out        fp16 [n_q, Hq, D]. A query with nothing to attend to gets zeros; rows of
+ *              tokens that belong to no request are left as they were.
+ *   workspace  >= kvq_paged_workspace_size bytes, zero before its first use (every call
+ *              leaves its counters zero); not to be used by two calls at once.
+ * A table entry outside [0, num_pages) raises device error flag 8 (kvq_poll_device_errors)
+ * and page 0 is read in its place; entries of pages with no attended token are not read.
+ * Codes and scales behind a request's last token may hold anything.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, DEVICE, CUDA.
+ */
+size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int head_dim, int n_q, int max_q_len);
+
+kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const uint8_t* k_codes, const uint16_t* k_scales,
+                            const uint8_t* v_codes, const uint16_t* v_scales, int num_pages, int page_size,
+                            const int32_t* block_table, int max_pages, int64_t table_stride, const int32_t* kv_lens,
+                            const int32_t* q_starts, int B, int n_q, int Hq, int Hkv, int max_q_len, int max_kv_len,
+                            int window, float softmax_scale, uint16_t* out, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/*
  * kvq_attend_split_info -- the sequence split the attention entry points choose for
  * these shapes on the current device (not on the pages; a planning query, e.g. to
  * size buffers or to check which merge path a call takes). One unit is one (batch
@@ -409,7 +526,8 @@ kvq_status kvq_debug_wait_timeout(uint32_t limit_us, void* stream);
  * *flags, host, may be NULL) the bit flags raised by kernels of this library
  * since the last poll, and clears them: 1 = a kernel gave up waiting for a TMA
  * load (bounded wait of 1 s), 2 = a bulk store did not drain, 4 = an attention
- * cluster merge did not receive (or release) a partial within 1 s. 0 means none.
+ * cluster merge did not receive (or release) a partial within 1 s, 8 = a block table
+ * named a page outside the cache. 0 means none.
  * Errors: CUDA.
  */
 kvq_status kvq_poll_device_errors(uint32_t* flags);

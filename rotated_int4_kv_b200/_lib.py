@@ -32,11 +32,18 @@ class AttendJob(ctypes.Structure):
                 ("v_scales", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+class PagedEncodeJob(ctypes.Structure):
+    """Mirror of ``kvq_paged_encode_job`` in include/kvq.h."""
+    _fields_ = [("plan", ctypes.c_void_p), ("x", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python rotated_int4_kv_b200/build.py` "
                           "(nvcc, sm_100a). There is no fallback implementation.")
     lib = ctypes.CDLL(LIB_PATH)
+    L = ctypes.c_int64
     P, I, F, S, U32P = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint32)
     sig = {
         "kvq_plan_create": (I, [ctypes.POINTER(P), I, I, P, P]),
@@ -58,6 +65,12 @@ def _load() -> ctypes.CDLL:
         "kvq_attend_decode_ref": (I, [P, P, P, I, I, I, I, I, P, I, F, P, P, S, P]),
         "kvq_attend_decode_noalloc": (I, [P, P, P, P, P, P, P, I, I, I, I, P, I, F, P, P]),
         "kvq_attend_decode_batch": (I, [ctypes.POINTER(AttendJob), I, I, I, I, I, P, I, F, P, S, P]),
+        "kvq_page_plan": (I, [P, P, I, P, I, L, P, I, P, P, I, P, P, I, P, P, P, P]),
+        "kvq_page_release": (I, [P, P, P, L, I, I, I, P, I, P, P]),
+        "kvq_encode_paged": (I, [ctypes.POINTER(PagedEncodeJob), I, I, I, I, I, P, P]),
+        "kvq_decode_paged": (I, [P, P, P, I, I, I, P, I, P, P]),
+        "kvq_paged_workspace_size": (S, [I, I, I, I, I, I]),
+        "kvq_attend_paged": (I, [P, P, P, L, L, P, P, P, P, I, I, P, I, L, P, P, I, I, I, I, I, I, I, F, P, P, S, P]),
         "kvq_poll_device_errors": (I, [U32P]),
         "kvq_attend_split_info": (I, [I, I, I, I, I, I, I, ctypes.POINTER(I), ctypes.POINTER(I), ctypes.POINTER(I)]),
         "kvq_debug_wait_timeout": (I, [ctypes.c_uint32, P]),

@@ -55,6 +55,7 @@ class Plan:
         self.group = int(group)
         self.transform = transform
         self.bits = int(bits)
+        self.device_index = torch.cuda.current_device() if torch.cuda.is_available() else -1
         self._h = ctypes.c_void_p()
         check(lib.kvq_plan_create_ex(ctypes.byref(self._h), self.head_dim, self.group,
                                      s.ctypes.data_as(ctypes.c_void_p), l.ctypes.data_as(ctypes.c_void_p),

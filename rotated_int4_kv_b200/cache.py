@@ -13,6 +13,8 @@ import numpy as np
 import torch
 
 from .api import (Plan, attend_decode, attend_decode_append, decode, encode_batch, make_workspace)
+from .paged import (PAGE_SIZES, PagePlan, attend_paged, encode_paged, make_paged_workspace, page_plan, page_release,
+                    paged_workspace_size)
 
 
 class Int4KVCache:
@@ -125,3 +127,84 @@ class Int4KVCache:
         k = decode(self.k_plans[layer], self.k_codes[layer], self.k_scales[layer], t0, n, stream=stream)
         v = decode(self.v_plans[layer], self.v_codes[layer], self.v_scales[layer], t0, n, stream=stream)
         return k, v
+
+
+class PagedInt4KVCache:
+    """Per-layer paged caches of requests of different lengths.
+
+    ``num_pages`` pages of ``page_size`` tokens are shared by up to ``max_requests`` requests of at
+    most ``max_pages`` pages each; the block table, the lengths and the free list live on the GPU
+    and serve every layer. One serving step: :meth:`begin` (one launch: pages, slots and lengths of
+    the step), per layer :meth:`update` and :meth:`attend`, and :meth:`release` for requests that
+    have ended. No call waits for the GPU, and all may be captured into a CUDA graph.
+    """
+
+    def __init__(self, layers: int, max_requests: int, kv_heads: int, head_dim: int, num_pages: int, page_size: int,
+                 max_pages: int, k_params, v_params, device=None, group: int = 32, transform: str = "srft",
+                 bits: int = 4):
+        if min(layers, max_requests, kv_heads, head_dim, num_pages, max_pages) <= 0:
+            raise ValueError("layers, max_requests, kv_heads, num_pages and max_pages must be positive")
+        if page_size not in PAGE_SIZES:
+            raise ValueError(f"page size must be one of {PAGE_SIZES}, got {page_size}")
+        dev = torch.device(device) if device is not None else torch.device("cuda")
+        self.device = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+        self.layers, self.requests, self.kv_heads, self.head_dim = layers, max_requests, kv_heads, head_dim
+        self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
+
+        def per_layer(params):
+            if np.asarray(params[0]).ndim == 1:
+                return [params] * layers
+            if len(params) != layers:
+                raise ValueError(f"expected one (signs, lambda) pair or {layers} of them")
+            return list(params)
+
+        with torch.cuda.device(self.device):
+            self.k_plans = [Plan(s, lam, group, transform, bits) for s, lam in per_layer(k_params)]
+            self.v_plans = [Plan(s, lam, group, transform, bits) for s, lam in per_layer(v_params)]
+
+        def pages(width, dtype):
+            return [torch.zeros((num_pages, kv_heads, page_size, width), dtype=dtype, device=self.device)
+                    for _ in range(layers)]
+        self.k_codes, self.v_codes = (pages(head_dim * bits // 8, torch.uint8) for _ in range(2))
+        self.k_scales, self.v_scales = (pages(head_dim // group, torch.float16) for _ in range(2))
+        self.block_table = torch.full((max_requests, max_pages), -1, dtype=torch.int32, device=self.device)
+        self.kv_lens = torch.zeros(max_requests, dtype=torch.int32, device=self.device)
+        self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=self.device)
+        self.free_head = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._ws, self._grown = {}, []
+
+    def begin(self, q_lens: torch.Tensor, n_tokens: int, stream=None) -> PagePlan:
+        """Pages, slots and lengths of a step in which request b gets q_lens[b] (int32, device) new
+        tokens, ``n_tokens`` of them at most in all; see :func:`page_plan`. ``kv_lens`` moves on."""
+        step = PagePlan.empty(self.requests, n_tokens, self.device, stream)._replace(kv_lens=self.kv_lens)
+        return page_plan(self.kv_lens, q_lens, self.block_table, self.free_pages, self.free_head, self.page_size,
+                         out=step, stream=stream)
+
+    def update(self, layer: int, k: torch.Tensor, v: torch.Tensor, step: PagePlan, stream=None) -> None:
+        """The step's new rows k, v fp16 [n_tokens, kv_heads, head_dim] into their pages (one launch)."""
+        encode_paged([(self.k_plans[layer], k, self.k_codes[layer], self.k_scales[layer]),
+                      (self.v_plans[layer], v, self.v_codes[layer], self.v_scales[layer])], step.slots, stream=stream)
+
+    def attend(self, layer: int, q: torch.Tensor, step: PagePlan, max_q_len: int = None, max_kv_len: int = None,
+               window: int = 0, softmax_scale: float = 0.0, out=None, stream=None) -> torch.Tensor:
+        """Causal attention of the step's tokens q fp16 [n_tokens, q_heads, head_dim] over the cache
+        (after :meth:`update`); see :func:`attend_paged`. Rows of padding tokens stay as ``out`` had them.
+        Calls on different streams that may overlap need caches of their own (one workspace)."""
+        n, q_heads = q.shape[0], q.shape[1]
+        longest = max(1, n if max_q_len is None else max_q_len)
+        need = paged_workspace_size(self.requests, q_heads, self.kv_heads, self.head_dim, n, longest)
+        ws = self._ws.get(q_heads)
+        if ws is None or ws.numel() < need:
+            if ws is not None:
+                self._grown.append(ws)  # a captured graph may hold its address
+            ws = self._ws[q_heads] = make_paged_workspace(self.requests, q_heads, self.kv_heads, self.head_dim, n,
+                                                          longest, self.device, stream)
+        return attend_paged(self.k_plans[layer], self.v_plans[layer], q, self.k_codes[layer], self.k_scales[layer],
+                            self.v_codes[layer], self.v_scales[layer], self.block_table, self.kv_lens, step.q_starts,
+                            max_q_len=longest, max_kv_len=max_kv_len, window=window, softmax_scale=softmax_scale,
+                            out=out, workspace=ws, stream=stream)
+
+    def release(self, done: torch.Tensor, stream=None) -> None:
+        """Requests with ``done`` (bool, device) give their pages back and become empty."""
+        page_release(done, self.kv_lens, self.block_table, self.free_pages, self.free_head, self.page_size,
+                     stream=stream)

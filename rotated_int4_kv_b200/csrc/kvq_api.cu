@@ -1,5 +1,6 @@
 // kvq_api.cu -- the C ABI: plan management, host-side argument checks, error
 // reporting and the driver entry point for TMA tensor maps.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -137,6 +138,17 @@ kvq_status encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, cons
       return KVQ_OK;
     }
   }
+  const kvq_status st = encode_tiled_new(map, dt, rank, base, dims, strides_bytes, box, swz, what);
+  if (st != KVQ_OK) return st;
+  std::lock_guard<std::mutex> lk(g_map_mu);
+  if (g_maps.size() >= kMaxCachedMaps) g_maps.clear();
+  g_maps.emplace(key, *map);
+  return KVQ_OK;
+}
+
+kvq_status encode_tiled_new(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
+                            const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                            CUtensorMapSwizzle swz, const char* what) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return fail(KVQ_ERR_CUDA, "cuTensorMapEncodeTiled not available from the driver");
   cuuint64_t d[5];
@@ -152,9 +164,6 @@ kvq_status encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, cons
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(KVQ_ERR_CUDA, std::string("tensor map for ") + what + " rejected by the driver");
-  std::lock_guard<std::mutex> lk(g_map_mu);
-  if (g_maps.size() >= kMaxCachedMaps) g_maps.clear();
-  g_maps.emplace(key, *map);
   return KVQ_OK;
 }
 
@@ -307,11 +316,47 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
       const double q = hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
       wdec[(size_t)n * D + k] = kvq::half_bits((float)((double)signs[n] * q / (double)lambda[c]));
     }
+  // paged-attention operands: the query rotation Lambda^-1 Q diag(s) (row = channel) and the
+  // output un-rotation diag(s) Q^T Lambda^-1 (row = sample), fp16 times a power of two that
+  // puts the largest entry in [1, 2) (no fp16 range limit applies to lambda), row-major and as
+  // A fragments: lane (g, c) of K step ks holds (row g | g + 8, columns 16 ks + 2c, + 1 | + 8, + 9)
+  std::vector<uint16_t> wpg((size_t)4 * D * D);
+  {
+    std::vector<double> m((size_t)D * D);
+    double top = 0.0;
+    for (int c = 0; c < D; ++c)
+      for (int n = 0; n < D; ++n) {
+        const double q = hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
+        m[(size_t)c * D + n] = (double)signs[n] * q / (double)lambda[c];
+        top = std::max(top, std::fabs(m[(size_t)c * D + n]));
+      }
+    int e = 0;
+    std::frexp(top, &e);  // top = f 2^e with f in [0.5, 1)
+    for (double& v : m) v = std::ldexp(v, 1 - e);
+    p->wq_scale = p->wo_scale = (float)std::ldexp(1.0, e - 1);
+    for (int which = 0; which < 2; ++which) {
+      uint16_t* row = wpg.data() + (size_t)which * D * D;
+      uint16_t* frag = wpg.data() + (size_t)(2 + which) * D * D;
+      for (int i = 0; i < D; ++i)
+        for (int k = 0; k < D; ++k)
+          row[(size_t)i * D + k] = kvq::half_bits((float)(which ? m[(size_t)k * D + i] : m[(size_t)i * D + k]));
+      size_t o = 0;
+      for (int mt = 0; mt < D / 16; ++mt)
+        for (int ks = 0; ks < D / 16; ++ks)
+          for (int lane = 0; lane < 32; ++lane)
+            for (int r = 0; r < 4; ++r)
+              for (int x = 0; x < 2; ++x) {
+                const int i = 16 * mt + (lane >> 2) + 8 * (r & 1), k = 16 * ks + 2 * (lane & 3) + 8 * (r >> 1) + x;
+                frag[o++] = row[(size_t)i * D + k];
+              }
+    }
+  }
   constexpr size_t kWtOff = 4096;  // after the two CodecConsts copies, 16-byte aligned for TMA
   static_assert(2 * sizeof(kvq::CodecConsts) <= kWtOff, "plan block layout");
   const size_t rot_off = kWtOff + wt.size() * 2;
   const size_t wdec_off = rot_off + rot.size() * 2;
-  const size_t bytes = wdec_off + wdec.size() * 2;
+  const size_t wpg_off = wdec_off + wdec.size() * 2;
+  const size_t bytes = wpg_off + wpg.size() * 2;
   void* blk = nullptr;
   if (cudaMalloc(&blk, bytes) != cudaSuccess) {
     delete p;
@@ -324,7 +369,8 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
        cudaMemcpy((char*)blk + kWtOff, wt.data(), wt.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) ||
       (!rot.empty() &&
        cudaMemcpy((char*)blk + rot_off, rot.data(), rot.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) ||
-      cudaMemcpy((char*)blk + wdec_off, wdec.data(), wdec.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
+      cudaMemcpy((char*)blk + wdec_off, wdec.data(), wdec.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess ||
+      cudaMemcpy((char*)blk + wpg_off, wpg.data(), wpg.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
     cudaFree(blk);
     delete p;
     return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
@@ -335,6 +381,10 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   p->wt_dev = wt.empty() ? nullptr : reinterpret_cast<const uint16_t*>((char*)blk + kWtOff);
   p->rot_dev = reinterpret_cast<const uint16_t*>((char*)blk + rot_off);
   p->wdec_dev = reinterpret_cast<const uint16_t*>((char*)blk + wdec_off);
+  p->wq_dev = reinterpret_cast<const uint16_t*>((char*)blk + wpg_off);
+  p->wo_dev = p->wq_dev + (size_t)D * D;
+  p->wqf_dev = reinterpret_cast<const uint4*>(p->wo_dev + (size_t)D * D);
+  p->wof_dev = reinterpret_cast<const uint4*>(p->wo_dev + (size_t)2 * D * D);
   *out = p;
   return KVQ_OK;
 }
@@ -633,10 +683,189 @@ kvq_status kvq_debug_wait_timeout(uint32_t limit_us, void* stream) {
   return kvq::launch_wait_probe(limit_us, (cudaStream_t)stream);
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------- pages
+namespace {
+
+// page_size -> its logarithm, -1 when it is not one of 16, 32, 64, 128
+int page_shift_of(int page_size) {
+  for (int s = 4; s <= 7; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+kvq_status check_pages(const char* who, int num_pages, int page_size, int Hkv) {
+  const std::string w = std::string(who) + ": ";
+  if (page_shift_of(page_size) < 0) return fail(KVQ_ERR_UNSUPPORTED, w + "page_size must be 16, 32, 64 or 128");
+  if (num_pages < 1 || Hkv < 1) return fail(KVQ_ERR_INVALID_ARG, w + "num_pages and Hkv must be positive");
+  if ((long long)num_pages * page_size > 0x7fffffffll || (long long)num_pages * Hkv > 0x7fffffffll)
+    return fail(KVQ_ERR_UNSUPPORTED, w + "num_pages * page_size and num_pages * Hkv must be below 2^31");
+  return KVQ_OK;
+}
+
+// No C++ exception leaves a C entry point.
+template <typename F>
+kvq_status guarded(const char* who, F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    try {
+      return fail(KVQ_ERR_CUDA, std::string(who) + ": out of host memory");
+    } catch (...) {
+      return KVQ_ERR_CUDA;
+    }
+  }
+}
+
+bool same_form(const kvq_plan* a, const kvq_plan* b) {
+  return a->D == b->D && a->G == b->G && a->device == b->device && a->xform == b->xform && a->bits == b->bits;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_page_plan(const int32_t* kv_lens, const int32_t* q_lens, int B, int32_t* table, int max_pages,
+                         int64_t table_stride, const int32_t* free_pages, int n_free, const int32_t* free_head,
+                         int32_t* free_head_out, int page_size, int32_t* slots, int32_t* positions, int n_slots,
+                         int32_t* q_starts, int32_t* kv_lens_out, int32_t* info, void* stream) {
+  return guarded("page_plan", [&]() -> kvq_status {
+    if (B < 0 || max_pages < 0 || n_free < 0 || n_slots < 0 || table_stride < max_pages)
+      return fail(KVQ_ERR_INVALID_ARG, "page_plan: negative size, or table_stride < max_pages");
+    const int shift = page_shift_of(page_size);
+    if (shift < 0) return fail(KVQ_ERR_UNSUPPORTED, "page_plan: page_size must be 16, 32, 64 or 128");
+    if (B > kvq::kMaxPlanRequests) return fail(KVQ_ERR_UNSUPPORTED, "page_plan: more than 16384 requests");
+    if ((B > 0 && (!kv_lens || !q_lens || !kv_lens_out)) || (B > 0 && max_pages > 0 && !table) ||
+        (n_free > 0 && !free_pages) || !free_head || !free_head_out || (n_slots > 0 && (!slots || !positions)) ||
+        !q_starts || !info)
+      return fail(KVQ_ERR_INVALID_ARG, "page_plan: null buffer");
+    return kvq::launch_page_plan(kv_lens, q_lens, B, table, max_pages, table_stride, free_pages, n_free, free_head,
+                                 free_head_out, shift, slots, positions, n_slots, q_starts, kv_lens_out, info,
+                                 (cudaStream_t)stream);
+  });
+}
+
+kvq_status kvq_page_release(const uint8_t* done, int32_t* kv_lens, const int32_t* table, int64_t table_stride, int B,
+                            int max_pages, int page_size, int32_t* free_pages, int n_free, int32_t* free_head,
+                            void* stream) {
+  return guarded("page_release", [&]() -> kvq_status {
+    if (B < 0 || max_pages < 0 || n_free < 0 || table_stride < max_pages)
+      return fail(KVQ_ERR_INVALID_ARG, "page_release: negative size, or table_stride < max_pages");
+    const int shift = page_shift_of(page_size);
+    if (shift < 0) return fail(KVQ_ERR_UNSUPPORTED, "page_release: page_size must be 16, 32, 64 or 128");
+    if (B == 0) return KVQ_OK;
+    if (!done || !kv_lens || (max_pages > 0 && !table) || (n_free > 0 && !free_pages) || !free_head)
+      return fail(KVQ_ERR_INVALID_ARG, "page_release: null buffer");
+    return kvq::launch_page_release(done, kv_lens, table, table_stride, B, max_pages, shift, free_pages, n_free,
+                                    free_head, (cudaStream_t)stream);
+  });
+}
+
+kvq_status kvq_encode_paged(const kvq_paged_encode_job* jobs, int njobs, int n, int Hkv, int page_size, int num_pages,
+                            const int32_t* slots, void* stream) {
+  return guarded("encode_paged", [&]() -> kvq_status {
+    if (njobs < 0 || (njobs > 0 && !jobs) || n < 0) return fail(KVQ_ERR_INVALID_ARG, "encode_paged: bad job array or n < 0");
+    kvq_status st = check_pages("encode_paged", num_pages, page_size, Hkv);
+    if (st != KVQ_OK) return st;
+    if (Hkv > kvq::kMaxPageHeads) return fail(KVQ_ERR_UNSUPPORTED, "encode_paged: more than 128 KV heads");
+    if ((long long)n * Hkv > 0x7fffffffll - 128) return fail(KVQ_ERR_UNSUPPORTED, "encode_paged: n * Hkv too large");
+    for (int i = 0; i < njobs; ++i) {
+      const kvq_paged_encode_job& j = jobs[i];
+      const std::string w = "encode_paged job " + std::to_string(i) + ": ";
+      if (!j.plan) return fail(KVQ_ERR_INVALID_ARG, w + "null plan");
+      if (!same_form(j.plan, jobs[0].plan))
+        return fail(KVQ_ERR_INVALID_ARG, w + "all jobs must share head_dim, group, transform, code width and device");
+      if (n == 0) continue;
+      if (!j.x || !j.codes || !j.scales || !slots) return fail(KVQ_ERR_INVALID_ARG, w + "null buffer");
+      if (!kvq::aligned16(j.x) || !kvq::aligned16(j.codes) || !kvq::aligned16(j.scales))
+        return fail(KVQ_ERR_ALIGNMENT, w + "buffers must be 16-byte aligned");
+      const int64_t D = j.plan->D;
+      for (const auto& [len, stride] : {std::pair<int, int64_t>{n, j.token_stride}, {Hkv, j.head_stride}}) {
+        if (len == 1) continue;
+        if (stride < D || stride >= (int64_t)1 << 38) return fail(KVQ_ERR_INVALID_ARG, w + "stride below head_dim or too large");
+        if (stride & 7) return fail(KVQ_ERR_ALIGNMENT, w + "strides must be multiples of 8 elements");
+      }
+    }
+    if (njobs == 0 || n == 0) return KVQ_OK;
+    st = kvq::check_plan_device(jobs[0].plan);
+    if (st != KVQ_OK) return st;
+    return kvq::launch_encode_paged(jobs, njobs, n, Hkv, page_shift_of(page_size), num_pages, slots,
+                                    (cudaStream_t)stream);
+  });
+}
+
+kvq_status kvq_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint16_t* scales, int num_pages,
+                            int page_size, int Hkv, const int32_t* slots, int n, uint16_t* out, void* stream) {
+  return guarded("decode_paged", [&]() -> kvq_status {
+    if (!p) return fail(KVQ_ERR_INVALID_ARG, "decode_paged: null plan");
+    if (n < 0) return fail(KVQ_ERR_INVALID_ARG, "decode_paged: n < 0");
+    kvq_status st = check_pages("decode_paged", num_pages, page_size, Hkv);
+    if (st != KVQ_OK) return st;
+    if ((long long)n * Hkv > 0x7fffffffll - 128) return fail(KVQ_ERR_UNSUPPORTED, "decode_paged: n * Hkv too large");
+    if (n == 0) return KVQ_OK;
+    if (!codes || !scales || !slots || !out) return fail(KVQ_ERR_INVALID_ARG, "decode_paged: null buffer");
+    if (!kvq::aligned16(codes) || !kvq::aligned16(scales) || !kvq::aligned16(out))
+      return fail(KVQ_ERR_ALIGNMENT, "decode_paged: buffers must be 16-byte aligned");
+    st = kvq::check_plan_device(p);
+    if (st != KVQ_OK) return st;
+    return kvq::launch_decode_paged(p, codes, scales, num_pages, page_shift_of(page_size), Hkv, slots, n, out,
+                                    (cudaStream_t)stream);
+  });
+}
+
+size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 128 && D != 256) || n_q < 0 || max_q_len < 1) return 0;
+  return kvq::paged_workspace_bytes(B, Hq, Hkv, n_q, max_q_len);
+}
+
+kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const uint8_t* kc, const uint16_t* ks, const uint8_t* vc,
+                            const uint16_t* vs, int num_pages, int page_size, const int32_t* table, int max_pages,
+                            int64_t table_stride, const int32_t* kv_lens, const int32_t* q_starts, int B, int n_q,
+                            int Hq, int Hkv, int max_q_len, int max_kv_len, int window, float sigma, uint16_t* out,
+                            void* ws, size_t ws_bytes, void* stream) {
+  return guarded("attend_paged", [&]() -> kvq_status {
+    if (!pk || !pv) return fail(KVQ_ERR_INVALID_ARG, "attend_paged: null plan");
+    if (!same_form(pk, pv))
+      return fail(KVQ_ERR_INVALID_ARG, "attend_paged: K and V plans differ in head_dim, group, transform, code width or device");
+    if (B < 0 || n_q < 0 || Hq < 1 || max_pages < 0 || max_kv_len < 0 || window < 0 || table_stride < max_pages)
+      return fail(KVQ_ERR_INVALID_ARG, "attend_paged: negative size, or table_stride < max_pages");
+    kvq_status st = check_pages("attend_paged", num_pages, page_size, Hkv);
+    if (st != KVQ_OK) return st;
+    if (Hq % Hkv != 0) return fail(KVQ_ERR_UNSUPPORTED, "attend_paged: Hq must be a multiple of Hkv");
+    if (max_q_len < 1) return fail(KVQ_ERR_INVALID_ARG, "attend_paged: max_q_len must be at least 1");
+    if (!q_starts && (n_q != B || max_q_len != 1))
+      return fail(KVQ_ERR_INVALID_ARG, "attend_paged: without q_starts every request has one query token");
+    if ((long long)n_q * Hq > 0x7fffffffll - 256 || (long long)max_pages * page_size > 0x7fffffffll - 256 ||
+        max_kv_len > 0x7fffffff - 256)
+      return fail(KVQ_ERR_UNSUPPORTED, "attend_paged: more than 2^31 query rows or tokens");
+    if (B == 0 || n_q == 0) return KVQ_OK;
+    if (!q || !out || !kc || !ks || !vc || !vs || !kv_lens || (max_pages > 0 && !table))
+      return fail(KVQ_ERR_INVALID_ARG, "attend_paged: null buffer");
+    for (const void* ptr : {(const void*)q, (const void*)out, (const void*)kc, (const void*)ks, (const void*)vc,
+                            (const void*)vs})
+      if (!kvq::aligned16(ptr)) return fail(KVQ_ERR_ALIGNMENT, "attend_paged: buffers must be 16-byte aligned");
+    if ((n_q > 1 && (q_token_stride & 7)) || (Hq > 1 && (q_head_stride & 7)))
+      return fail(KVQ_ERR_ALIGNMENT, "attend_paged: query strides must be multiples of 8 elements");
+    if ((n_q > 1 && q_token_stride < 0) || (Hq > 1 && q_head_stride < 0))
+      return fail(KVQ_ERR_INVALID_ARG, "attend_paged: negative query stride");
+    const size_t need = kvq::paged_workspace_bytes(B, Hq, Hkv, n_q, max_q_len);
+    if (!ws || ws_bytes < need) return fail(KVQ_ERR_WORKSPACE, "attend_paged: workspace missing or too small");
+    if (!kvq::aligned16(ws)) return fail(KVQ_ERR_ALIGNMENT, "attend_paged: workspace must be 16-byte aligned");
+    st = kvq::check_plan_device(pk);
+    if (st != KVQ_OK) return st;
+    const kvq::PagedAttendHost a{pk, pv, q, q_token_stride, q_head_stride, kc, ks, vc, vs, num_pages,
+                                 page_shift_of(page_size), table, max_pages, table_stride, kv_lens, q_starts, B, n_q,
+                                 Hq, Hkv, max_q_len, max_kv_len, window, sigma, out, ws, ws_bytes};
+    return kvq::launch_attend_paged(a, (cudaStream_t)stream);
+  });
+}
+
 kvq_status kvq_poll_device_errors(uint32_t* flags) {
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(KVQ_ERR_CUDA, "poll: device synchronize failed");
   const uint32_t f = kvq::codec_error_flags(true) | kvq::attend_error_flags(true) | kvq::encode_tc_error_flags(true) |
-                     kvq::decode_tc_error_flags(true);
+                     kvq::decode_tc_error_flags(true) | kvq::paged_error_flags(true);
   if (flags) *flags = f;
   return KVQ_OK;
 }

@@ -1,0 +1,1003 @@
+// kvq_attend_paged.cu -- attention of few query tokens per request over a paged int4/int8
+// cache for sm_100a, in the rotated domain (the paper describes no read path; it follows
+// from the transform being orthonormal, as in the dense decode attention):
+//   q~ = Lambda_K^-1 Q diag(s_K) q,   score_t = sigma q~ . (c_K scale_K)_t,
+//   o = sum_t softmax(score)_t (c_V scale_V)_t,   out = diag(s_V) Q^T Lambda_V^-1 o.
+//
+// Work. A unit is (request, KV head, tile of 8 query rows), a query row one (query token,
+// head of the KV head's group); its tokens are taken in tiles of 128. The tiles of all units
+// form one line, requests after requests, and every CTA of a persistent grid takes an equal
+// piece of it, however ragged the lengths are: a piece is the end of one unit, some whole
+// units, the beginning of another. The lengths live on the GPU, so every CTA adds them up
+// for itself (one block scan). Units cut by a piece's border are joined through the
+// workspace: each CTA writes its softmax partial (m, l, o), the last one to arrive at the
+// unit's counter (found by an atomic, nobody waits) merges them in CTA order, so the result
+// does not depend on who was last.
+//
+// A CTA is one producer warp and eight consumer warps. The producer streams a tile's pages
+// into a ring of stages: per page one TMA box of K codes and one of V codes (swizzled for
+// ldmatrix), and the scale rows as plain bulk copies. Consumer warp w takes tokens 16 w ..
+// 16 w + 15 of a stage, all channels, and keeps its own softmax state and output; the warps
+// are joined when a unit ends, while the producer already loads the next unit's tiles.
+//
+// Products are mma.m16n8k16 with tokens (scores) or channels (output) as rows and the 8
+// query rows as columns: the loop is bound by issue slots and HBM, not by the tensor cores.
+//   * A code enters as the fp16 subnormal c 2^-24 (int4: nibble + 8 in the low bits of an
+//     fp16 word, or 16 times that in the next four, minus the offset; both exact), one
+//     logical and one fp16 operation per pair; the powers of two are taken out of the
+//     query's fragments and of the sums.
+//   * q~ is one fp16 rounding per element after a power-of-two normalisation per row
+//     (2^-12 relative on average, so a score's error is about 2^-12 of |q||k|/sqrt(D), below
+//     what the fp16 rounding of the caller's q has put there).
+//   * P is fp16 (2^-11 relative per weight, its sum l is in fp32 of the unrounded values)
+//     times the V scale over a power of two that bounds the scales seen so far, so that
+//     neither large nor small V leave the fp16 range.
+// The query's rotation and the output's un-rotation are products with a per-plan matrix
+// that was laid out as fragments when the plan was made; they are read through L2 by the
+// warp that multiplies with them, 32 KB (D = 128) per unit, and take no shared memory.
+#include <algorithm>
+
+#include "kvq_internal.h"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+
+__device__ uint32_t g_paged_err = 0;
+
+namespace {
+
+constexpr int kRows = 8;        // query rows per unit (mma N)
+constexpr int kWarps = 8;       // consumer warps
+constexpr int kTile = 128;      // tokens per tile: 16 per consumer warp
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kMaxCtas = 2 * 160;  // partial slots in the workspace: two per CTA
+
+template <int D, int G, int BITS>
+struct PCfg {
+  static constexpr int NC = D / 32;               // 32-channel chunks of a row
+  static constexpr int NG = D / G;                // scale groups of a row
+  static constexpr int RB = D * BITS / 8;         // code bytes of a row
+  static constexpr int MT = D / 16;               // 16-channel tiles (output) and K steps (scores)
+  static constexpr int kMinBlocks = D == 128 ? 2 : 1;
+  static constexpr int kKBytes = kTile * RB;
+  static constexpr int kSBytes = kTile * NG * 2;
+  static constexpr int kStage = 2 * (kKBytes + kSBytes);
+  static constexpr int kStages = BITS == 4 ? 4 : 2;
+  static constexpr int kObuf = 4 * kRows * D * 4;          // four warps' outputs
+  static constexpr int kOmStride = D + 4;                  // q~ and the unit's output, fp32, padded rows
+  static constexpr int kOm = kRows * kOmStride * 4;
+  static constexpr int kMl = kWarps * 2 * kRows * 4;
+  static constexpr int kBars = 256;
+  static constexpr int kSmem = kStages * kStage + kObuf + kOm + kMl + kBars + 1024;
+  static_assert(kSmem <= (kMinBlocks == 2 ? 113 : 227) * 1024, "shared memory");
+  static constexpr int PART = 2 * kRows + kRows * D;       // a partial: m, l, o
+};
+
+struct PagedParams {
+  CUtensorMap kmap, vmap;  // code pages [num_pages * Hkv][P][RB], box one page of <= 128 bytes a row
+  const uint16_t* q;
+  const uint16_t* ks;
+  const uint16_t* vs;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  const uint4* wq;
+  const uint4* wo;
+  uint16_t* out;
+  float* part;
+  int* cnt;
+  long long q_ts, q_hs, table_stride;
+  float qfac, ofac;        // sigma log2(e) times the query matrix' scale; the output matrix' scale
+  int B, n_q, Hq, Hkv, Gq, rt_max, max_q, max_kv, num_pages, page_shift, window, min_tiles;
+};
+
+// ---------------------------------------------------------------- small helpers
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
+
+// (a & mask) ^ c where c lies within mask
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(mask), "r"(c));
+  return d;
+}
+
+// Eight int4 codes of a word as fp16 pairs: h0 = (n0, n4) 2^-24, h1 = (n1, n5) 2^-20,
+// h2 = (n2, n6) 2^-24, h3 = (n3, n7) 2^-20.
+__device__ __forceinline__ void nib8(uint32_t w, uint32_t (&h)[4]) {
+  const __half2 o1 = u2h(0x00080008u), o16 = u2h(0x00800080u);  // 8 2^-24, 128 2^-24
+  const uint32_t w8 = w >> 8;
+  h[0] = h2u(__hsub2(u2h(and_xor(w, 0x000F000Fu, 0x00080008u)), o1));
+  h[1] = h2u(__hsub2(u2h(and_xor(w, 0x00F000F0u, 0x00800080u)), o16));
+  h[2] = h2u(__hsub2(u2h(and_xor(w8, 0x000F000Fu, 0x00080008u)), o1));
+  h[3] = h2u(__hsub2(u2h(and_xor(w8, 0x00F000F0u, 0x00800080u)), o16));
+}
+// Four int8 codes of a word: h0 = (b0, b2) 2^-24, h1 = (b1, b3) 2^-24.
+__device__ __forceinline__ void byte4(uint32_t w, uint32_t (&h)[2]) {
+  const __half2 o = u2h(0x00800080u);
+  h[0] = h2u(__hsub2(u2h(and_xor(w, 0x00FF00FFu, 0x00800080u)), o));
+  h[1] = h2u(__hsub2(u2h(and_xor(w >> 8, 0x00FF00FFu, 0x00800080u)), o));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+
+// The power of two 2^-e that brings a row's largest magnitude into [2^9, 2^10); mx is the
+// largest of this lane's elements of row g, the row's lanes are c = 0 .. 3. Returns e.
+__device__ __forceinline__ int row_exponent(float mx) {
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 9;
+  return mx > 0.0f ? min(max(e, -100), 100) : 0;
+}
+
+// Byte offset of 16-byte column cc of token row `row` of a stage's codes: rows of up to 128
+// bytes with the TMA swizzle of that width, longer rows as boxes of 128 bytes.
+template <int RB>
+__device__ __forceinline__ int code_off(int row, int cc) {
+  if constexpr (RB == 64) return row * 64 + ((cc ^ ((row >> 1) & 3)) << 4);
+  return (cc >> 3) * (kTile * 128) + row * 128 + (((cc & 7) ^ (row & 7)) << 4);
+}
+
+// ---------------------------------------------------------------- the requests
+struct Request {
+  int qs, qn, kv;      // first query token, query tokens, cached tokens
+  int t_lo;            // first token that any of its queries attends
+  int tile0, nt, rt;   // first tile, tiles, row tiles
+};
+
+__device__ __forceinline__ Request request_of(const PagedParams& p, int b) {
+  Request r;
+  r.qs = b;
+  r.qn = 1;
+  if (p.q_starts) {
+    r.qs = min(max(__ldg(p.q_starts + b), 0), p.n_q);
+    r.qn = min(max(__ldg(p.q_starts + b + 1), r.qs), p.n_q) - r.qs;
+  }
+  r.kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+  const long long lo = p.window ? (long long)r.kv - r.qn + 1 - p.window : 0;
+  r.t_lo = (int)min(max(lo, 0ll), (long long)r.kv);
+  r.tile0 = r.t_lo / kTile;
+  r.nt = max(1, (r.kv + kTile - 1) / kTile - r.tile0);
+  r.rt = (min(r.qn, p.max_q) * p.Gq + kRows - 1) / kRows;
+  return r;
+}
+
+__device__ __forceinline__ long long tiles_of(const PagedParams& p, const Request& r) {
+  return (long long)p.Hkv * r.rt * r.nt;
+}
+
+// Inclusive prefix sum over the block's kThreads threads; total in *sum.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w <= kWarps; ++w) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  *sum = all;
+  return v + before;
+}
+
+// A CTA's piece [at, end) of the line of tiles, walked segment by segment (a segment: the
+// tiles of one unit). `base` is the place of request b's first tile.
+struct Walk {
+  long long at, end, base;
+  int b;
+  Request r;
+  // the segment: unit u of request b, its tiles [i0, i1)
+  int u, i0, i1;
+
+  __device__ __forceinline__ bool next(const PagedParams& p) {
+    if (at >= end) return false;
+    while (at >= base + tiles_of(p, r)) {
+      base += tiles_of(p, r);
+      r = request_of(p, ++b);
+    }
+    const long long off = at - base;
+    u = (int)(off / r.nt);
+    i0 = (int)(off - (long long)u * r.nt);
+    i1 = (int)min((long long)r.nt, i0 + (end - at));
+    at += i1 - i0;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- the kernel
+template <int D, int G, int BITS>
+__global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
+    attend_paged_kernel(const __grid_constant__ PagedParams p) {
+  using C = PCfg<D, G, BITS>;
+  constexpr int NC = C::NC, NG = C::NG, MT = C::MT, RB = C::RB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = smem;
+  float4* obuf = reinterpret_cast<float4*>(smem + C::kStages * C::kStage);
+  float* om = reinterpret_cast<float*>(smem + C::kStages * C::kStage + C::kObuf);  // [8][kOmStride]
+  float* wml = om + C::kOm / 4;                                                    // [warp][m, l][8]
+  uint64_t* full = reinterpret_cast<uint64_t*>(wml + C::kMl / 4);
+  uint64_t* empty = full + C::kStages;
+  long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [9]
+  long long* found = scan + kWarps + 1;                                // base of the first request, its index
+  int* flag = reinterpret_cast<int*>(found + 2);
+  static_assert((2 * C::kStages + kWarps + 1 + 2 + 1) * 8 <= C::kBars, "barrier region");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    fence_mbarrier_init();
+  }
+  grid_dep_launch();
+  grid_dep_wait();  // lengths, table, pages, queries and the workspace may come from the kernel before
+
+  // ---- this CTA's piece of the line of tiles
+  long long total = 0, mine = 0, upto = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    mine = b0 + tid < p.B ? tiles_of(p, request_of(p, b0 + tid)) : 0;
+    long long sum;
+    upto = total + block_scan(mine, scan, &sum);
+    total += sum;
+  }
+  const long long per = max((long long)p.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+  Walk w;
+  w.at = min(total, per * blockIdx.x);
+  w.end = min(total, w.at + per);
+  if (w.at >= w.end) return;
+  if (p.B <= kThreads) {
+    if (mine && w.at >= upto - mine && w.at < upto) {
+      found[0] = upto - mine;
+      found[1] = tid;
+    }
+  } else {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.B && before <= w.at; b0 += kThreads) {
+      mine = b0 + tid < p.B ? tiles_of(p, request_of(p, b0 + tid)) : 0;
+      long long sum;
+      upto = before + block_scan(mine, scan, &sum);
+      if (mine && w.at >= upto - mine && w.at < upto) {
+        found[0] = upto - mine;
+        found[1] = b0 + tid;
+      }
+      before += sum;
+    }
+  }
+  __syncthreads();  // also publishes the barriers' initialisation
+  w.base = found[0];
+  w.b = (int)found[1];
+  w.r = request_of(p, w.b);
+  const int P = 1 << p.page_shift;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    const int ppt = kTile >> p.page_shift;  // pages per tile, at most 8: one lane each
+    const uint32_t box = (uint32_t)(P * (RB < 128 ? RB : 128));
+    const uint32_t sbytes = (uint32_t)(P * NG * 2);
+    const uint32_t page_bytes = 2 * ((uint32_t)(P * RB) + sbytes);
+    const uint64_t pol = l2_evict_first_policy();
+    int n = 0;
+    while (w.next(p)) {
+      const int h = w.u / w.r.rt;
+      const int32_t* row = p.table + (long long)w.b * p.table_stride;
+      auto entry = [&](int i) {  // the table entry of this lane's page in tile i; -1: nothing to load
+        const int pi = (w.r.tile0 + i) * ppt + lane;
+        const bool want = lane < ppt && i < w.i1 && (long long)pi * P < w.r.kv && ((long long)pi + 1) * P > w.r.t_lo;
+        int e = -1;
+        if (want) {
+          e = __ldg(row + pi);
+          if (e < 0 || e >= p.num_pages) {
+            atomicOr(&g_paged_err, kErrBadPage);
+            e = 0;
+          }
+        }
+        return e;
+      };
+      int page = entry(w.i0);
+      for (int i = w.i0; i < w.i1; ++i, ++n) {
+        const int s = n % C::kStages;
+        const int coming = entry(i + 1);
+        bool ok = true;
+        if (n >= C::kStages) ok = mbar_wait_bounded(&empty[s], ((n / C::kStages) - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) atomicOr(&g_paged_err, kErrTimeoutLoad);
+          return;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(here) * page_bytes);
+        __syncwarp();
+        if (page >= 0) {
+          uint8_t* st = ring + s * C::kStage;
+          const int ph = page * p.Hkv + h;
+#pragma unroll
+          for (int j = 0; j < (RB + 127) / 128; ++j) {
+            uint8_t* kd = st + j * (kTile * 128) + lane * box;
+            if (p.rt_max == 1) {  // the pages are read once: out of L2's way
+              tma_load_3d_hint(kd, &p.kmap, &full[s], 128 * j, 0, ph, pol);
+              tma_load_3d_hint(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, 0, ph, pol);
+            } else {
+              tma_load_3d(kd, &p.kmap, &full[s], 128 * j, 0, ph);
+              tma_load_3d(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, 0, ph);
+            }
+          }
+          uint8_t* sd = st + 2 * C::kKBytes + lane * sbytes;
+          bulk_load(sd, p.ks + (size_t)ph * (P * NG), sbytes, &full[s]);
+          bulk_load(sd + C::kSBytes, p.vs + (size_t)ph * (P * NG), sbytes, &full[s]);
+        }
+        page = coming;
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3, mi = lane >> 3;
+  int n = 0;        // tiles taken so far
+  bool ok = true;   // false after a wait ran out: the rest is passed over, every barrier still met
+  while (w.next(p)) {
+    const Request& r = w.r;
+    const int h = w.u / r.rt, rt = w.u - h * r.rt;
+    const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
+    // row x of the tile: query token (rt * 8 + x) / Gq, head of the group the remainder
+    auto q_row = [&](int x, int& tok, int& head) {
+      const int y = rt * kRows + x;
+      tok = y / p.Gq;
+      head = h * p.Gq + (y - tok * p.Gq);
+    };
+
+    // ---- (1) rotate the rows: X[channel][row] = Wq q, channel tiles over the warps
+    {
+      int tok, head;
+      q_row(g < nrows ? g : 0, tok, head);
+      const uint16_t* src = p.q + (long long)(r.qs + tok) * p.q_ts + (long long)head * p.q_hs;
+      uint32_t bq[MT][2];
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) : 0u;
+      }
+#pragma unroll
+      for (int t = 0; t < MT / kWarps; ++t) {
+        const int mt = warp + kWarps * t;
+        float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks) {
+          const uint4 a = __ldg(p.wq + (mt * MT + ks) * 32 + lane);
+          mma_16816((ks & 1) ? a1 : a0, a.x, a.y, a.z, a.w, bq[ks][0], bq[ks][1]);
+        }
+        float* o0 = om + (2 * c) * C::kOmStride + 16 * mt + g;
+        o0[0] = a0[0] + a1[0];
+        o0[C::kOmStride] = a0[1] + a1[1];
+        o0[8] = a0[2] + a1[2];
+        o0[C::kOmStride + 8] = a0[3] + a1[3];
+      }
+    }
+    consumers_sync();
+    // ---- (2) this lane's B fragments of the scores (column g), normalised by 2^-e per row
+    uint32_t qf[MT][2];
+    float rowfac[2];  // of the scores' columns 2c, 2c + 1: back to base-2 scores
+    {
+      const float* qr = om + g * C::kOmStride;
+      // K step ks of the codes: int4 chunk ks / 2, channels 8c + (0, 4 | 1, 5) or (2, 6 | 3, 7);
+      // int8 channels 16 ks + 4c + (0, 2 | 1, 3)
+      auto chan = [&](int ks, int e) {
+        if constexpr (BITS == 4) return 32 * (ks >> 1) + 8 * c + ((ks & 1) ? 2 : 0) + (e >> 1) + ((e & 1) ? 4 : 0);
+        return 16 * ks + 4 * c + (e >> 1) + ((e & 1) ? 2 : 0);
+      };
+      float mx = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(qr[chan(ks, e)]));
+      const int ex = row_exponent(mx);
+      const float f = pow2f(-ex), fhi = BITS == 4 ? f * 0.0625f : f;  // the odd pairs' codes stand 16 times too high
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+        qf[ks][0] = pack_half2(qr[chan(ks, 0)] * f, qr[chan(ks, 1)] * f);
+        qf[ks][1] = pack_half2(qr[chan(ks, 2)] * fhi, qr[chan(ks, 3)] * fhi);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        rowfac[e] = p.qfac * 16777216.0f * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+    }
+    // what rows 2c, 2c + 1 attend: tokens in (lo, hi]
+    int hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      int tok, head;
+      q_row(min(2 * c + e, nrows - 1), tok, head);
+      hi[e] = r.kv - r.qn + tok;
+      lo[e] = p.window ? (int)max((long long)hi[e] - p.window, -1ll) : -1;
+    }
+    int first_hi, last_lo;  // of the tile's first and last row: tokens in between are attended by all rows
+    {
+      int tok, head;
+      q_row(0, tok, head);
+      first_hi = r.kv - r.qn + tok;
+      q_row(nrows - 1, tok, head);
+      last_lo = p.window ? (int)max((long long)r.kv - r.qn + tok - p.window, -1ll) : -1;
+    }
+
+    // ---- (3) the tiles
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+    float o[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    int ve = -14;                 // V scales seen so far are below 2^ve
+    uint32_t vlim = 0x0400u;      // the fp16 bits of 2^ve
+    uint32_t vinv = 0x74007400u;  // 2^-ve as an fp16 pair
+    for (int i = w.i0; i < w.i1; ++i, ++n) {
+      const int s = n % C::kStages;
+      if (!ok) continue;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (n / C::kStages) & 1))) {
+        if (lane == 0) atomicOr(&g_paged_err, kErrTimeoutLoad);
+        ok = false;
+        continue;
+      }
+      const uint8_t* st = ring + s * C::kStage;
+      const int r0 = 16 * warp;                                // the warp's rows of the stage
+      const int t0 = (r.tile0 + i) * kTile + r0;               // and their first token
+      if (t0 >= r.kv || t0 + 16 <= r.t_lo) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        continue;
+      }
+      const bool edge = t0 + 16 > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
+      const bool cut = t0 + 15 > first_hi || t0 <= last_lo;     // some (token, row) pairs are masked
+      // ---- scores: C layout (tokens g, g + 8; columns 2c, 2c + 1)
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        const uint8_t* kt = st;
+        float ska[NG], skb[NG];
+        {
+          const uint32_t* sa = reinterpret_cast<const uint32_t*>(st + 2 * C::kKBytes + (r0 + g) * (NG * 2));
+          const uint32_t* sb = sa + 8 * (NG / 2);
+#pragma unroll
+          for (int j = 0; j < NG / 2; ++j) {
+            const float2 fa = __half22float2(u2h(sa[j])), fb = __half22float2(u2h(sb[j]));
+            ska[2 * j] = fa.x;
+            ska[2 * j + 1] = fa.y;
+            skb[2 * j] = fb.x;
+            skb[2 * j + 1] = fb.y;
+          }
+        }
+        auto add = [&](int grp, const float (&a)[4]) {
+          sc[0] = fmaf(ska[grp], a[0], sc[0]);
+          sc[1] = fmaf(ska[grp], a[1], sc[1]);
+          sc[2] = fmaf(skb[grp], a[2], sc[2]);
+          sc[3] = fmaf(skb[grp], a[3], sc[3]);
+        };
+        const int row = r0 + ((mi & 1) << 3) + (lane & 7);
+        if constexpr (BITS == 4) {
+#pragma unroll
+          for (int gp = 0; gp < NC / 2; ++gp) {  // two 32-channel chunks per ldmatrix
+            uint32_t x[4];                        // (tok g | g + 8) of chunk 2 gp, the same of 2 gp + 1
+            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(kt + code_off<RB>(row, 2 * gp + (mi >> 1))));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int ch = 2 * gp + j;
+              uint32_t a[4], b[4];
+              nib8(x[2 * j], a);
+              nib8(x[2 * j + 1], b);
+              if constexpr (G == 32) {
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0], qf[2 * ch][1]);
+                mma_16816(acc, a[2], b[2], a[3], b[3], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
+                add(ch, acc);
+              } else {
+                // lane c's channels (8c .. 8c + 7 of the chunk) lie in its half c / 2
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t m = (c >> 1) == k ? 0xffffffffu : 0u;
+                  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0] & m, qf[2 * ch][1] & m);
+                  mma_16816(acc, a[2], b[2], a[3], b[3], qf[2 * ch + 1][0] & m, qf[2 * ch + 1][1] & m);
+                  add(2 * ch + k, acc);
+                }
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch) {  // one 32-channel chunk per ldmatrix
+            uint32_t x[4];                   // (tok g | g + 8) of channels 0 - 15, the same of 16 - 31
+            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(kt + code_off<RB>(row, 2 * ch + (mi >> 1))));
+            uint32_t a[2], b[2], a2[2], b2[2];
+            byte4(x[0], a);
+            byte4(x[1], b);
+            byte4(x[2], a2);
+            byte4(x[3], b2);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0], qf[2 * ch][1]);
+            if constexpr (G == 32) {
+              mma_16816(acc, a2[0], b2[0], a2[1], b2[1], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
+              add(ch, acc);
+            } else {
+              float acc2[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16816(acc2, a2[0], b2[0], a2[1], b2[1], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
+              add(2 * ch, acc);
+              add(2 * ch + 1, acc2);
+            }
+          }
+        }
+      }
+      sc[0] *= rowfac[0];
+      sc[1] *= rowfac[1];
+      sc[2] *= rowfac[0];
+      sc[3] *= rowfac[1];
+      if (cut) {
+        const int ta = t0 + g, tb = ta + 8;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (ta > hi[e] || ta <= lo[e]) sc[e] = -INFINITY;
+          if (tb > hi[e] || tb <= lo[e]) sc[2 + e] = -INFINITY;
+        }
+      }
+      // ---- online softmax in base 2: m_run is a ceiling of the scores so far; it moves, by
+      // some headroom more than needed, only when a score of this stage passes it
+      const float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
+      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1])) {
+        constexpr float kHeadroom = 3.0f;
+        float a = mx0, b = mx1;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+          b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+        }
+        const float m0 = a > m_run[0] ? a + kHeadroom : m_run[0];
+        const float m1 = b > m_run[1] ? b + kHeadroom : m_run[1];
+        const float f0 = m0 == m_run[0] ? 1.0f : ex2_approx(m_run[0] - m0);
+        const float f1 = m1 == m_run[1] ? 1.0f : ex2_approx(m_run[1] - m1);
+        l_run[0] *= f0;
+        l_run[1] *= f1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[mt][0] *= f0;
+          o[mt][1] *= f1;
+          o[mt][2] *= f0;
+          o[mt][3] *= f1;
+        }
+        m_run[0] = m0;
+        m_run[1] = m1;
+      }
+      const float ms0 = m_run[0] == -INFINITY ? 0.0f : m_run[0];
+      const float ms1 = m_run[1] == -INFINITY ? 0.0f : m_run[1];
+      const float p0 = ex2_approx(sc[0] - ms0), p1 = ex2_approx(sc[1] - ms1);
+      const float p2 = ex2_approx(sc[2] - ms0), p3 = ex2_approx(sc[3] - ms1);
+      l_run[0] += p0 + p2;
+      l_run[1] += p1 + p3;
+      // P as the B operand of the output product: (tokens 2c, 2c + 1 | + 8; column g)
+      const uint32_t pb0 = movmatrix_trans(pack_half2(p0, p1)), pb1 = movmatrix_trans(pack_half2(p2, p3));
+      // ---- V scales: tokens 2c, 2c + 1, 2c + 8, 2c + 9
+      const uint8_t* vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
+      {
+        // the largest of the warp's scales: lane l holds half of token l / 2's row
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vsc) + lane * (NG / 4);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < NG / 4; ++j) {
+          const uint32_t u = vw[j] & 0x7FFF7FFFu;
+          top = max(top, max(u & 0xFFFFu, u >> 16));
+        }
+        const int t = t0 + (lane >> 1);
+        if (edge && (t >= r.kv || t < r.t_lo)) top = 0;
+        if (__any_sync(0xffffffffu, top >= vlim)) {
+          const int x = min((int)(__reduce_max_sync(0xffffffffu, top) >> 10), 30);
+          const int nve = x - 14;
+          if (nve > ve) {
+            const float f = pow2f(ve - nve);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][0] *= f;
+              o[mt][1] *= f;
+              o[mt][2] *= f;
+              o[mt][3] *= f;
+            }
+            ve = nve;
+            vlim = (uint32_t)(x + 1) << 10;
+            vinv = (uint32_t)__half_as_ushort(__float2half_rn(pow2f(-nve))) * 0x10001u;
+          }
+        }
+      }
+      uint32_t sw[4][NG / 2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = 2 * c + (e & 1) + ((e & 2) << 2);
+        const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + x * (NG * 2));
+        const bool live = !edge || (t0 + x < r.kv && t0 + x >= r.t_lo);
+#pragma unroll
+        for (int j = 0; j < NG / 2; ++j) sw[e][j] = live ? sp[j] : 0u;
+      }
+      // P times the scale of group grp, as the two B registers
+      auto weighted = [&](int grp, uint32_t& b0, uint32_t& b1) {
+        const uint32_t sel = (grp & 1) ? 0x7632u : 0x5410u;
+        const uint32_t s0 = prmt(sw[0][grp >> 1], sw[1][grp >> 1], sel), s1 = prmt(sw[2][grp >> 1], sw[3][grp >> 1], sel);
+        b0 = h2u(__hmul2(__hmul2(u2h(s0), u2h(vinv)), u2h(pb0)));
+        b1 = h2u(__hmul2(__hmul2(u2h(s1), u2h(vinv)), u2h(pb1)));
+      };
+      // ---- output: O[channel][column] += V[channel][token] P[token][column]
+      {
+        const uint8_t* vt = st + C::kKBytes;
+        const int row = r0 + ((mi & 1) << 3) + (lane & 7);
+        if constexpr (BITS == 4) {
+#pragma unroll
+          for (int gp = 0; gp < NC / 2; ++gp) {
+            uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of chunk 2 gp, the same of 2 gp + 1
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB>(row, 2 * gp + (mi >> 1))));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int ch = 2 * gp + j;
+              uint32_t a[4], b[4];  // channels 4g, 4g + 1 (16 times), 4g + 2, 4g + 3 (16 times) of the chunk
+              nib8(x[2 * j], a);
+              nib8(x[2 * j + 1], b);
+              if constexpr (G == 32) {
+                uint32_t b0, b1;
+                weighted(ch, b0, b1);
+                mma_16816(o[2 * ch], a[0], a[1], b[0], b[1], b0, b1);
+                mma_16816(o[2 * ch + 1], a[2], a[3], b[2], b[3], b0, b1);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {  // lane g's channels lie in half g / 4 of the chunk
+                  const uint32_t m = (g >> 2) == k ? 0xffffffffu : 0u;
+                  uint32_t b0, b1;
+                  weighted(2 * ch + k, b0, b1);
+                  mma_16816(o[2 * ch], a[0] & m, a[1] & m, b[0] & m, b[1] & m, b0, b1);
+                  mma_16816(o[2 * ch + 1], a[2] & m, a[3] & m, b[2] & m, b[3] & m, b0, b1);
+                }
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < NC; ++ch) {
+            uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of channels 0 - 15, the same of 16 - 31
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB>(row, 2 * ch + (mi >> 1))));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t a[2], b[2], b0, b1;  // channels 2g, 2g + 1 of the half
+              byte4(x[2 * k], a);
+              byte4(x[2 * k + 1], b);
+              weighted(G == 32 ? ch : 2 * ch + k, b0, b1);
+              mma_16816(o[2 * ch + k], a[0], a[1], b[0], b[1], b0, b1);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---- (4) join the warps: M, L, and O = sum of o 2^(m - M), in true units
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
+      l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], off);
+    }
+    consumers_sync();  // q~ has been read
+    if (g == 0) {
+      float* ml = wml + warp * 2 * kRows;
+      ml[2 * c] = m_run[0];
+      ml[2 * c + 1] = m_run[1];
+      ml[kRows + 2 * c] = l_run[0];
+      ml[kRows + 2 * c + 1] = l_run[1];
+    }
+    consumers_sync();
+    float M[2], f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      M[e] = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) M[e] = fmaxf(M[e], wml[x * 2 * kRows + 2 * c + e]);
+      f[e] = m_run[e] == -INFINITY ? 0.0f : ex2_approx(m_run[e] - M[e]) * pow2f(24 + ve);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float odd = BITS == 4 ? 0.0625f : 1.0f;  // rows g + 8 hold the codes that stood 16 times too high
+      o[mt][0] *= f[0];
+      o[mt][1] *= f[1];
+      o[mt][2] *= f[0] * odd;
+      o[mt][3] *= f[1] * odd;
+    }
+    if (warp >= kWarps / 2) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        obuf[((warp - kWarps / 2) * MT + mt) * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
+    }
+    consumers_sync();
+    if (warp < kWarps / 2) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float4& v = obuf[(warp * MT + mt) * 32 + lane];
+        const float4 u = v;
+        v = make_float4(o[mt][0] + u.x, o[mt][1] + u.y, o[mt][2] + u.z, o[mt][3] + u.w);
+      }
+    }
+    consumers_sync();
+    for (int x = tid; x < MT * 32; x += kWarps * 32) {
+      float4 v = obuf[x];
+#pragma unroll
+      for (int k = 1; k < kWarps / 2; ++k) {
+        const float4 u = obuf[k * MT * 32 + x];
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      const int mt = x >> 5, gg = (x & 31) >> 2, cc = x & 3;
+      // the channels of tile mt's rows g and g + 8
+      const int ch = BITS == 4 ? (mt >> 1) * 32 + 4 * gg + ((mt & 1) ? 2 : 0) : 16 * mt + 2 * gg;
+      float* d0 = om + (2 * cc) * C::kOmStride + ch;
+      *reinterpret_cast<float2*>(d0) = make_float2(v.x, v.z);
+      *reinterpret_cast<float2*>(d0 + C::kOmStride) = make_float2(v.y, v.w);
+    }
+    // M and L of row `row`, from the warps
+    auto joined = [&](int row, float& Mr, float& Lr) {
+      Mr = -INFINITY;
+      Lr = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) Mr = fmaxf(Mr, wml[x * 2 * kRows + row]);
+      if (Mr != -INFINITY) {
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float mw = wml[x * 2 * kRows + row];
+          if (mw != -INFINITY) Lr = fmaf(wml[x * 2 * kRows + kRows + row], ex2_approx(mw - Mr), Lr);
+        }
+      }
+    };
+    consumers_sync();
+    float* Lrow = wml + kWarps * kRows;  // the unit's L per row (over the warps' values, once they are read)
+    const bool whole = w.i0 == 0 && w.i1 == r.nt;
+    float Lr = 0.0f, Mr = 0.0f;
+    if (tid < kRows) joined(tid, Mr, Lr);
+    consumers_sync();
+    bool store = true;
+    if (whole) {
+      if (tid < kRows) Lrow[tid] = Lr;
+    } else {
+      // ---- (5) this CTA's partial of a unit that other CTAs share. The unit's tiles are
+      // [u0, u0 + nt) of the line; CTA x holds [x per, (x + 1) per) of it; a CTA's slot 0 is
+      // for the segment that starts its piece, slot 1 for the one that ends it.
+      const long long u0 = w.base + (long long)w.u * r.nt;
+      auto slot_of = [&](long long x) { return p.part + (2 * x + (x * per >= u0 ? 0 : 1)) * C::PART; };
+      float* mine_p = slot_of(blockIdx.x);
+      if (tid < kRows) {
+        __stcg(mine_p + tid, Mr);
+        __stcg(mine_p + kRows + tid, Lr);
+      }
+      for (int x = tid; x < kRows * D / 4; x += kWarps * 32) {
+        const int row = x / (D / 4), k = x - row * (D / 4);
+        __stcg(reinterpret_cast<float4*>(mine_p + 2 * kRows) + x,
+               *reinterpret_cast<const float4*>(om + row * C::kOmStride + 4 * k));
+      }
+      consumers_sync();
+      const long long xa = u0 / per, xb = (u0 + r.nt - 1) / per;
+      if (tid == 0) {
+        int* cnt = p.cnt + (long long)w.b * p.Hkv * p.rt_max + h * p.rt_max + rt;
+        __threadfence();
+        const int before = atomicAdd(cnt, 1);
+        const int last = before == (int)(xb - xa);
+        if (last) {
+          *cnt = 0;  // every CTA of the unit has been here
+          __threadfence();
+        }
+        *flag = last;
+      }
+      consumers_sync();
+      store = *flag != 0;
+      if (store) {
+        // merge in CTA order: first the maxima and sums (a thread per row), then the outputs
+        const int np = (int)(xb - xa + 1);
+        if (tid < kRows) {
+          float Mx = -INFINITY, Lx = 0.0f;
+          for (int k = 0; k < np; ++k) Mx = fmaxf(Mx, __ldcg(slot_of(xa + k) + tid));
+          for (int k = 0; k < np; ++k) {
+            const float mk = __ldcg(slot_of(xa + k) + tid);
+            if (mk != -INFINITY) Lx = fmaf(__ldcg(slot_of(xa + k) + kRows + tid), ex2_approx(mk - Mx), Lx);
+          }
+          Lrow[tid] = Lx;
+          wml[tid] = Mx;
+        }
+        consumers_sync();
+        for (int x = tid; x < kRows * D / 4; x += kWarps * 32) {
+          const int row = x / (D / 4), k4 = x - row * (D / 4);
+          const float Mx = wml[row];
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k0 = 0; k0 < np; k0 += 4) {  // four partials' loads in flight
+            float4 v[4];
+            float mk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k0 + k < np) {
+                const float* sp = slot_of(xa + k0 + k);
+                mk[k] = __ldcg(sp + row);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(sp + 2 * kRows) + x);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k0 + k < np && mk[k] != -INFINITY) {
+                const float fk = ex2_approx(mk[k] - Mx);
+                acc.x = fmaf(fk, v[k].x, acc.x);
+                acc.y = fmaf(fk, v[k].y, acc.y);
+                acc.z = fmaf(fk, v[k].z, acc.z);
+                acc.w = fmaf(fk, v[k].w, acc.w);
+              }
+            }
+          }
+          *reinterpret_cast<float4*>(om + row * C::kOmStride + 4 * k4) = acc;
+        }
+      }
+    }
+    consumers_sync();
+    if (store) {
+      // ---- (6) out = Wo (o / L): samples as rows; o / L enters as an fp16 hi + lo pair
+      const float L = Lrow[g];
+      const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // nothing attended: zeros (NaN stays)
+      const float* orow = om + g * C::kOmStride;
+      float mx = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
+          mx = fmaxf(mx, fmaxf(fabsf(v.x * inv), fabsf(v.y * inv)));
+        }
+      }
+      const int ex = row_exponent(mx);
+      const float fx = inv * pow2f(-ex);
+      float acc[MT / kWarps][4];
+#pragma unroll
+      for (int t = 0; t < MT / kWarps; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+        uint32_t bh[2], bl[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
+          const __half2 hv = __floats2half2_rn(v.x * fx, v.y * fx);
+          const float2 hf = __half22float2(hv);
+          bh[e] = h2u(hv);
+          bl[e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
+        }
+#pragma unroll
+        for (int t = 0; t < MT / kWarps; ++t) {
+          const uint4 a = __ldg(p.wo + ((warp + kWarps * t) * MT + ks) * 32 + lane);
+          mma_16816(acc[t], a.x, a.y, a.z, a.w, bh[0], bh[1]);
+          mma_16816(acc[t], a.x, a.y, a.z, a.w, bl[0], bl[1]);
+        }
+      }
+      float fo[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+      __half* xb = reinterpret_cast<__half*>(obuf);  // [8][D + 8]
+#pragma unroll
+      for (int t = 0; t < MT / kWarps; ++t) {
+        const int s0 = 16 * (warp + kWarps * t) + g;
+        __half* x0 = xb + (2 * c) * (D + 8) + s0;
+        x0[0] = __float2half_rn(acc[t][0] * fo[0]);
+        x0[D + 8] = __float2half_rn(acc[t][1] * fo[1]);
+        x0[8] = __float2half_rn(acc[t][2] * fo[0]);
+        x0[D + 8 + 8] = __float2half_rn(acc[t][3] * fo[1]);
+      }
+      consumers_sync();
+      for (int x = tid; x < nrows * (D / 8); x += kWarps * 32) {
+        const int row = x / (D / 8), k = x - row * (D / 8);
+        int tok, head;
+        q_row(row, tok, head);
+        *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
+            *reinterpret_cast<const uint4*>(xb + row * (D + 8) + 8 * k);
+      }
+    }
+    consumers_sync();  // om, wml and obuf are free for the next segment
+  }
+}
+
+// ---------------------------------------------------------------- host side
+constexpr int kMinTilesPerCta = 2;
+// Room for the partials of a launch: the same for every geometry, so that calls of different
+// geometries may follow one another in one workspace and the counters behind it stay zero.
+constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (2 * kRows + kRows * kMaxD) * 4;
+
+template <int D, int G, int BITS>
+kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
+  using C = PCfg<D, G, BITS>;
+  PagedParams p{};
+  const int P = 1 << a.page_shift;
+  const uint64_t dims[3] = {(uint64_t)C::RB, (uint64_t)P, (uint64_t)a.num_pages * a.Hkv};
+  const uint64_t strides[2] = {(uint64_t)C::RB, (uint64_t)C::RB * P};
+  const uint32_t box[3] = {(uint32_t)(C::RB < 128 ? C::RB : 128), (uint32_t)P, 1u};
+  const CUtensorMapSwizzle sw = C::RB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  kvq_status st = encode_tiled_new(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.kc, dims, strides, box, sw, "K pages");
+  if (st == KVQ_OK)
+    st = encode_tiled_new(&p.vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.vc, dims, strides, box, sw, "V pages");
+  if (st != KVQ_OK) return st;
+  p.q = a.q;
+  p.ks = a.ks;
+  p.vs = a.vs;
+  p.table = a.table;
+  p.kv_lens = a.kv_lens;
+  p.q_starts = a.q_starts;
+  p.wq = a.pk->wqf_dev;
+  p.wo = a.pv->wof_dev;
+  p.out = a.out;
+  p.q_ts = a.q_token_stride;
+  p.q_hs = a.q_head_stride;
+  p.table_stride = a.table_stride;
+  const float sigma = a.sigma > 0.0f ? a.sigma : 1.0f / sqrtf((float)D);
+  p.qfac = sigma * 1.4426950408889634f * a.pk->wq_scale;
+  p.ofac = a.pv->wo_scale;
+  p.B = a.B;
+  p.n_q = a.n_q;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.Gq = a.Hq / a.Hkv;
+  p.max_q = a.max_q_len;
+  p.rt_max = (int)(((long long)std::min(a.max_q_len, a.n_q) * p.Gq + kRows - 1) / kRows);
+  p.max_kv = (int)std::min<long long>(a.max_kv_len, (long long)a.max_pages * P);
+  p.num_pages = a.num_pages;
+  p.page_shift = a.page_shift;
+  p.window = a.window;
+  p.min_tiles = kMinTilesPerCta;
+  char* ws = reinterpret_cast<char*>(a.ws);
+  p.part = reinterpret_cast<float*>(ws);
+  p.cnt = reinterpret_cast<int*>(ws + kPartBytes);
+  // no more CTAs than pieces of min_tiles tiles if every request were as long as it may be
+  const long long most = (long long)a.B * a.Hkv * p.rt_max * std::max(1, (p.max_kv + kTile - 1) / kTile);
+  const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kMinBlocks);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(slots, (most + p.min_tiles - 1) / p.min_tiles));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = strm;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = allow_smem<attend_paged_kernel<D, G, BITS>>(a.pk->device, C::kSmem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_paged_kernel<D, G, BITS>, p);
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("attend_paged launch: ") + cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int n_q, int max_q_len) {
+  const long long rt = ((long long)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv) + kRows - 1) / kRows;
+  return kPartBytes + (((size_t)B * Hkv * rt * 4 + 255) / 256) * 256;
+}
+
+kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s) {
+  return dispatch_dgb(a.pk->D, a.pk->G, a.pk->bits, [&](auto d, auto g, auto b) {
+    return run_paged<decltype(d)::value, decltype(g)::value, decltype(b)::value>(a, s);
+  });
+}
+
+uint32_t paged_error_flags(bool clear) {
+  uint32_t v = 0;
+  cudaMemcpyFromSymbol(&v, g_paged_err, sizeof(v));
+  if (clear && v) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbol(g_paged_err, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace kvq

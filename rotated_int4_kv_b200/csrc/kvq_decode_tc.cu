@@ -19,6 +19,9 @@
 // A tile is a box of the cache: T_box consecutive tokens of BH_box consecutive (b, h)
 // (T_box * BH_box = 128 rows, T_box the power of two >= n up to 128), so that its code
 // rows arrive by one TMA tensor load and its output rows leave by TMA tensor stores.
+// Pages (PG): the rows are (token, head) pairs of a slot map, scattered over the cache, so
+// each dequantiser thread brings its own row's codes and scales by async copies of 16 (8)
+// bytes, a tile ahead of their use; a slot outside the pages reads as zeros.
 // Roles (one CTA per SM, persistent over a contiguous range of tiles):
 //   warp 0      TMA: W_dec (resident for the whole launch, 32 or 128 KB), then the code
 //               rows of each tile into one of two slots (swizzled, so that the per-row
@@ -98,7 +101,26 @@ struct DtParams {
   const uint16_t* scales;
   int BH, n, T_cap, t0;
   int T_box, BH_box, t_shift, n_ttiles, ntiles;
+  // pages: row t of the job is head t % H of the token at slots[t / H]
+  const int32_t* slots;
+  const uint8_t* codes;
+  long long n_slots;
+  int H, page_shift;
 };
+
+// The cache row of row (bh, t) of the job, -1 where there is none.
+template <bool PG>
+__device__ __forceinline__ long long dt_cache_row(const DtParams& P, int bh, int t) {
+  if (!(bh < P.BH && t < P.n)) return -1;
+  if constexpr (PG) {
+    const int tok = t / P.H, slot = __ldg(P.slots + tok);
+    if (slot < 0 || slot >= P.n_slots) return -1;
+    return (((long long)(slot >> P.page_shift) * P.H + (t - tok * P.H)) << P.page_shift) +
+           (slot & ((1 << P.page_shift) - 1));
+  } else {
+    return (long long)bh * P.T_cap + P.t0 + t;
+  }
+}
 
 // A tile's first (b, h) and first token (relative to t0).
 __device__ __forceinline__ void dt_tile_origin(const DtParams& P, int tile, int& bh0, int& tt0) {
@@ -107,12 +129,12 @@ __device__ __forceinline__ void dt_tile_origin(const DtParams& P, int tile, int&
   tt0 = (tile - tb * P.n_ttiles) * P.T_box;
 }
 
-// The fp16 scale pairs of cache row (bh, t0 + t), zeros outside the job. The loads are
+// The fp16 scale pairs of a cache row, zeros for row -1. The loads are
 // volatile so that they issue here, a tile before their use, and are not moved next to it.
 template <int NS>
-__device__ __forceinline__ void load_scales(const DtParams& P, int bh, int t, uint32_t (&s)[NS]) {
-  if (bh < P.BH && t < P.n) {
-    const uint16_t* sp = P.scales + ((size_t)bh * P.T_cap + P.t0 + t) * (size_t)(2 * NS);
+__device__ __forceinline__ void load_scales(const DtParams& P, long long crow, uint32_t (&s)[NS]) {
+  if (crow >= 0) {
+    const uint16_t* sp = P.scales + crow * (2 * NS);
     if constexpr (NS == 2) {
       asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "l"(sp));
     } else {
@@ -128,22 +150,22 @@ __device__ __forceinline__ void load_scales(const DtParams& P, int bh, int t, ui
   }
 }
 
-// A cache hint for the scales of cache row (bh, t0 + t): a prefetch is not a load, so a
+// A cache hint for the scales of a cache row: a prefetch is not a load, so a
 // release arrival of this thread does not wait for it.
 template <int NS>
-__device__ __forceinline__ void prefetch_scales(const DtParams& P, int bh, int t) {
-  if (bh < P.BH && t < P.n) {
-    const uint16_t* sp = P.scales + ((size_t)bh * P.T_cap + P.t0 + t) * (size_t)(2 * NS);
+__device__ __forceinline__ void prefetch_scales(const DtParams& P, long long crow) {
+  if (crow >= 0) {
+    const uint16_t* sp = P.scales + crow * (2 * NS);
     asm volatile("prefetch.global.L1 [%0];" ::"l"(sp));
   }
 }
 
-// Async copy of the scales of cache row (bh, t0 + t) into dst (zeros outside the job: a
-// copy of zero source bytes fills its destination with zeros and reads nothing).
+// Async copy of the scales of a cache row into dst (zeros for row -1: a copy of zero
+// source bytes fills its destination with zeros and reads nothing).
 template <int NS>
-__device__ __forceinline__ void cp_async_scales(uint32_t* dst, const DtParams& P, int bh, int t) {
-  const bool in = bh < P.BH && t < P.n;
-  const uint16_t* sp = in ? P.scales + ((size_t)bh * P.T_cap + P.t0 + t) * (size_t)(2 * NS) : P.scales;
+__device__ __forceinline__ void cp_async_scales(uint32_t* dst, const DtParams& P, long long crow) {
+  const bool in = crow >= 0;
+  const uint16_t* sp = in ? P.scales + crow * (2 * NS) : P.scales;
   if constexpr (NS == 2) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(sp), "r"(in ? 8 : 0)
                  : "memory");
@@ -180,7 +202,23 @@ __device__ __forceinline__ uint4 code_piece(const uint8_t* slot, int r, int c) {
   }
 }
 
-template <int D, int BITS, int G>
+// Async copies of a cache row's codes into row r of a code slot (the layout of code_piece).
+template <int D, int BITS>
+__device__ __forceinline__ void cp_async_codes(uint8_t* slot, int r, const DtParams& P, long long crow) {
+  using C = DtCfg<D, BITS>;
+  const bool in = crow >= 0;
+  const uint8_t* src = in ? P.codes + crow * C::kRowBytes : P.codes;
+#pragma unroll
+  for (int c = 0; c < C::kRowBytes / 16; ++c) {
+    const int off = C::kBoxRow == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                                     : (c >> 3) * (kDtRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot + off)), "l"(src + 16 * c),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
+
+template <int D, int BITS, int G, bool PG = false>
 __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_constant__ DtParams P) {
   using C = DtCfg<D, BITS>;
   constexpr int NS = D / G / 2;
@@ -243,7 +281,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && ntile > 0) {
-      prefetch_tensormap(&P.cmap);
+      if constexpr (!PG) prefetch_tensormap(&P.cmap);
       prefetch_tensormap(&P.omap);
       // W_dec is a plan constant: loaded while the previous kernel in the stream finishes
       mbar_arrive_expect_tx(bfull, C::kB);
@@ -251,7 +289,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       for (int kc = 0; kc < C::KC; ++kc) tma_load_2d(sB + kc * C::kChunkB, &P.bmap, bfull, 64 * kc, 0);
       grid_dep_wait();
       const uint64_t pol = l2_evict_first_policy();
-      for (int i = 0; i < ntile; ++i) {
+      for (int i = 0; !PG && i < ntile; ++i) {
         const int slot = i % C::kCSlots;
         if (i >= C::kCSlots && !mbar_wait_bounded(&cfree[slot], ((i / C::kCSlots) - 1) & 1)) {
           atomicOr(&g_dec_tc_err, kErrTimeoutLoad);
@@ -326,41 +364,57 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     // there is one (an arrival with release semantics does not wait for it, unlike a load in
     // flight), else a cache prefetch now and a load at the end of the tile
     uint32_t* srow = sS + row * NS;
-    auto next_scales = [&](int i) {
+    auto row_of = [&](int i) {
       int bh0, tt0;
       dt_tile_origin(P, t_begin + i, bh0, tt0);
+      return dt_cache_row<PG>(P, bh0 + bh_l, tt0 + t_l);
+    };
+    auto next_scales = [&](long long crow) {
       if constexpr (kSS > 0) {
-        cp_async_scales<NS>(srow, P, bh0 + bh_l, tt0 + t_l);
+        cp_async_scales<NS>(srow, P, crow);
       } else {
-        prefetch_scales<NS>(P, bh0 + bh_l, tt0 + t_l);
+        prefetch_scales<NS>(P, crow);
       }
     };
-    auto take_scales = [&](int i, uint32_t (&sc)[NS]) {
+    // (pages: the wait also covers this row's codes of the same tile)
+    auto take_scales = [&](long long crow, uint32_t (&sc)[NS]) {
+      if constexpr (kSS > 0 || PG) cp_async_wait_all();
       if constexpr (kSS > 0) {
-        cp_async_wait_all();
 #pragma unroll
         for (int j = 0; j < NS; ++j) sc[j] = srow[j];
       } else {
-        int bh0, tt0;
-        dt_tile_origin(P, t_begin + i, bh0, tt0);
-        load_scales<NS>(P, bh0 + bh_l, tt0 + t_l, sc);
+        load_scales<NS>(P, crow, sc);
       }
     };
+    // the cache row of tile i, and (pages: a slot map away) that of tile i + 1
+    long long crow = ntile > 0 ? row_of(0) : -1, nrow = -1;
     uint32_t sg[2 * NS];
     if (ntile > 0) {
       uint32_t sc[NS];
-      next_scales(0);
-      take_scales(0, sc);
+      if constexpr (PG) cp_async_codes<D, BITS>(sC, row, P, crow);
+      next_scales(crow);
+      if (ntile > 1) nrow = row_of(1);
+      take_scales(crow, sc);
       factors(sc, sg);
     }
     for (int i = 0; i < ntile; ++i) {
       const int slot = i % C::kCSlots;
       const uint8_t* cs = sC + slot * C::kCodeTile;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&cfull[slot], (i / C::kCSlots) & 1))) {
-        if (lane == 0) atomicOr(&g_dec_tc_err, kErrTimeoutLoad);
-        break;
+      if constexpr (!PG) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&cfull[slot], (i / C::kCSlots) & 1))) {
+          if (lane == 0) atomicOr(&g_dec_tc_err, kErrTimeoutLoad);
+          break;
+        }
       }
-      if (i + 1 < ntile) next_scales(i + 1);
+      crow = nrow;
+      if (i + 1 < ntile) {
+        // pages: this thread alone reads and writes its row of the slots; the slot that the
+        // next tile's codes go to was read in the tile before this one
+        if constexpr (PG && C::kCSlots == 2)
+          cp_async_codes<D, BITS>(sC + ((i + 1) % 2) * C::kCodeTile, row, P, crow);
+        next_scales(crow);
+      }
+      if (i + 2 < ntile) nrow = row_of(i + 2);
       bool ok = true;
       // CPS K chunks per step: one wait for their ring slots, one proxy fence and CPS
       // arrivals per step, their conversions interleaved (more independent work per warp).
@@ -382,8 +436,10 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
           w[4 * pc + 3] = v.w;
         }
         if (kp + CPS == C::KC) {  // every code of this tile has been read: release the slot
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&cfree[slot]);
+          if constexpr (!PG) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&cfree[slot]);
+          }
         }
         bool free_ok = true;
 #pragma unroll
@@ -445,8 +501,10 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       if (i + 1 < ntile) {
         // the next tile's factors, after this tile's last arrival: a release arrival waits
         // for every load of its thread still in flight
+        // (pages with one code slot: its values are all in use by now, the next ones may come)
+        if constexpr (PG && C::kCSlots == 1) cp_async_codes<D, BITS>(sC, row, P, crow);
         uint32_t sn[NS];
-        take_scales(i + 1, sn);
+        take_scales(crow, sn);
         factors(sn, sg);
       }
     }
@@ -468,7 +526,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       int bh0, tt0;
       uint32_t sc[NS];
       dt_tile_origin(P, t_begin, bh0, tt0);
-      load_scales<NS>(P, bh0 + bh_l, tt0 + t_l, sc);
+      load_scales<NS>(P, dt_cache_row<PG>(P, bh0 + bh_l, tt0 + t_l), sc);
       row_norm<NS>(sc, alpha);
     }
     for (int i = 0; i < ntile; ++i) {
@@ -479,7 +537,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       if (i + 1 < ntile) {
         int nb, nt;
         dt_tile_origin(P, t_begin + i + 1, nb, nt);
-        load_scales<NS>(P, nb + bh_l, nt + t_l, sn);
+        load_scales<NS>(P, dt_cache_row<PG>(P, nb + bh_l, nt + t_l), sn);
       }
       const bool any = bh0 + w_bh < P.BH && tt0 + w_t < P.n;  // some row of the warp's box is in the job
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], (i >> 1) & 1))) {
@@ -626,6 +684,63 @@ kvq_status launch_decode_tc(const kvq_plan* p, const uint8_t* codes, const uint1
     return dt_launch<decltype(d)::value, decltype(g)::value, decltype(b)::value>(P, sms, strm);
   });
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("decode (tensor cores) launch: ") + cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+namespace {
+template <int D, int G, int BITS>
+cudaError_t dt_launch_paged(const DtParams& P, int device, cudaStream_t strm) {
+  using C = DtCfg<D, BITS>;
+  const cudaError_t e = allow_smem<decode_tc_kernel<D, BITS, G, true>>(device, C::template kSmem<G>);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(std::min(P.ntiles, num_sms(device)));
+  cfg.blockDim = dim3(kDtThreads);
+  cfg.dynamicSmemBytes = C::template kSmem<G>;
+  cfg.stream = strm;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<D, BITS, G, true>, P);
+}
+}  // namespace
+
+// The rows at n slots (H heads each) of the pages -> out [n][H][D] fp16.
+kvq_status launch_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint16_t* scales, int num_pages,
+                               int page_shift, int H, const int32_t* slots, int n, uint16_t* out, cudaStream_t strm) {
+  const int D = p->D;
+  DtParams P{};
+  const int rows = n * H;  // checked by the caller
+  P.T_box = kDtRows;
+  P.BH_box = 1;
+  P.t_shift = 7;
+  P.n_ttiles = P.ntiles = (rows + kDtRows - 1) / kDtRows;
+  P.BH = 1;
+  P.n = rows;
+  P.scales = scales;
+  P.codes = codes;
+  P.slots = slots;
+  P.n_slots = (long long)num_pages << page_shift;
+  P.H = H;
+  P.page_shift = page_shift;
+  const uint64_t bd[2] = {(uint64_t)D, (uint64_t)D};
+  const uint64_t bs[1] = {(uint64_t)D * 2};
+  const uint32_t bb[2] = {64u, (uint32_t)D};
+  kvq_status st = encode_tiled_new(&P.bmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p->wdec_dev, bd, bs, bb,
+                                   CU_TENSOR_MAP_SWIZZLE_128B, "decode matrix");
+  if (st != KVQ_OK) return st;
+  const uint64_t od[3] = {(uint64_t)D, (uint64_t)rows, 1u};
+  const uint64_t os[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * rows};
+  const uint32_t ob[3] = {32u, 32u, 1u};
+  st = encode_tiled_new(&P.omap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B,
+                        "decode_paged output");
+  if (st != KVQ_OK) return st;
+  const cudaError_t e = dispatch_dgb(D, p->G, p->bits, [&](auto d, auto g, auto b) {
+    return dt_launch_paged<decltype(d)::value, decltype(g)::value, decltype(b)::value>(P, p->device, strm);
+  });
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("decode_paged launch: ") + cudaGetErrorString(e));
   return KVQ_OK;
 }
 

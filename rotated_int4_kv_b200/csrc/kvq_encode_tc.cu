@@ -34,6 +34,10 @@
 // per-channel factor lambda_c / sqrt(D) is applied in the epilogue. An MMA then
 // covers all D channels (N = D), one CTA per tile at either head dim, half the
 // tensor work of the hi/lo product.
+//
+// Pages (PG): the rows of x are n tokens of H heads at given strides, a tile is 128 / H
+// whole tokens (a TMA box {64, H, 128 / H}; the rows behind it stay unused), and each
+// token's destination row comes from a slot map read before the accumulator is waited for.
 #include <algorithm>
 #include <cstdio>
 #include <mutex>
@@ -70,6 +74,16 @@ template <int MAXJ>
 struct TcBatch {
   TcJob j[MAXJ];
   int njobs, ntiles;
+};
+
+// Paged destination of a launch's jobs: row (token, head) of x goes to
+// pages[slot / P][head][slot % P] with slot = slots[token]; tokens whose slot is outside
+// [0, n_slots) are skipped. tok = tokens per tile, box = bytes of one K chunk of a tile.
+struct TcPages {
+  const int32_t* slots;
+  long long n_slots;
+  int H, page_shift, n, tok;
+  uint32_t box;
 };
 
 template <int D, bool EX>
@@ -138,8 +152,9 @@ __device__ __forceinline__ void store_scales(uint16_t* dst, const uint32_t (&sb)
   }
 }
 
-template <int D, bool EX, int G, int BITS, int MAXJ>
-__global__ void __launch_bounds__(kTcThreads, 1) encode_tc_kernel(const __grid_constant__ TcBatch<MAXJ> bt) {
+template <int D, bool EX, int G, int BITS, int MAXJ, bool PG = false>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    encode_tc_kernel(const __grid_constant__ TcBatch<MAXJ> bt, const __grid_constant__ TcPages pg) {
   using C = TcCfg<D, EX>;
   constexpr int kTcChunks = C::kChunks;
   extern __shared__ uint8_t smem_raw[];
@@ -228,8 +243,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) encode_tc_kernel(const __grid_c
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&afull[s], C::kChunkA);
-          tma_load_2d_hint(sA + s * C::kChunkA, &J.xmap, &afull[s], kc * 64, row, pol);
+          if constexpr (PG) {
+            mbar_arrive_expect_tx(&afull[s], pg.box);
+            tma_load_3d_hint(sA + s * C::kChunkA, &J.xmap, &afull[s], kc * 64, 0, (t - J.tile0) * pg.tok, pol);
+          } else {
+            mbar_arrive_expect_tx(&afull[s], C::kChunkA);
+            tma_load_2d_hint(sA + s * C::kChunkA, &J.xmap, &afull[s], kc * 64, row, pol);
+          }
         }
         if (!ok) {
           atomicOr(&g_enc_tc_err, kErrTimeoutLoad);
@@ -300,21 +320,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) encode_tc_kernel(const __grid_c
     const int q = warp & 3;
     const int h = (warp - 2) >> 2;
     int job = ntile > 0 ? job_of(bt.j, bt.njobs, 0, t_begin) : 0;
+    // pages: this thread's place in a tile (the slot map may come from the previous kernel)
+    const int ptok = PG ? (32 * q + lane) / pg.H : 0, phead = PG ? 32 * q + lane - ptok * pg.H : 0;
+    if constexpr (PG) grid_dep_wait();
     for (int i = 0; i < ntile; ++i) {
       const int t = t_begin + i;
       job = job_of(bt.j, bt.njobs, job, t);
       const TcJob& J = bt.j[job];
       const int a = i & 1;
+      int slot = -1;
+      if constexpr (PG) {
+        const int tok = (t - J.tile0) * pg.tok + ptok;
+        if (ptok < pg.tok && tok < pg.n) slot = __ldg(pg.slots + tok);
+      }
       // warp-uniform outcome: the tcgen05.ld below needs the whole warp
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], (i >> 1) & 1))) {
         if (lane == 0) atomicOr(&g_enc_tc_err, kErrTimeoutLoad);
         break;
       }
       tc_fence_after();
-      const int r = (t - J.tile0) * kTcRows + 32 * q + lane;  // row of this thread's vector in the job
-      const bool valid = r < J.rows;
-      const int bh = valid ? r / J.n : 0;
-      const size_t orow = (size_t)bh * J.T_cap + J.pos + (r - bh * J.n);
+      bool valid;
+      size_t orow;
+      if constexpr (PG) {
+        valid = slot >= 0 && slot < pg.n_slots;
+        orow = (((size_t)(slot >> pg.page_shift) * pg.H + phead) << pg.page_shift) + (slot & ((1 << pg.page_shift) - 1));
+      } else {
+        const int r = (t - J.tile0) * kTcRows + 32 * q + lane;  // row of this thread's vector in the job
+        valid = r < J.rows;
+        const int bh = valid ? r / J.n : 0;
+        orow = (size_t)bh * J.T_cap + J.pos + (r - bh * J.n);
+      }
       const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * C::kN + 32 * NGH * h);
       uint32_t sb[NGH * SPC];
       if constexpr (EX) {
@@ -817,7 +852,7 @@ template <int D, bool EX, int G, int BITS>
 cudaError_t tc_launch(cudaLaunchConfig_t cfg, const TcBatch<kTcMaxJobs>& bt, int tiles, int sms) {
   cfg.gridDim = dim3(TcCfg<D, EX>::kSplit == 2 ? 2 * std::min(tiles, sms / 2) : std::min(tiles, sms));
   cfg.dynamicSmemBytes = TcCfg<D, EX>::kSmem;
-  return cudaLaunchKernelEx(&cfg, encode_tc_kernel<D, EX, G, BITS, kTcMaxJobs>, bt);
+  return cudaLaunchKernelEx(&cfg, encode_tc_kernel<D, EX, G, BITS, kTcMaxJobs>, bt, TcPages{});
 }
 
 template <int G, int BITS>
@@ -918,6 +953,83 @@ kvq_status launch_encode_tc(const kvq_encode_job* jobs, int njobs, cudaStream_t 
     });
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("encode (tensor cores) launch: ") + cudaGetErrorString(e));
+  }
+  return KVQ_OK;
+}
+
+namespace {
+
+constexpr int kTcPageJobs = 2;  // K and V of a layer share a launch
+
+template <int D, bool EX, int G, int BITS>
+cudaError_t tc_launch_paged(cudaLaunchConfig_t cfg, const TcBatch<kTcPageJobs>& bt, const TcPages& pg, int device) {
+  const int sms = num_sms(device);
+  const cudaError_t e = allow_smem<encode_tc_kernel<D, EX, G, BITS, kTcPageJobs, true>>(device, TcCfg<D, EX>::kSmem);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(TcCfg<D, EX>::kSplit == 2 ? 2 * std::min(bt.ntiles, sms / 2) : std::min(bt.ntiles, sms));
+  cfg.dynamicSmemBytes = TcCfg<D, EX>::kSmem;
+  return cudaLaunchKernelEx(&cfg, encode_tc_kernel<D, EX, G, BITS, kTcPageJobs, true>, bt, pg);
+}
+
+}  // namespace
+
+// n tokens of H heads per job into pages; the jobs share n, H, the slot map and the page size.
+kvq_status launch_encode_paged(const kvq_paged_encode_job* jobs, int njobs, int n, int H, int page_shift,
+                               int num_pages, const int32_t* slots, cudaStream_t strm) {
+  const kvq_plan* p0 = jobs[0].plan;
+  const int D = p0->D;
+  const bool ex = p0->xform == 1;
+  for (int i0 = 0; i0 < njobs; i0 += kTcPageJobs) {
+    const int nj = std::min(kTcPageJobs, njobs - i0);
+    TcBatch<kTcPageJobs> bt{};
+    TcPages pg{};
+    pg.slots = slots;
+    pg.n_slots = (long long)num_pages << page_shift;
+    pg.H = H;
+    pg.page_shift = page_shift;
+    pg.n = n;
+    pg.tok = kTcRows / H;
+    pg.box = (uint32_t)(pg.tok * H * 128);
+    const int tiles = (n + pg.tok - 1) / pg.tok;
+    for (int k = 0; k < nj; ++k) {
+      const kvq_paged_encode_job& j = jobs[i0 + k];
+      TcJob& J = bt.j[k];
+      // dimensions of size one have no stride of their own
+      const uint64_t hs = H == 1 ? (uint64_t)D : (uint64_t)j.head_stride;
+      const uint64_t ts = n == 1 ? hs * H : (uint64_t)j.token_stride;
+      const uint64_t xd[3] = {(uint64_t)D, (uint64_t)H, (uint64_t)n};
+      const uint64_t xs[2] = {hs * 2, ts * 2};
+      const uint32_t xb[3] = {64u, (uint32_t)H, (uint32_t)pg.tok};
+      kvq_status st = encode_tiled_new(&J.xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, j.x, xd, xs, xb,
+                                       CU_TENSOR_MAP_SWIZZLE_128B, "encode_paged x");
+      if (st != KVQ_OK) return st;
+      const uint64_t wd[2] = {(uint64_t)D, (uint64_t)(ex ? D : 2 * D)};
+      const uint64_t ws[1] = {(uint64_t)D * 2};
+      const uint32_t wb[2] = {64u, (uint32_t)(ex ? D : 256)};
+      st = encode_tiled_new(&J.wmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, j.plan->wt_dev, wd, ws, wb,
+                            CU_TENSOR_MAP_SWIZZLE_128B, "encode weights");
+      if (st != KVQ_OK) return st;
+      J.codes = j.codes;
+      J.scales = j.scales;
+      J.chan = j.plan->enc_dev->chan;
+      J.tile0 = k * tiles;
+    }
+    bt.njobs = nj;
+    bt.ntiles = nj * tiles;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.stream = strm;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = dispatch_dgb(D, p0->G, p0->bits, [&](auto d, auto g, auto b) {
+      constexpr int kD = decltype(d)::value, kG = decltype(g)::value, kB = decltype(b)::value;
+      return ex ? tc_launch_paged<kD, true, kG, kB>(cfg, bt, pg, p0->device)
+                : tc_launch_paged<kD, false, kG, kB>(cfg, bt, pg, p0->device);
+    });
+    if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("encode_paged launch: ") + cudaGetErrorString(e));
   }
   return KVQ_OK;
 }

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <type_traits>
 
@@ -48,6 +49,16 @@ struct kvq_plan {
   // Tensor-core decode operand in the same block: W_dec = diag(s) Q^T Lambda^-1 as fp16,
   // D rows (output samples) x D columns (channels, in the dequantiser's pair order).
   const uint16_t* wdec_dev = nullptr;
+  // Paged-attention operands in the same block, fp16 times a power of two (one rounding per
+  // entry, the largest entry in [1, 2)): Lambda^-1 Q diag(s) (query rotation) and
+  // diag(s) Q^T Lambda^-1 (output un-rotation), each as row-major [D][D] and in the order of
+  // mma.m16n8k16 A fragments (16 bytes per (16-row tile, K step, lane)).
+  const uint16_t* wq_dev = nullptr;
+  const uint16_t* wo_dev = nullptr;
+  const uint4* wqf_dev = nullptr;
+  const uint4* wof_dev = nullptr;
+  float wq_scale = 1.0f;   // what the stored matrices are multiplied by to give the true ones
+  float wo_scale = 1.0f;
 };
 
 namespace kvq {
@@ -79,9 +90,26 @@ kvq_status encode_tiled(CUtensorMap* map, CUtensorMapDataType dt, int rank, cons
                         const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                         CUtensorMapSwizzle swz, const char* what);
 
+// the same without the cache of encoded maps
+kvq_status encode_tiled_new(CUtensorMap* map, CUtensorMapDataType dt, int rank, const void* base,
+                            const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                            CUtensorMapSwizzle swz, const char* what);
+
 int num_sms(int device);
 
 kvq_status check_plan_device(const kvq_plan* p);
+
+// Lets a kernel use `bytes` of dynamic shared memory on `device` (an attribute of the
+// kernel on one device; set once for each).
+template <auto Kernel>
+cudaError_t allow_smem(int device, int bytes) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // tensor-core encode (kvq_encode_tc.cu)
 bool encode_tc_supported(int D, int G);
@@ -155,6 +183,46 @@ kvq_status launch_attend_fp16(const uint16_t* q, const uint16_t* k, const uint16
 
 kvq_status attend_split_info(int B, int Hq, int Hkv, int D, int G, int bits, int T, int* splits, int* cluster,
                              int* head_tiles);
+// pages (kvq_page_plan.cu, kvq_encode_tc.cu, kvq_decode_tc.cu, kvq_attend_paged.cu)
+constexpr int kMaxPlanRequests = 16384;  // requests of one page_plan call (12 bytes of shared memory each)
+constexpr int kMaxPageHeads = 128;       // KV heads of a paged encode (a tile holds whole tokens)
+kvq_status launch_page_plan(const int32_t* kv_lens, const int32_t* q_lens, int B, int32_t* table, int max_pages,
+                            long long table_stride, const int32_t* free_pages, int n_free, const int32_t* free_head,
+                            int32_t* free_head_out, int page_shift, int32_t* slots, int32_t* positions, int n_slots,
+                            int32_t* q_starts, int32_t* kv_out, int32_t* info, cudaStream_t s);
+kvq_status launch_page_release(const uint8_t* done, int32_t* kv_lens, const int32_t* table, long long table_stride,
+                               int B, int max_pages, int page_shift, int32_t* free_pages, int n_free,
+                               int32_t* free_head, cudaStream_t s);
+kvq_status launch_encode_paged(const kvq_paged_encode_job* jobs, int njobs, int n, int H, int page_shift,
+                               int num_pages, const int32_t* slots, cudaStream_t s);
+kvq_status launch_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint16_t* scales, int num_pages,
+                               int page_shift, int H, const int32_t* slots, int n, uint16_t* out, cudaStream_t s);
+// One paged attention call (host view of kvq_attend_paged's arguments).
+struct PagedAttendHost {
+  const kvq_plan* pk;
+  const kvq_plan* pv;
+  const uint16_t* q;
+  long long q_token_stride, q_head_stride;
+  const uint8_t* kc;
+  const uint16_t* ks;
+  const uint8_t* vc;
+  const uint16_t* vs;
+  int num_pages, page_shift;
+  const int32_t* table;
+  int max_pages;
+  long long table_stride;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  int B, n_q, Hq, Hkv, max_q_len, max_kv_len, window;
+  float sigma;
+  uint16_t* out;
+  void* ws;
+  size_t ws_bytes;
+};
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int n_q, int max_q_len);
+kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s);
+uint32_t paged_error_flags(bool clear);
+
 kvq_status launch_wait_probe(uint32_t limit_us, cudaStream_t s);
 
 // device error word (bit flags raised by kernels that gave up a bounded wait)

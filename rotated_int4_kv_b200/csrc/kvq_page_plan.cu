@@ -1,0 +1,266 @@
+// kvq_page_plan.cu -- block tables and slot maps of a serving step, built on the GPU from
+// the requests' lengths, and the return of finished requests' pages.
+//
+// For request b with kv cached and q new tokens and pages of P tokens,
+//   have = ceil(kv / P), want = ceil((kv + q) / P), need = want - have (0 when want does
+//   not fit the table), upto = inclusive prefix sum of need,
+//   served = want fits and (need == 0 or upto <= free entries left),
+// the pages of a served request come from the free list at upto - need, and token j goes to
+// position kv + j, slot = page * P + position % P. Integers only; every output is a
+// function of the inputs alone (no atomics), so two calls on the same inputs agree.
+//
+// The work is a few hundred KB at most, so the time is latency: one launch, one
+// thread-block cluster. Every CTA scans all requests itself (B <= 16384: a block scan of at
+// most 16 requests per thread) into its shared memory, a cluster barrier then separates all
+// reads of the lengths and of the free-list head from the writes that may alias them, and
+// the cluster's warps share the table entries (a warp per request) and the tokens (32 at a
+// time, the owning request by binary search over the starts in shared memory). A split into
+// a scan kernel and a fill kernel would cost a second launch.
+#include <algorithm>
+
+#include "kvq_internal.h"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanCluster = 8;       // CTAs at most (portable cluster size)
+constexpr int kPlanPerCta = 4096;     // tokens or requests per CTA before another joins
+
+struct PagePlanParams {
+  const int32_t* kv_lens;
+  const int32_t* q_lens;
+  int32_t* table;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* free_head_out;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* q_starts;
+  int32_t* kv_out;
+  int32_t* info;
+  long long table_stride;
+  int B, max_pages, n_free, page_shift, n_slots;
+};
+
+__device__ __forceinline__ int32_t sat32(long long v) { return v > 0x7fffffffll ? 0x7fffffff : (int32_t)v; }
+
+// Inclusive prefix sum of v over the block; total in *sum. `part` holds 32 values.
+__device__ __forceinline__ long long block_scan(long long v, long long* part, long long* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += u;
+  }
+  __syncthreads();  // `part` may still be read by the scan before this one
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = part[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += u;
+    }
+    part[lane] = w;
+  }
+  __syncthreads();
+  *sum = part[31];
+  return v + (warp ? part[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PagePlanParams p) {
+  extern __shared__ int32_t s_req[];   // [B] start, [B] first entry of the free list (-1: refused), [B] cached tokens
+  __shared__ long long part[32];
+  __shared__ long long served_pages;
+  __shared__ int refused;
+  int32_t* s_start = s_req;
+  int32_t* s_first = s_req + p.B;
+  int32_t* s_kv = s_req + 2 * p.B;
+  const int tid = threadIdx.x;
+  const int P = 1 << p.page_shift;
+  if (tid == 0) {
+    served_pages = 0;
+    refused = 0;
+  }
+  grid_dep_launch();
+  grid_dep_wait();
+  const int head = min(max(__ldcg(p.free_head), 0), p.n_free);
+  const long long room = p.n_free - head;
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long qs = 0, ns = 0;
+  for (int b = b0; b < b1; ++b) {
+    const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
+    const long long want = (kv + q + P - 1) >> p.page_shift;
+    qs += q;
+    ns += want <= p.max_pages ? want - ((kv + P - 1) >> p.page_shift) : 0;
+  }
+  long long total, wanted;
+  long long q_at = block_scan(qs, part, &total) - qs;
+  long long n_at = block_scan(ns, part, &wanted) - ns;
+  long long got = 0;
+  int ref = 0;
+  for (int b = b0; b < b1; ++b) {
+    const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
+    const long long want = (kv + q + P - 1) >> p.page_shift;
+    const bool fits = want <= p.max_pages;
+    const long long need = fits ? want - ((kv + P - 1) >> p.page_shift) : 0;
+    const bool served = fits && (need == 0 || n_at + need <= room);
+    s_start[b] = sat32(q_at);
+    s_first[b] = served ? (need ? head + (int)n_at : 0) : -1;
+    s_kv[b] = (int32_t)kv;
+    if (served) got += need;
+    else ++ref;
+    q_at += q;
+    n_at += need;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    got += __shfl_xor_sync(0xffffffffu, got, off);
+    ref += __shfl_xor_sync(0xffffffffu, ref, off);
+  }
+  if ((tid & 31) == 0) {
+    if (got) atomicAdd(reinterpret_cast<unsigned long long*>(&served_pages), (unsigned long long)got);
+    if (ref) atomicAdd(&refused, ref);
+  }
+  __syncthreads();
+  // every CTA has read the lengths and the head: from here on they may be overwritten
+  if (gridDim.x > 1) {
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  const int nthreads = (int)gridDim.x * kPlanThreads, gt = (int)blockIdx.x * kPlanThreads + tid;
+  if (gt == 0) {
+    p.free_head_out[0] = head + (int)served_pages;
+    p.q_starts[p.B] = sat32(total);
+    p.info[0] = sat32(total);
+    p.info[1] = (int)served_pages;
+    p.info[2] = refused;
+    p.info[3] = sat32(wanted);
+  }
+  // starts and lengths; the start of b + 1 bounds the new tokens of b, which a served
+  // request has in full (its length fits its table, so it is below the saturation)
+  auto q_of = [&](int b) { return (b + 1 < p.B ? (long long)s_start[b + 1] : (long long)sat32(total)) - s_start[b]; };
+  for (int b = gt; b < p.B; b += nthreads) {
+    p.q_starts[b] = s_start[b];
+    p.kv_out[b] = s_first[b] >= 0 ? (int32_t)(s_kv[b] + q_of(b)) : s_kv[b];
+  }
+  // new table entries: a warp per request
+  for (int b = gt >> 5; b < p.B; b += nthreads >> 5) {
+    const int first = s_first[b];
+    if (first < 0) continue;
+    const long long kv = s_kv[b];
+    const int have = (int)((kv + P - 1) >> p.page_shift), want = (int)((kv + q_of(b) + P - 1) >> p.page_shift);
+    for (int e = have + (tid & 31); e < want; e += 32)
+      p.table[(long long)b * p.table_stride + e] = __ldg(p.free_pages + first + e - have);
+  }
+  // slots and positions, one token per thread; behind the last token both are -1
+  for (long long t = gt; t < p.n_slots; t += nthreads) {
+    int slot = -1, pos = -1;
+    if (t < total && p.B > 0) {
+      int lo = 0, hi = p.B;  // last request whose start is <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      const long long kv = s_kv[lo], at = kv + (t - s_start[lo]);
+      pos = sat32(at);
+      const int first = s_first[lo];
+      if (first >= 0) {
+        const int blk = (int)(at >> p.page_shift), have = (int)((kv + P - 1) >> p.page_shift);
+        const int page = blk < have ? __ldcg(p.table + (long long)lo * p.table_stride + blk)
+                                    : __ldg(p.free_pages + first + blk - have);
+        // a page whose slots would not fit 32 bits is no page of a cache
+        slot = page < 0 || page > (0x7fffffff >> p.page_shift) ? -1 : page * P + (int)(at & (P - 1));
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+}
+
+// Finished requests: the pages of every marked row go back in front of the free list's
+// head, in row order, and the row's length becomes 0. One CTA: a release is rare and small.
+__global__ void __launch_bounds__(kPlanThreads) page_release_kernel(const uint8_t* done, int32_t* kv_lens,
+                                                                    const int32_t* table, long long table_stride,
+                                                                    int B, int max_pages, int page_shift,
+                                                                    int32_t* free_pages, int n_free,
+                                                                    int32_t* free_head) {
+  __shared__ long long part[32];
+  const int tid = threadIdx.x, P = 1 << page_shift;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int head = min(max(__ldcg(free_head), 0), n_free);
+  long long before = 0;  // pages returned by earlier chunks
+  for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
+    const int b = c0 + tid;
+    const bool mine = b < B && done[b] != 0;
+    const int n = mine ? (int)min(((long long)max(kv_lens[b], 0) + P - 1) >> page_shift, (long long)max_pages) : 0;
+    long long sum;
+    const long long at = before + block_scan(n, part, &sum) - n;
+    // entry i of the row goes to head - 1 - (at + i): never in front of the list's start
+    for (int i = 0; i < n && at + i < head; ++i) free_pages[head - 1 - (at + i)] = table[b * table_stride + i];
+    if (mine) kv_lens[b] = 0;
+    before += sum;
+  }
+  __syncthreads();
+  if (tid == 0) free_head[0] = head - (int)min(before, (long long)head);
+}
+
+}  // namespace
+
+kvq_status launch_page_plan(const int32_t* kv_lens, const int32_t* q_lens, int B, int32_t* table, int max_pages,
+                            long long table_stride, const int32_t* free_pages, int n_free, const int32_t* free_head,
+                            int32_t* free_head_out, int page_shift, int32_t* slots, int32_t* positions, int n_slots,
+                            int32_t* q_starts, int32_t* kv_out, int32_t* info, cudaStream_t s) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = allow_smem<page_plan_kernel>(device, kMaxPlanRequests * 12);
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("page_plan: ") + cudaGetErrorString(e));
+  const PagePlanParams p{kv_lens, q_lens,   table,  free_pages, free_head,    free_head_out, slots,     positions,
+                         q_starts, kv_out, info,   table_stride, B,           max_pages,     n_free,    page_shift,
+                         n_slots};
+  const int ctas = std::min(kPlanCluster, std::max(1, (std::max(B, n_slots) + kPlanPerCta - 1) / kPlanPerCta));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = (size_t)B * 12;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, page_plan_kernel, p);
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("page_plan launch: ") + cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+kvq_status launch_page_release(const uint8_t* done, int32_t* kv_lens, const int32_t* table, long long table_stride,
+                               int B, int max_pages, int page_shift, int32_t* free_pages, int n_free,
+                               int32_t* free_head, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, page_release_kernel, done, kv_lens, table, table_stride, B, max_pages,
+                                           page_shift, free_pages, n_free, free_head);
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("page_release launch: ") + cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+}  // namespace kvq

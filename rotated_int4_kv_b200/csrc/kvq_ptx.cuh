@@ -14,6 +14,7 @@ enum : uint32_t {
   kErrTimeoutLoad = 1u,      // an mbarrier for an incoming TMA load never completed
   kErrTimeoutStore = 2u,     // a bulk store group never drained
   kErrTimeoutCombine = 4u,   // a cluster merge never received (or never released) a partial
+  kErrBadPage = 8u,          // a block table named a page outside the cache
 };
 
 // Wait budget for any single barrier, in nanoseconds of %globaltimer.
