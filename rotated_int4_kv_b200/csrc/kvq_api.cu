@@ -318,8 +318,11 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
     }
   // paged-attention operands: the query rotation Lambda^-1 Q diag(s) (row = channel) and the
   // output un-rotation diag(s) Q^T Lambda^-1 (row = sample), fp16 times a power of two that
-  // puts the largest entry in [1, 2) (no fp16 range limit applies to lambda), row-major and as
-  // A fragments: lane (g, c) of K step ks holds (row g | g + 8, columns 16 ks + 2c, + 1 | + 8, + 9)
+  // puts the largest entry in [1, 2) (no fp16 range limit applies to lambda). Twice: as
+  // row-major matrices with the channels in the order in which the prompt kernel converts a
+  // word of codes (int4: 0 4 1 5 2 6 3 7 of each eight, int8: 0 2 1 3 4 6 5 7), and in
+  // natural order as A fragments: lane (g, c) of K step ks holds (row g | g + 8, columns
+  // 16 ks + 2c, + 1 | + 8, + 9)
   std::vector<uint16_t> wpg((size_t)4 * D * D);
   {
     std::vector<double> m((size_t)D * D);
@@ -337,9 +340,10 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
     for (int which = 0; which < 2; ++which) {
       uint16_t* row = wpg.data() + (size_t)which * D * D;
       uint16_t* frag = wpg.data() + (size_t)(2 + which) * D * D;
+      auto entry = [&](int i, int k) { return kvq::half_bits((float)(which ? m[(size_t)k * D + i] : m[(size_t)i * D + k])); };
       for (int i = 0; i < D; ++i)
         for (int k = 0; k < D; ++k)
-          row[(size_t)i * D + k] = kvq::half_bits((float)(which ? m[(size_t)k * D + i] : m[(size_t)i * D + k]));
+          row[(size_t)i * D + k] = which ? entry(i, kvq::word_channel(k, bits)) : entry(kvq::word_channel(i, bits), k);
       size_t o = 0;
       for (int mt = 0; mt < D / 16; ++mt)
         for (int ks = 0; ks < D / 16; ++ks)
@@ -347,7 +351,7 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
             for (int r = 0; r < 4; ++r)
               for (int x = 0; x < 2; ++x) {
                 const int i = 16 * mt + (lane >> 2) + 8 * (r & 1), k = 16 * ks + 2 * (lane & 3) + 8 * (r >> 1) + x;
-                frag[o++] = row[(size_t)i * D + k];
+                frag[o++] = entry(i, k);
               }
     }
   }
@@ -816,7 +820,7 @@ kvq_status kvq_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint1
 
 size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 128 && D != 256) || n_q < 0 || max_q_len < 1) return 0;
-  return kvq::paged_workspace_bytes(B, Hq, Hkv, n_q, max_q_len);
+  return kvq::paged_workspace_bytes(Hq, Hkv, max_q_len);
 }
 
 kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,
@@ -850,7 +854,7 @@ kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16
       return fail(KVQ_ERR_ALIGNMENT, "attend_paged: query strides must be multiples of 8 elements");
     if ((n_q > 1 && q_token_stride < 0) || (Hq > 1 && q_head_stride < 0))
       return fail(KVQ_ERR_INVALID_ARG, "attend_paged: negative query stride");
-    const size_t need = kvq::paged_workspace_bytes(B, Hq, Hkv, n_q, max_q_len);
+    const size_t need = kvq::paged_workspace_bytes(Hq, Hkv, max_q_len);
     if (!ws || ws_bytes < need) return fail(KVQ_ERR_WORKSPACE, "attend_paged: workspace missing or too small");
     if (!kvq::aligned16(ws)) return fail(KVQ_ERR_ALIGNMENT, "attend_paged: workspace must be 16-byte aligned");
     st = kvq::check_plan_device(pk);
@@ -865,7 +869,8 @@ kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16
 kvq_status kvq_poll_device_errors(uint32_t* flags) {
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(KVQ_ERR_CUDA, "poll: device synchronize failed");
   const uint32_t f = kvq::codec_error_flags(true) | kvq::attend_error_flags(true) | kvq::encode_tc_error_flags(true) |
-                     kvq::decode_tc_error_flags(true) | kvq::paged_error_flags(true);
+                     kvq::decode_tc_error_flags(true) | kvq::paged_error_flags(true) |
+                     kvq::prompt_error_flags(true);
   if (flags) *flags = f;
   return KVQ_OK;
 }

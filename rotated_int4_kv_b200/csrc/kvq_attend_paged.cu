@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       consumers_sync();
       const long long xa = u0 / per, xb = (u0 + r.nt - 1) / per;
       if (tid == 0) {
-        int* cnt = p.cnt + (long long)w.b * p.Hkv * p.rt_max + h * p.rt_max + rt;
+        int* cnt = p.cnt + xa;  // no two units that are cut have the same first CTA
         __threadfence();
         const int before = atomicAdd(cnt, 1);
         const int last = before == (int)(xb - xa);
@@ -911,9 +911,13 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
 
 // ---------------------------------------------------------------- host side
 constexpr int kMinTilesPerCta = 2;
-// Room for the partials of a launch: the same for every geometry, so that calls of different
-// geometries may follow one another in one workspace and the counters behind it stay zero.
+// Workspace: a counter per CTA, at the start whatever the geometry (calls of different
+// geometries, and the prompt kernel, may follow one another in one workspace and find the
+// counters zero), then the partials.
+constexpr size_t kCntBytes = (kMaxCtas * 4 + 255) / 256 * 256;
 constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (2 * kRows + kRows * kMaxD) * 4;
+// Query rows of a request from which on the prompt kernel takes a call.
+constexpr int kPromptRows = 48;
 
 template <int D, int G, int BITS>
 kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
@@ -956,8 +960,8 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.window = a.window;
   p.min_tiles = kMinTilesPerCta;
   char* ws = reinterpret_cast<char*>(a.ws);
-  p.part = reinterpret_cast<float*>(ws);
-  p.cnt = reinterpret_cast<int*>(ws + kPartBytes);
+  p.cnt = reinterpret_cast<int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + kCntBytes);
   // no more CTAs than pieces of min_tiles tiles if every request were as long as it may be
   const long long most = (long long)a.B * a.Hkv * p.rt_max * std::max(1, (p.max_kv + kTile - 1) / kTile);
   const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kMinBlocks);
@@ -979,12 +983,14 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
 
 }  // namespace
 
-size_t paged_workspace_bytes(int B, int Hq, int Hkv, int n_q, int max_q_len) {
-  const long long rt = ((long long)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv) + kRows - 1) / kRows;
-  return kPartBytes + (((size_t)B * Hkv * rt * 4 + 255) / 256) * 256;
+bool paged_uses_prompt(int Hq, int Hkv, int max_q_len) { return (long long)max_q_len * (Hq / Hkv) >= kPromptRows; }
+
+size_t paged_workspace_bytes(int Hq, int Hkv, int max_q_len) {
+  return kCntBytes + (paged_uses_prompt(Hq, Hkv, max_q_len) ? std::max(kPartBytes, prompt_part_bytes()) : kPartBytes);
 }
 
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s) {
+  if (paged_uses_prompt(a.Hq, a.Hkv, a.max_q_len)) return launch_attend_prompt(a, reinterpret_cast<char*>(a.ws) + kCntBytes, s);
   return dispatch_dgb(a.pk->D, a.pk->G, a.pk->bits, [&](auto d, auto g, auto b) {
     return run_paged<decltype(d)::value, decltype(g)::value, decltype(b)::value>(a, s);
   });

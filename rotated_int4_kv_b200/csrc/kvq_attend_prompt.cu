@@ -1,0 +1,1014 @@
+// kvq_attend_prompt.cu -- attention of many query tokens per request (prompts, chunks of
+// prompts) over a paged int4/int8 cache for sm_100a, on the 5th-generation tensor cores, in
+// the rotated domain as the few-token kernel (kvq_attend_paged.cu):
+//   q~ = Lambda_K^-1 Q diag(s_K) q,   S = q~ K^T with K = c_K scale_K,
+//   O = softmax(sigma S) V with V = c_V scale_V,   out = O (Lambda_V^-1 Q diag(s_V)).
+//
+// Work. A unit is (request, block of R query rows, KV head), a query row one (query token,
+// head of the KV head's group), R = 256 at head_dim 128 and 128 at 256; its tokens are taken
+// in tiles of T = 128 (64), of which those that the mask leaves empty for the whole unit are
+// not counted. The tiles of all units form one line and every CTA of a persistent grid (one
+// per SM) takes an equal piece of it. A unit cut by a piece's border leaves partials (m, l, o)
+// in the workspace, which a second kernel joins in CTA order; whole units are written here.
+//
+// Roles (13 warps):
+//   dequantisers  codes and scales of the next tile travel through registers; a word of codes
+//                 becomes fp16 pairs by masks, times the scale (one rounding per element), and
+//                 goes to shared memory as K- or V-rows with a 128-byte swizzle. Two K and two
+//                 V tiles are held, and every query row of the unit uses a converted tile.
+//   MMA           one thread issues S = Q K^T (shared, shared -> TMEM) and O += P V (P in
+//                 TMEM over S; V as a transposed operand, so one layout serves both).
+//   softmax       a thread per query row: the maximum over its S row, exp2, P as fp16 back to
+//                 TMEM. O is rescaled only when a row's maximum has grown by more than 2^8
+//                 since the last time, which after the first tiles is rare.
+// Head_dim 128 has two query blocks of 128 rows that alternate: while one's softmax runs the
+// tensor cores work for the other. At head_dim 256 there is room in TMEM for one block and
+// two S buffers: the scores of the next tile are made while the softmax of this one runs.
+// The query's rotation and the output's un-rotation are products of the same kind: the
+// plan's matrix passes through the K tiles' ring, and each row normalises its own result.
+//
+// Number formats. K and V are fp16 c * scale: exact multiples of 2^-24 below 2^-13 and one
+// rounding (2^-12 on average) elsewhere; a tile with a scale from 2^12 (int8: 2^9) on is held
+// divided by 2^8, so that no product leaves fp16. q~ and O enter their products as one fp16
+// rounding after a power-of-two normalisation per row, P as one fp16 rounding; S, O, the
+// maxima and sums are fp32. A token whose V scale is not finite is held as zeros and the
+// rows that attend it (and no others) are set to NaN at the end.
+#include <algorithm>
+#include <string>
+
+#include "kvq_internal.h"
+#include "kvq_ptx.cuh"
+
+namespace kvq {
+
+__device__ uint32_t g_prompt_err = 0;
+
+namespace {
+
+constexpr int kPrWarps = 13;
+constexpr int kPrThreads = kPrWarps * 32;
+constexpr int kPrMaxCtas = 160;
+constexpr int kPrPart = 256 * (128 + 2);  // floats of a partial: m, l and o of R rows (R * D = 32768)
+constexpr int kFlagRing = 8;              // tiles whose flags are held: softmax is at most three behind
+
+template <int D, int G, int BITS>
+struct PrCfg {
+  static constexpr int NQ = D == 128 ? 2 : 1;   // blocks of 128 query rows
+  static constexpr int SB = D == 128 ? 1 : 2;   // S buffers per block
+  static constexpr int R = 128 * NQ;
+  static constexpr int T = D == 128 ? 128 : 64;
+  static constexpr int ND = kPrWarps - 1 - 4 * NQ;  // dequantiser warps
+  static constexpr int NW = D / T;              // ring tiles of a rotation matrix
+  static constexpr int NJ = 16 / ND;            // items (a row's 32 channels) of a thread, tile and operand
+  static constexpr int CW = BITS;               // 32-bit words of an item's codes
+  static constexpr int kQ = NQ * 128 * D * 2;
+  static constexpr int kTile = T * D * 2;
+  static constexpr int kScan = kPrThreads * 8;
+  static constexpr int kFlags = kFlagRing * 5 * 4;
+  static constexpr int kBars = 256;
+  static constexpr int kSmem = kQ + 4 * kTile + kScan + kFlags + kBars + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // TMEM columns
+  static constexpr int kO = 0;                  // O of block q at q * D
+  static constexpr int kS = 256;                // S of block q, buffer s at kS + (q + s) * T
+};
+
+struct PromptParams {
+  const uint16_t* q;
+  const uint8_t* kc;
+  const uint16_t* ks;
+  const uint8_t* vc;
+  const uint16_t* vs;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  const uint16_t* wq;      // [channel][sample], rows in word_channel order
+  const uint16_t* wo;      // [sample][channel], columns in word_channel order
+  const uint4* wof;        // the same as fragments, natural order
+  uint16_t* out;
+  float* part;
+  int4* desc;              // [CTA]: the cut unit that starts in it (request, row block, head, partials | slot << 16), 0: none
+  long long q_ts, q_hs, table_stride;
+  float qfac, ofac;
+  int B, n_q, Hq, Hkv, Gq, max_q, max_kv, num_pages, page_shift, window, min_tiles;
+};
+
+__device__ __forceinline__ uint32_t ph2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 pu2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ float ppow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// (a & mask) ^ x where x lies within mask or in bits that are zero in mask
+__device__ __forceinline__ uint32_t mask_xor(uint32_t a, uint32_t mask, uint32_t x) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(mask), "r"(x));
+  return d;
+}
+// The exponent e with mx 2^-e in [2^9, 2^10), 0 for mx = 0.
+__device__ __forceinline__ int row_exp(float mx) {
+  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 9;
+  return mx > 0.0f ? min(max(e, -100), 100) : 0;
+}
+
+// ---------------------------------------------------------------- the line of tiles
+template <int R, int T>
+struct PrRequest {
+  int qs, qn, kv, rows, nrt;
+  __device__ __forceinline__ void load(const PromptParams& p, int b) {
+    qs = b;
+    qn = 1;
+    if (p.q_starts) {
+      qs = min(max(__ldg(p.q_starts + b), 0), p.n_q);
+      qn = min(max(__ldg(p.q_starts + b + 1), qs), p.n_q) - qs;
+    }
+    kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+    rows = min(qn, p.max_q) * p.Gq;
+    nrt = (rows + R - 1) / R;
+  }
+  // tokens [lo, hi) that some row of block rt attends, its first tile and its tiles (at least one)
+  __device__ __forceinline__ void span(const PromptParams& p, int rt, int& lo, int& hi, int& tile0, int& nt) const {
+    const int first = rt * R / p.Gq, last = (min((rt + 1) * R, rows) - 1) / p.Gq;
+    hi = min(max(kv - qn + last + 1, 0), kv);
+    lo = p.window ? (int)min((long long)hi, max((long long)kv - qn + first + 1 - p.window, 0ll)) : 0;
+    tile0 = lo / T;
+    nt = max(1, (hi + T - 1) / T - tile0);
+  }
+};
+
+// A CTA's piece [at, end) of the line, walked segment by segment.
+template <int R, int T>
+struct PrWalk {
+  long long at, end, base;  // base: the place of block (b, rt)'s first tile
+  int b, rt;
+  PrRequest<R, T> r;
+  int lo, hi, tile0, nt;    // of block (b, rt)
+  int h, i0, i1;            // the segment: head h, tiles [i0, i1) of the unit
+
+  __device__ __forceinline__ void start(const PromptParams& p, int b_, long long base_) {
+    b = b_;
+    base = base_;
+    rt = 0;
+    r.load(p, b);
+    if (r.nrt) r.span(p, 0, lo, hi, tile0, nt);
+  }
+  __device__ __forceinline__ bool next(const PromptParams& p) {
+    if (at >= end) return false;
+    while (rt >= r.nrt || at >= base + (long long)p.Hkv * nt) {
+      if (rt < r.nrt) {
+        base += (long long)p.Hkv * nt;
+        ++rt;
+      }
+      while (rt >= r.nrt) {
+        r.load(p, ++b);
+        rt = 0;
+      }
+      r.span(p, rt, lo, hi, tile0, nt);
+    }
+    const long long off = at - base;
+    h = (int)(off / nt);
+    i0 = (int)(off - (long long)h * nt);
+    i1 = (int)min((long long)nt, i0 + (end - at));
+    at += i1 - i0;
+    return true;
+  }
+};
+
+// Sets the CTA's piece and where it starts; false when it is empty. `tot` holds kPrThreads values.
+template <int R, int T>
+__device__ __forceinline__ bool find_piece(const PromptParams& p, long long* tot, PrWalk<R, T>& w, long long& per) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ long long part[kPrWarps + 1];
+  __shared__ long long found[2];
+  long long total = 0, upto = 0, mine = 0;
+  // the tiles of requests b0 .. b0 + kPrThreads - 1, a warp per request, then a scan over the block
+  auto scan = [&](int b0, long long& sum) {
+    for (int x = warp; x < kPrThreads; x += kPrWarps) {
+      long long n = 0;
+      if (b0 + x < p.B) {
+        PrRequest<R, T> r;
+        r.load(p, b0 + x);
+        for (int rt = lane; rt < r.nrt; rt += 32) {
+          int lo, hi, t0, nt;
+          r.span(p, rt, lo, hi, t0, nt);
+          n += nt;
+        }
+        if (r.nrt > 1) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
+        }
+      } else if (b0 + x >= p.B + kPrWarps) {
+        break;
+      }
+      if (lane == 0) tot[x] = n * p.Hkv;
+    }
+    __syncthreads();
+    mine = b0 + tid < p.B ? tot[tid] : 0;
+    long long v = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int x = 0; x < kPrWarps; ++x) {
+      if (x < warp) v += part[x];
+      sum += part[x];
+    }
+    __syncthreads();
+    return v;
+  };
+  for (int b0 = 0; b0 < p.B; b0 += kPrThreads) {
+    long long sum;
+    upto = total + scan(b0, sum);
+    total += sum;
+  }
+  per = max((long long)p.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+  w.at = min(total, per * blockIdx.x);
+  w.end = min(total, w.at + per);
+  if (w.at >= w.end) return false;
+  if (p.B <= kPrThreads) {
+    if (mine && w.at >= upto - mine && w.at < upto) {
+      found[0] = upto - mine;
+      found[1] = tid;
+    }
+  } else {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.B && before <= w.at; b0 += kPrThreads) {
+      long long sum;
+      upto = before + scan(b0, sum);
+      if (mine && w.at >= upto - mine && w.at < upto) {
+        found[0] = upto - mine;
+        found[1] = b0 + tid;
+      }
+      before += sum;
+    }
+  }
+  __syncthreads();
+  w.start(p, (int)found[1], found[0]);
+  return true;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, int G, int BITS>
+__global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __grid_constant__ PromptParams p) {
+  using C = PrCfg<D, G, BITS>;
+  constexpr int NQ = C::NQ, SB = C::SB, R = C::R, T = C::T, ND = C::ND, NW = C::NW, NJ = C::NJ;
+  constexpr int NG = D / G, RB = D * BITS / 8;
+  constexpr int kBlkQ = 128 * 128, kBlkT = T * 128;  // bytes of a 64-channel block of Q, of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + C::kQ;
+  uint8_t* sV = sK + 2 * C::kTile;
+  long long* scan = reinterpret_cast<long long*>(sV + 2 * C::kTile);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(scan) + C::kScan);  // [ring][5]
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(flags) + C::kFlags);
+  uint64_t* kempty = kfull + 2;
+  uint64_t* vfull = kempty + 2;
+  uint64_t* vempty = vfull + 2;
+  uint64_t* aready = vempty + 2;  // [NQ] an A operand (raw query, q~, o) is in sQ
+  uint64_t* sfull = aready + 2;   // [block or buffer] S (or a rotation's result) is in TMEM
+  uint64_t* pfull = sfull + 2;    // [block or buffer] P is in TMEM
+  uint64_t* odone = pfull + 2;    // [NQ] a P V product has been added
+  uint64_t* mdone = odone + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&kfull[s], ND);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], ND);
+      mbar_init(&vempty[s], 1);
+      mbar_init(&aready[s], 4);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&pfull[s], 4);
+      mbar_init(&odone[s], 1);
+    }
+    mbar_init(mdone, 1);
+    fence_mbarrier_init();
+  }
+  for (int x = tid; x < kFlagRing * 5; x += kPrThreads) flags[x] = 0;
+  grid_dep_launch();
+  if (warp == kPrWarps - 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();  // lengths, table, pages, queries and the workspace may come from the kernel before
+  PrWalk<R, T> w;
+  long long per;
+  const bool any = find_piece<R, T>(p, scan, w, per);
+  if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  bool ok = true;  // false after a wait ran out: the role goes through its loops without work
+
+  if (any && warp < 4 * NQ) {
+    // ------------------------------------------------------------ softmax: a thread per query row
+    const int qb = NQ == 2 ? warp >> 2 : 0;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = tl + C::kO + qb * D;
+    const uint32_t trot = D == 128 ? tl + C::kS + qb * T : tl + C::kO;
+    uint8_t* q_row = sQ + qb * (128 * D * 2) + row * 128;
+    auto q_unit = [&](int u) {  // 16-byte unit u of this row
+      return reinterpret_cast<uint4*>(q_row + (u >> 3) * kBlkQ + (((u & 7) ^ (row & 7)) << 4));
+    };
+    uint32_t ns[2] = {0, 0}, no = 0;  // phases of sfull, odone so far
+    int kt = 0;                       // tiles so far (the flags' ring)
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, ph))) {
+        if (lane == 0) atomicOr(&g_prompt_err, kErrTimeoutLoad);
+        ok = false;
+      }
+      tc_fence_after();
+    };
+    auto announce = [&](uint64_t* bar) {  // this warp's part of an operand in shared memory is written
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    while (w.next(p)) {
+      const int n = w.i1 - w.i0;
+      if (w.r.rows - w.rt * R <= 128 * qb) {  // no rows for this block
+        kt += n;
+        continue;
+      }
+      const int y = w.rt * R + qb * 128 + row;
+      const bool valid = y < w.r.rows;
+      const int tok = y / p.Gq, head = w.h * p.Gq + (y - tok * p.Gq);
+      // ---- the raw query
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(w.r.qs + tok) * p.q_ts + (long long)head * p.q_hs);
+#pragma unroll 8
+        for (int u = 0; u < D / 8; ++u) *q_unit(u) = valid ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+      }
+      announce(&aready[qb]);
+      // ---- q~, normalised by a power of two per row
+      const int s0 = NQ == 2 ? qb : 0;
+      wait(&sfull[s0], ns[s0]++ & 1);
+      float fac;
+      {
+        float mx = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(trot + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, fabsf(v[k]));
+        }
+        const int ex = row_exp(mx);
+        const float f = ppow2(-ex);
+        fac = p.qfac * ppow2(ex);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(trot + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *q_unit(c / 8 + k) = make_uint4(pack_half2(v[8 * k] * f, v[8 * k + 1] * f), pack_half2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                                            pack_half2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack_half2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+        }
+      }
+      announce(&aready[qb]);
+      // what this row attends: tokens in (lo, hi]; all rows of the warp attend those in (wlo, whi]
+      const int hi = valid ? w.r.kv - w.r.qn + tok : 0x7fffffff;
+      const int lo = valid && p.window ? (int)max((long long)hi - p.window, -1ll) : -1;
+      const int whi = __reduce_min_sync(0xffffffffu, hi), wlo = __reduce_max_sync(0xffffffffu, lo);
+      float m_run = -INFINITY, l_run = 0.0f;
+      int ve = 0;          // O is held divided by 2^ve
+      bool row_nan = false;
+      for (int i = 0; i < n; ++i, ++kt) {
+        const int idx = NQ == 2 ? qb : (i & 1);
+        const uint32_t ts = tl + C::kS + idx * T;
+        wait(&sfull[idx], ns[idx]++ & 1);
+        if (!ok) continue;
+        const int t0 = (w.tile0 + w.i0 + i) * T;
+        const bool cut = t0 + T - 1 > whi || t0 <= wlo;
+        volatile uint32_t* fl = flags + (kt % kFlagRing) * 5;
+        const uint32_t flag = fl[0];
+        const float f = (flag & 1) ? fac * 256.0f : fac;
+        auto masked = [&](int t, float v) { return t > hi || t <= lo ? -INFINITY : v; };
+        // the row's maximum
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < T; c += 32) {
+          float v[32];
+          tmem_ld32(ts + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+        }
+        mx *= f;
+        // the product before this tile's: every phase of odone is waited for, or a parity could
+        // stand for the phase before (with one S buffer, S of this tile came after that product)
+        if (SB == 2 && i > 0) wait(&odone[qb], (no + i - 1) & 1);
+        const int nve = (flag & 2) ? 8 : ve;
+        constexpr float kSlack = 8.0f;
+        if (__any_sync(0xffffffffu, mx > m_run + kSlack) || nve != ve) {
+          const float m = fmaxf(m_run, mx);
+          float g = m == m_run ? 1.0f : ex2_approx(m_run - m);
+          l_run *= g;
+          if (i > 0) {
+            if (nve != ve) g *= 1.0f / 256.0f;
+            if (SB == 1) wait(&odone[qb], (no + i - 1) & 1);
+            if (!ok) continue;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tmem_ld32(to + c, v);
+              tmem_ld_wait();
+              tmem_regs_fence(v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= g;
+              tmem_st32(to + c, v);
+            }
+          }
+          m_run = m;
+          ve = nve;
+        }
+        if (flag & 4) {  // some V scales of the tile are not finite
+          for (int t = 0; t < T; ++t)
+            if (((fl[1 + (t >> 5)] >> (t & 31)) & 1) && t0 + t <= hi && t0 + t > lo) row_nan = true;
+        }
+        // P
+        const float ms = m_run == -INFINITY ? 0.0f : m_run;
+        float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < T; c += 32) {
+          float v[32];
+          tmem_ld32(ts + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
+          }
+          uint32_t h[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float a = ex2_approx(fmaf(v[2 * k], f, -ms)), b = ex2_approx(fmaf(v[2 * k + 1], f, -ms));
+            l0 += a;
+            l1 += b;
+            h[k] = pack_half2(a, b);
+          }
+          tmem_st16(ts + c / 2, h);
+        }
+        l_run += l0 + l1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[idx]);
+      }
+      wait(&odone[qb], (no + n - 1) & 1);
+      no += n;
+      if (row_nan) l_run = __int_as_float(0x7fc00000);
+      if (w.i0 == 0 && w.i1 == w.nt) {
+        // ---- out = Wo (o / l), o normalised like q~
+        const float inv = l_run > 0.0f || l_run != l_run ? 1.0f / l_run : 0.0f;  // nothing attended: zeros (NaN stays)
+        float mx = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(to + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, fabsf(v[k]));
+        }
+        const int ex = row_exp(mx * inv);
+        const float f = inv * ppow2(-ex);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(to + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *q_unit(c / 8 + k) = make_uint4(pack_half2(v[8 * k] * f, v[8 * k + 1] * f), pack_half2(v[8 * k + 2] * f, v[8 * k + 3] * f),
+                                            pack_half2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack_half2(v[8 * k + 6] * f, v[8 * k + 7] * f));
+        }
+        announce(&aready[qb]);
+        wait(&sfull[s0], ns[s0]++ & 1);
+        const float of = p.ofac * ppow2(ex) * ppow2(ve);
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)(w.r.qs + tok) * p.Hq + head) * D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(trot + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+          if (valid && ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[c / 8 + k] = make_uint4(pack_half2(v[8 * k] * of, v[8 * k + 1] * of), pack_half2(v[8 * k + 2] * of, v[8 * k + 3] * of),
+                                          pack_half2(v[8 * k + 4] * of, v[8 * k + 5] * of), pack_half2(v[8 * k + 6] * of, v[8 * k + 7] * of));
+          }
+        }
+      } else {
+        // ---- a partial of a unit that other CTAs share: [m][l][4 channels][row]
+        const long long u0 = w.base + (long long)w.h * w.nt;
+        const long long x0 = (long long)blockIdx.x * per;
+        float* dst = p.part + (2 * (long long)blockIdx.x + (x0 >= u0 ? 0 : 1)) * kPrPart;
+        const int pr = qb * 128 + row;
+        dst[pr] = m_run;
+        dst[R + pr] = l_run;
+        const float vf = ppow2(ve);
+        float4* od = reinterpret_cast<float4*>(dst + 2 * R) + pr;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float v[32];
+          tmem_ld32(to + c, v);
+          tmem_ld_wait();
+          tmem_regs_fence(v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            od[(size_t)(c / 4 + k) * R] = make_float4(v[4 * k] * vf, v[4 * k + 1] * vf, v[4 * k + 2] * vf, v[4 * k + 3] * vf);
+        }
+        const long long xa = u0 / per, xb = (u0 + w.nt - 1) / per;
+        if (tid == 0 && xa == blockIdx.x) p.desc[blockIdx.x] = make_int4(w.b, w.rt, w.h, (int)(xb - xa + 1) | (x0 >= u0 ? 0 : 1 << 16));
+      }
+    }
+  } else if (any && warp < kPrWarps - 1) {
+    // ------------------------------------------------------------ dequantisers
+    const int dw = warp - 4 * NQ, dtid = dw * 32 + lane;
+    const int P1 = (1 << p.page_shift) - 1;
+    int kc = 0, vc = 0, kt = 0;  // ring tiles so far (K with the matrices, V), tiles so far
+    auto wait = [&](uint64_t* bar, int count) {  // until ring tile `count` may be written
+      if (count >= 2 && ok && !__all_sync(0xffffffffu, mbar_wait_bounded(&bar[count & 1], ((count >> 1) - 1) & 1))) {
+        if (lane == 0) atomicOr(&g_prompt_err, kErrTimeoutLoad);
+        ok = false;
+      }
+    };
+    auto announce = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto matrix = [&](const uint16_t* m) {  // a rotation matrix [D][D] through the K ring
+#pragma unroll 1
+      for (int t = 0; t < NW; ++t, ++kc) {
+        wait(kempty, kc);
+        uint8_t* dst = sK + (kc & 1) * C::kTile;
+        const uint4* src = reinterpret_cast<const uint4*>(m + (size_t)t * T * D);
+#pragma unroll 8
+        for (int x = dtid; x < T * (D / 8); x += ND * 32) {
+          const int r = x / (D / 8), u = x - r * (D / 8);
+          *reinterpret_cast<uint4*>(dst + (u >> 3) * kBlkT + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = __ldg(src + x);
+        }
+        announce(&kfull[kc & 1]);
+      }
+    };
+    // item j of this thread: row it_row(j) of a tile, 32 channels from 32 it_chunk(j)
+    auto it_row = [&](int j) { return ((dw + ND * j) % (T / 8)) * 8 + (lane & 7); };
+    auto it_chunk = [&](int j) { return ((dw + ND * j) / (T / 8)) * 4 + (lane >> 3); };
+    struct Item {
+      uint32_t c[C::CW];
+      uint32_t s;  // the item's scale (G = 32) or two scales
+    };
+    // item j's codes as fp16 into a tile
+    auto convert = [&](uint8_t* tile, int j, const Item& it, bool big) {
+      const int r = it_row(j), ch = it_chunk(j);
+      uint8_t* dst = tile + (ch >> 1) * kBlkT + r * 128;
+      __half2 s0 = pu2h(prmt(it.s, it.s, 0x1010)), s1 = G == 32 ? s0 : pu2h(prmt(it.s, it.s, 0x3232));
+      if (big) {
+        const __half2 d = __half2half2(__ushort_as_half((unsigned short)0x1c00));  // 2^-8
+        s0 = __hmul2(s0, d);
+        s1 = __hmul2(s1, d);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __half2 s = k < 2 ? s0 : s1;
+        uint4 o;
+        if constexpr (BITS == 4) {
+          const uint32_t x = it.c[k], x8 = x >> 8;
+          const __half2 o1 = pu2h(0x64086408u), o16 = pu2h(0xD480D480u), i16 = pu2h(0x2C002C00u);  // 1032, -72, 1/16
+          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x, 0x000F000Fu, 0x64086408u)), o1), s));
+          o.y = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x, 0x00F000F0u, 0x64806480u)), i16, o16), s));
+          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x8, 0x000F000Fu, 0x64086408u)), o1), s));
+          o.w = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x8, 0x00F000F0u, 0x64806480u)), i16, o16), s));
+        } else {
+          const __half2 o1 = pu2h(0x64806480u);  // 1152
+          const uint32_t a = it.c[2 * k], b = it.c[2 * k + 1];
+          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a, 0x00FF00FFu, 0x64806480u)), o1), s));
+          o.y = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a >> 8, 0x00FF00FFu, 0x64806480u)), o1), s));
+          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b, 0x00FF00FFu, 0x64806480u)), o1), s));
+          o.w = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b >> 8, 0x00FF00FFu, 0x64806480u)), o1), s));
+        }
+        *reinterpret_cast<uint4*>(dst + ((((ch & 1) * 4 + k) ^ (r & 7)) << 4)) = o;
+      }
+    };
+    while (w.next(p)) {
+      const int n = w.i1 - w.i0;
+      matrix(p.wq);
+      const int32_t* trow = p.table + (long long)w.b * p.table_stride;
+      const int t_first = (w.tile0 + w.i0) * T;
+      const int t_hi = w.hi, t_lo = w.lo;
+      // the cache row of item j in tile i, -1: no token that the unit attends
+      auto entry = [&](int i, int j) {
+        const int t = t_first + i * T + it_row(j);
+        return i < n && t >= t_lo && t < t_hi ? __ldg(trow + (t >> p.page_shift)) : -1;
+      };
+      auto cache_row = [&](int i, int j, int e) -> long long {
+        const int t = t_first + i * T + it_row(j);
+        if (!(i < n && t >= t_lo && t < t_hi)) return -1;
+        if (e < 0 || e >= p.num_pages) {
+          atomicOr(&g_prompt_err, kErrBadPage);
+          e = 0;
+        }
+        return (((long long)e * p.Hkv + w.h) << p.page_shift) + (t & P1);
+      };
+      auto load_codes = [&](const uint8_t* base, long long r, int j, Item& it) {
+        const uint4* src = reinterpret_cast<const uint4*>(base + r * RB + it_chunk(j) * (4 * BITS));
+#pragma unroll
+        for (int x = 0; x < C::CW / 4; ++x) {
+          const uint4 v = r >= 0 ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+          it.c[4 * x] = v.x;
+          it.c[4 * x + 1] = v.y;
+          it.c[4 * x + 2] = v.z;
+          it.c[4 * x + 3] = v.w;
+        }
+      };
+      auto load_scale = [&](const uint16_t* base, long long r, int j, Item& it) {
+        const uint16_t* src = base + r * NG + it_chunk(j) * (32 / G);
+        it.s = r < 0 ? 0u : G == 32 ? (uint32_t)__ldg(src) : __ldg(reinterpret_cast<const uint32_t*>(src));
+      };
+      Item k[NJ], v[NJ];
+      long long rows[NJ];   // of the next tile
+      int ent[NJ];          // table entries of the tile after it
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        rows[j] = cache_row(0, j, entry(0, j));
+        load_codes(p.kc, rows[j], j, k[j]);
+        load_scale(p.ks, rows[j], j, k[j]);
+        load_scale(p.vs, rows[j], j, v[j]);
+        load_codes(p.vc, rows[j], j, v[j]);
+        ent[j] = entry(1, j);
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        rows[j] = cache_row(1, j, ent[j]);
+        ent[j] = entry(2, j);
+      }
+      for (int i = 0; i < n; ++i, ++kt, ++kc, ++vc) {
+        // ---- scales that need care: bit 0 large K, bit 1 large V, bit 2 V not finite
+        uint32_t* fl = flags + (kt % kFlagRing) * 5;
+        {
+          constexpr uint32_t kBig = BITS == 4 ? 0x6C00u : 0x6000u;  // 2^12, 2^9
+          uint32_t kx = 0, vx = 0;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const uint32_t a = k[j].s & 0x7FFF7FFFu, b = v[j].s & 0x7FFF7FFFu;
+            kx = max(kx, max(a & 0xFFFFu, a >> 16));
+            vx = max(vx, max(b & 0xFFFFu, b >> 16));
+          }
+          if (max(kx, vx) >= kBig) {
+            if (vx >= 0x7C00u) {
+#pragma unroll
+              for (int j = 0; j < NJ; ++j) {
+                if ((v[j].s & 0x7C00u) == 0x7C00u || (v[j].s & 0x7C000000u) == 0x7C000000u) {
+                  v[j].s = 0;
+                  atomicOr(&fl[1 + (it_row(j) >> 5)], 1u << (it_row(j) & 31));
+                }
+              }
+            }
+            atomicOr(&fl[0], (kx >= kBig ? 1u : 0u) | (vx >= kBig ? 2u : 0u) | (vx >= 0x7C00u ? 4u : 0u));
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(ND * 32) : "memory");
+        const uint32_t flag = *reinterpret_cast<volatile uint32_t*>(fl);
+        if (dtid < 5) flags[((kt + kFlagRing / 2) % kFlagRing) * 5 + dtid] = 0;  // last read four tiles ago
+        // ---- K
+        wait(kempty, kc);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) convert(sK + (kc & 1) * C::kTile, j, k[j], flag & 1);
+        announce(&kfull[kc & 1]);
+        uint32_t vsc[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          vsc[j] = v[j].s;
+          load_codes(p.kc, rows[j], j, k[j]);
+          load_scale(p.ks, rows[j], j, k[j]);
+          load_scale(p.vs, rows[j], j, v[j]);
+        }
+        // ---- V
+        wait(vempty, vc);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          Item it = v[j];
+          it.s = vsc[j];
+          convert(sV + (vc & 1) * C::kTile, j, it, flag & 2);
+        }
+        announce(&vfull[vc & 1]);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          load_codes(p.vc, rows[j], j, v[j]);
+          rows[j] = cache_row(i + 2, j, ent[j]);
+          ent[j] = entry(i + 3, j);
+        }
+      }
+      if (w.i0 == 0 && w.i1 == w.nt) matrix(p.wo);
+    }
+  } else if (any && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id_s = umma_idesc_f16(128, T), id_o = umma_idesc_f16(128, D) | kUmmaTransposeB;
+    int kc = 0, vc = 0;
+    uint32_t na[2] = {0, 0}, np[2] = {0, 0};
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      if (ok && !mbar_wait_bounded(bar, ph)) {
+        atomicOr(&g_prompt_err, kErrTimeoutLoad);
+        ok = false;
+      }
+      tc_fence_after();
+      return ok;
+    };
+    // columns d (+)= A block q of sQ times the K ring's tile
+    auto product = [&](uint32_t d, int q, int slot) {
+      const uint32_t a = smem_u32(sQ + q * (128 * D * 2)), b = smem_u32(sK + slot * C::kTile);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_f16(d, umma_desc_sw128(a + (ks >> 2) * kBlkQ + (ks & 3) * 32), umma_desc_sw128(b + (ks >> 2) * kBlkT + (ks & 3) * 32),
+                 id_s, ks > 0);
+    };
+    while (w.next(p)) {
+      const int n = w.i1 - w.i0;
+      const int nq = NQ == 2 && w.r.rows - w.rt * R > 128 ? 2 : 1;
+      auto rotate = [&]() {  // the A operands times a rotation matrix
+        for (int q = 0; q < nq; ++q) wait(&aready[q], na[q]++ & 1);
+        for (int t = 0; t < NW; ++t, ++kc) {
+          if (wait(&kfull[kc & 1], (kc >> 1) & 1)) {
+            for (int q = 0; q < nq; ++q) product(tmem + (D == 128 ? C::kS + q * T : C::kO + t * T), q, kc & 1);
+            umma_commit(&kempty[kc & 1]);
+          }
+        }
+        if (ok)
+          for (int q = 0; q < nq; ++q) umma_commit(&sfull[NQ == 2 ? q : 0]);
+      };
+      rotate();
+      for (int q = 0; q < nq; ++q) wait(&aready[q], na[q]++ & 1);
+      for (int s = 0; s < SB && s < n; ++s, ++kc) {
+        if (!wait(&kfull[kc & 1], (kc >> 1) & 1)) continue;
+        for (int q = 0; q < nq; ++q) {
+          product(tmem + C::kS + (NQ == 2 ? q : s) * T, q, kc & 1);
+          umma_commit(&sfull[NQ == 2 ? q : s]);
+        }
+        umma_commit(&kempty[kc & 1]);
+      }
+      for (int i = 0; i < n; ++i, ++vc) {
+        const bool more = i + SB < n;
+        wait(&vfull[vc & 1], (vc >> 1) & 1);
+        const uint32_t vb = smem_u32(sV + (vc & 1) * C::kTile);
+        for (int q = 0; q < nq; ++q) {
+          const int idx = NQ == 2 ? q : (i & 1);
+          const uint32_t ts = tmem + C::kS + idx * T;
+          if (wait(&pfull[idx], np[idx]++ & 1)) {
+#pragma unroll
+            for (int kk = 0; kk < T / 16; ++kk)
+              umma_f16_ts(tmem + C::kO + q * D, ts + 8 * kk, umma_desc_mn_sw128(vb + kk * 2048, kBlkT), id_o, i > 0 || kk > 0);
+            umma_commit(&odone[q]);
+          }
+          if (more) {
+            if (q == 0) wait(&kfull[kc & 1], (kc >> 1) & 1);
+            if (ok) {
+              product(ts, q, kc & 1);
+              umma_commit(&sfull[idx]);
+            }
+          }
+        }
+        if (ok) umma_commit(&vempty[vc & 1]);
+        if (more) {
+          if (ok) umma_commit(&kempty[kc & 1]);
+          ++kc;
+        }
+      }
+      if (w.i0 == 0 && w.i1 == w.nt) rotate();
+    }
+    umma_commit(mdone);
+    if (!mbar_wait_bounded(mdone, 0)) atomicOr(&g_prompt_err, kErrTimeoutLoad);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kPrWarps - 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- the join
+// Block (x, y): rows 8y .. 8y + 7 of the cut unit whose first CTA is x: the partials in CTA
+// order, then out = Wo (o / l) with o as an fp16 hi + lo pair. Reading the partials bounds it.
+constexpr int kJoinWarps = 4;
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __grid_constant__ PromptParams p) {
+  constexpr int R = 32768 / D, T = D == 128 ? 128 : 64, MT = D / 16, ST = D + 4;
+  __shared__ __align__(16) float om[8 * ST];
+  __shared__ __align__(16) __half ob[8 * (D + 8)];
+  __shared__ float ml[2][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int4 u = __ldcg(p.desc + blockIdx.x);
+  if (u.w == 0) return;
+  PrRequest<R, T> r;
+  r.load(p, u.x);
+  const int r0 = 8 * (int)blockIdx.y, nrows = min(8, min(R, r.rows - u.y * R) - r0);
+  if (nrows <= 0) return;
+  // the unit's first CTA holds it in slot 1 unless the unit starts its piece; the others in slot 0
+  const float* first = p.part + (2 * (long long)blockIdx.x) * kPrPart;
+  const int np = u.w & 0xFFFF, first_slot = u.w >> 16;
+  auto slot = [&](int k) { return k == 0 ? first + first_slot * kPrPart : first + 2 * (long long)k * kPrPart; };
+  if (tid < 8) {
+    float M = -INFINITY, L = 0.0f;
+    for (int k = 0; k < np; ++k) M = fmaxf(M, __ldcg(slot(k) + r0 + tid));
+    for (int k = 0; k < np; ++k) {
+      const float m = __ldcg(slot(k) + r0 + tid), l = __ldcg(slot(k) + R + r0 + tid);
+      if (m != -INFINITY) L = fmaf(l, ex2_approx(m - M), L);
+      else L += l;  // 0, or NaN for a row that attends a value that is no number
+    }
+    ml[0][tid] = M;
+    ml[1][tid] = L;
+  }
+  __syncthreads();
+  for (int x = tid; x < 8 * (D / 4); x += kJoinWarps * 32) {
+    const int row = x & 7, k4 = x >> 3;
+    const float M = ml[0][row];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += 4) {
+      float4 v[4];
+      float m[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k < np) {
+          m[k] = __ldcg(slot(k0 + k) + r0 + row);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(slot(k0 + k) + 2 * R) + (size_t)k4 * R + r0 + row);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k < np && m[k] != -INFINITY) {
+          const float f = ex2_approx(m[k] - M);
+          acc.x = fmaf(f, v[k].x, acc.x);
+          acc.y = fmaf(f, v[k].y, acc.y);
+          acc.z = fmaf(f, v[k].z, acc.z);
+          acc.w = fmaf(f, v[k].w, acc.w);
+        }
+      }
+    }
+    float* o = om + row * ST;
+    o[word_channel(4 * k4, BITS)] = acc.x;
+    o[word_channel(4 * k4 + 1, BITS)] = acc.y;
+    o[word_channel(4 * k4 + 2, BITS)] = acc.z;
+    o[word_channel(4 * k4 + 3, BITS)] = acc.w;
+  }
+  __syncthreads();
+  const int g = lane >> 2, c = lane & 3;
+  const float L = ml[1][g];
+  const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;
+  const float* orow = om + g * ST;
+  float mx = 0.0f;
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) {
+    const float4 v = *reinterpret_cast<const float4*>(orow + 16 * x + 4 * c);
+    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+  }
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int ex = row_exp(mx * inv);
+  const float f = inv * ppow2(-ex);
+  float acc[MT / kJoinWarps][4] = {};
+#pragma unroll
+  for (int ks = 0; ks < MT; ++ks) {
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
+      const __half2 hv = __floats2half2_rn(v.x * f, v.y * f);
+      const float2 hf = __half22float2(hv);
+      bh[e] = ph2u(hv);
+      bl[e] = pack_half2(v.x * f - hf.x, v.y * f - hf.y);
+    }
+#pragma unroll
+    for (int t = 0; t < MT / kJoinWarps; ++t) {
+      const uint4 a = __ldg(p.wof + ((warp + kJoinWarps * t) * MT + ks) * 32 + lane);
+      mma_16816(acc[t], a.x, a.y, a.z, a.w, bh[0], bh[1]);
+      mma_16816(acc[t], a.x, a.y, a.z, a.w, bl[0], bl[1]);
+    }
+  }
+  float fo[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) fo[e] = p.ofac * ppow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+#pragma unroll
+  for (int t = 0; t < MT / kJoinWarps; ++t) {
+    __half* x0 = ob + (2 * c) * (D + 8) + 16 * (warp + kJoinWarps * t) + g;
+    x0[0] = __float2half_rn(acc[t][0] * fo[0]);
+    x0[D + 8] = __float2half_rn(acc[t][1] * fo[1]);
+    x0[8] = __float2half_rn(acc[t][2] * fo[0]);
+    x0[D + 8 + 8] = __float2half_rn(acc[t][3] * fo[1]);
+  }
+  __syncthreads();
+  for (int x = tid; x < nrows * (D / 8); x += kJoinWarps * 32) {
+    const int row = x / (D / 8), k = x - row * (D / 8);
+    const int y = u.y * R + r0 + row, tok = y / p.Gq, head = u.z * p.Gq + (y - tok * p.Gq);
+    *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
+        *reinterpret_cast<const uint4*>(ob + row * (D + 8) + 8 * k);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+template <int D, int G, int BITS>
+kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
+  using C = PrCfg<D, G, BITS>;
+  PromptParams p{};
+  p.q = a.q;
+  p.kc = a.kc;
+  p.ks = a.ks;
+  p.vc = a.vc;
+  p.vs = a.vs;
+  p.table = a.table;
+  p.kv_lens = a.kv_lens;
+  p.q_starts = a.q_starts;
+  p.wq = a.pk->wq_dev;
+  p.wo = a.pv->wo_dev;
+  p.wof = a.pv->wof_dev;
+  p.out = a.out;
+  p.part = reinterpret_cast<float*>(part);
+  p.desc = reinterpret_cast<int4*>(p.part + (size_t)2 * kPrMaxCtas * kPrPart);
+  p.q_ts = a.q_token_stride;
+  p.q_hs = a.q_head_stride;
+  p.table_stride = a.table_stride;
+  const float sigma = a.sigma > 0.0f ? a.sigma : 1.0f / sqrtf((float)D);
+  p.qfac = sigma * 1.4426950408889634f * a.pk->wq_scale;
+  p.ofac = a.pv->wo_scale;
+  p.B = a.B;
+  p.n_q = a.n_q;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.Gq = a.Hq / a.Hkv;
+  p.max_q = a.max_q_len;
+  p.max_kv = (int)std::min<long long>(a.max_kv_len, (long long)a.max_pages << a.page_shift);
+  p.num_pages = a.num_pages;
+  p.page_shift = a.page_shift;
+  p.window = a.window;
+  p.min_tiles = 2;
+  const long long blocks = ((long long)std::min(a.max_q_len, a.n_q) * p.Gq + C::R - 1) / C::R;
+  const long long most = (long long)a.B * a.Hkv * blocks * std::max(1, (p.max_kv + C::T - 1) / C::T);
+  const int sms = std::min(kPrMaxCtas, num_sms(a.pk->device));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(sms, (most + p.min_tiles - 1) / p.min_tiles));
+  cfg.blockDim = dim3(kPrThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = strm;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = allow_smem<attend_prompt_kernel<D, G, BITS>>(a.pk->device, C::kSmem);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_prompt_kernel<D, G, BITS>, p);
+  if (e == cudaSuccess) {
+    const int rows = std::min<long long>(C::R, (long long)std::min(a.max_q_len, a.n_q) * p.Gq);
+    cfg.gridDim.y = (unsigned)((rows + 7) / 8);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, join_prompt_kernel<D, BITS>, p);
+  }
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("attend_paged launch: ") + cudaGetErrorString(e));
+  return KVQ_OK;
+}
+
+}  // namespace
+
+size_t prompt_part_bytes() {
+  return (size_t)2 * kPrMaxCtas * kPrPart * 4 + kPrMaxCtas * sizeof(int4);
+}
+
+kvq_status launch_attend_prompt(const PagedAttendHost& a, void* part, cudaStream_t s) {
+  return dispatch_dgb(a.pk->D, a.pk->G, a.pk->bits, [&](auto d, auto g, auto b) {
+    return run_prompt<decltype(d)::value, decltype(g)::value, decltype(b)::value>(a, part, s);
+  });
+}
+
+uint32_t prompt_error_flags(bool clear) {
+  uint32_t v = 0;
+  cudaMemcpyFromSymbol(&v, g_prompt_err, sizeof(v));
+  if (clear && v) {
+    const uint32_t z = 0;
+    cudaMemcpyToSymbol(g_prompt_err, &z, sizeof(z));
+  }
+  return v;
+}
+
+}  // namespace kvq

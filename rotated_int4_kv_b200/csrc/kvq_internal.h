@@ -51,8 +51,9 @@ struct kvq_plan {
   const uint16_t* wdec_dev = nullptr;
   // Paged-attention operands in the same block, fp16 times a power of two (one rounding per
   // entry, the largest entry in [1, 2)): Lambda^-1 Q diag(s) (query rotation) and
-  // diag(s) Q^T Lambda^-1 (output un-rotation), each as row-major [D][D] and in the order of
-  // mma.m16n8k16 A fragments (16 bytes per (16-row tile, K step, lane)).
+  // diag(s) Q^T Lambda^-1 (output un-rotation), each as row-major [D][D] with the channels in
+  // the order of word_channel, and in natural order as mma.m16n8k16 A fragments (16 bytes per
+  // (16-row tile, K step, lane)).
   const uint16_t* wq_dev = nullptr;
   const uint16_t* wo_dev = nullptr;
   const uint4* wqf_dev = nullptr;
@@ -98,6 +99,12 @@ kvq_status encode_tiled_new(CUtensorMap* map, CUtensorMapDataType dt, int rank, 
 int num_sms(int device);
 
 kvq_status check_plan_device(const kvq_plan* p);
+
+// The channel at place p of a row when every 32-bit word of its codes is converted to fp16
+// pairs by masks: int4 pairs (0, 4) (1, 5) (2, 6) (3, 7), int8 pairs (0, 2) (1, 3).
+constexpr int word_channel(int p, int bits) {
+  return bits == 4 ? (p & ~7) + ((p & 7) >> 1) + 4 * (p & 1) : (p & ~3) + ((p & 3) >> 1) + 2 * (p & 1);
+}
 
 // Lets a kernel use `bytes` of dynamic shared memory on `device` (an attribute of the
 // kernel on one device; set once for each).
@@ -219,9 +226,15 @@ struct PagedAttendHost {
   void* ws;
   size_t ws_bytes;
 };
-size_t paged_workspace_bytes(int B, int Hq, int Hkv, int n_q, int max_q_len);
+size_t paged_workspace_bytes(int Hq, int Hkv, int max_q_len);
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s);
 uint32_t paged_error_flags(bool clear);
+// Rows (query tokens x heads of a KV head's group) of a request above which the prompt kernel
+// (kvq_attend_prompt.cu) takes a call.
+bool paged_uses_prompt(int Hq, int Hkv, int max_q_len);
+size_t prompt_part_bytes();
+kvq_status launch_attend_prompt(const PagedAttendHost& a, void* part, cudaStream_t s);
+uint32_t prompt_error_flags(bool clear);
 
 kvq_status launch_wait_probe(uint32_t limit_us, cudaStream_t s);
 
