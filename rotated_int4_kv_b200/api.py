@@ -61,6 +61,8 @@ class Plan:
                                      s.ctypes.data_as(ctypes.c_void_p), l.ctypes.data_as(ctypes.c_void_p),
                                      TRANSFORMS[transform], self.bits),
               "kvq_plan_create_ex")
+        # what the compiled binding reads of a plan
+        self._desc = (self._h.value, self.head_dim, self.group, self.bits, self.device_index)
         self._lib = lib
 
     @property
@@ -73,6 +75,7 @@ class Plan:
 
     def close(self) -> None:
         if getattr(self, "_h", None) and self._h.value:
+            self._desc = None
             self._lib.kvq_plan_destroy(self._h)
             self._h = ctypes.c_void_p()
 

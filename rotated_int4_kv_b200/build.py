@@ -1,4 +1,5 @@
-"""Build the in-tree shared library ``libkvq.so`` (CUDA C++ for sm_100a) with nvcc.
+"""Build the in-tree shared library ``libkvq.so`` (CUDA C++ for sm_100a) with nvcc, and the Python
+extension ``_paged.so`` over its paged calls with g++.
 
 Usage: ``python rotated_int4_kv_b200/build.py [--force] [--verbose]`` (run it as a script:
 importing the package loads the library it builds). Object files
@@ -11,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_codec.cu", "kvq_encode_tc.cu", "kvq_decode_tc.cu", "kvq_attend.cu",
            "kvq_page_plan.cu", "kvq_attend_paged.cu", "kvq_attend_prompt.cu"]
+BINDING = "paged_binding.cpp"   # the Python extension module _paged (torch's C++ interface, linked to libkvq.so)
+BINDING_LIB = os.path.join(PKG, "_paged.so")
 HEADERS = ["kvq_internal.h", "kvq_ptx.cuh", "kvq_quant.cuh", "srft_fft.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -68,11 +72,31 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 print(open(log).read())
     if force or jobs or _stale(LIB, objs):
-        cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs, "-lrt"]
+        cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libkvq.so", "-o", LIB, *objs, "-lrt"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stderr[-4000:])
+    _build_binding(force)
     return LIB
+
+
+def _build_binding(force: bool) -> None:
+    src = os.path.join(CSRC, BINDING)
+    if not force and not _stale(BINDING_LIB, [src, os.path.join(ROOT, "include", "kvq.h"), LIB]):
+        return
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+                                os.path.join(cuda, "include"), sysconfig.get_paths()["include"])),
+           src, "-o", BINDING_LIB, LIB, f"-L{os.path.join(t, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{os.path.join(t, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    with open(os.path.join(BUILD, "paged_binding.log"), "w") as f:
+        f.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stderr[-4000:]}")
 
 
 def main(argv=None) -> int:
