@@ -47,10 +47,9 @@ __device__ uint32_t g_paged_err = 0;
 namespace {
 
 constexpr int kRows = 8;        // query rows per unit (mma N)
-constexpr int kWarps = 8;       // consumer warps
-constexpr int kTile = 128;      // tokens per tile: 16 per consumer warp
+constexpr int kWarps = 4;       // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kMaxCtas = 2 * 160;  // partial slots in the workspace: two per CTA
+constexpr int kMaxCtas = 3 * 160;  // partial slots in the workspace: two per CTA
 
 template <int D, int G, int BITS>
 struct PCfg {
@@ -58,19 +57,26 @@ struct PCfg {
   static constexpr int NG = D / G;                // scale groups of a row
   static constexpr int RB = D * BITS / 8;         // code bytes of a row
   static constexpr int MT = D / 16;               // 16-channel tiles (output) and K steps (scores)
-  static constexpr int kMinBlocks = D == 128 ? 2 : 1;
+  static constexpr int kSub = (D == 128 && BITS == 4) ? 2 : 1;  // 16-token subtiles per warp and tile
+  static constexpr int kTile = 16 * kWarps * kSub;         // tokens per tile
+  static constexpr int kCtas = D == 128 ? 3 : 2;           // resident CTAs per SM
   static constexpr int kKBytes = kTile * RB;
   static constexpr int kSBytes = kTile * NG * 2;
   static constexpr int kStage = 2 * (kKBytes + kSBytes);
-  static constexpr int kStages = BITS == 4 ? 4 : 2;
-  static constexpr int kObuf = 4 * kRows * D * 4;          // four warps' outputs
-  static constexpr int kOmStride = D + 4;                  // q~ and the unit's output, fp32, padded rows
+  static constexpr int kObuf = (kWarps / 2) * kRows * D * 4;  // half of the warps' outputs
+  static constexpr int kOmStride = D + 4;                     // q~ and the unit's output, fp32, padded rows
   static constexpr int kOm = kRows * kOmStride * 4;
+  static constexpr int kQn = BITS == 4 ? NG : NC;             // query fragments: 16 bytes per lane each
+  static constexpr int kQf = kQn * 32 * 16;
+  static constexpr int kBias = NG * 4 * 16;
   static constexpr int kMl = kWarps * 2 * kRows * 4;
   static constexpr int kBars = 256;
-  static constexpr int kSmem = kStages * kStage + kObuf + kOm + kMl + kBars + 1024;
-  static_assert(kSmem <= (kMinBlocks == 2 ? 113 : 227) * 1024, "shared memory");
-  static constexpr int PART = 2 * kRows + kRows * D;       // a partial: m, l, o
+  static constexpr int kFixed = kObuf + kOm + kQf + kBias + kMl + kBars + 1024;
+  static constexpr int kRoom = (kCtas == 3 ? 75 : 113) * 1024 - kFixed;
+  static constexpr int kStages = kRoom / kStage < 4 ? kRoom / kStage : 4;
+  static constexpr int kSmem = kStages * kStage + kFixed;
+  static_assert(kStages >= 2, "shared memory");
+  static constexpr int PART = 2 * kRows + kRows * D;          // a partial: m, l, o
 };
 
 struct PagedParams {
@@ -103,21 +109,34 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t 
   return d;
 }
 
-// Eight int4 codes of a word as fp16 pairs: h0 = (n0, n4) 2^-24, h1 = (n1, n5) 2^-20,
-// h2 = (n2, n6) 2^-24, h3 = (n3, n7) 2^-20.
+// Eight int4 codes of a word plus 8, as fp16 pairs: h0 = (n0, n4) 2^-24, h1 = (n1, n5) 2^-20,
+// h2 = (n2, n6) 2^-24, h3 = (n3, n7) 2^-20 (subnormals, exact).
+__device__ __forceinline__ void nib8_plus8(uint32_t w, uint32_t (&h)[4]) {
+  const uint32_t w8 = w >> 8;
+  h[0] = and_xor(w, 0x000F000Fu, 0x00080008u);
+  h[1] = and_xor(w, 0x00F000F0u, 0x00800080u);
+  h[2] = and_xor(w8, 0x000F000Fu, 0x00080008u);
+  h[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
+}
+// The same without the offset.
 __device__ __forceinline__ void nib8(uint32_t w, uint32_t (&h)[4]) {
   const __half2 o1 = u2h(0x00080008u), o16 = u2h(0x00800080u);  // 8 2^-24, 128 2^-24
-  const uint32_t w8 = w >> 8;
-  h[0] = h2u(__hsub2(u2h(and_xor(w, 0x000F000Fu, 0x00080008u)), o1));
-  h[1] = h2u(__hsub2(u2h(and_xor(w, 0x00F000F0u, 0x00800080u)), o16));
-  h[2] = h2u(__hsub2(u2h(and_xor(w8, 0x000F000Fu, 0x00080008u)), o1));
-  h[3] = h2u(__hsub2(u2h(and_xor(w8, 0x00F000F0u, 0x00800080u)), o16));
+  nib8_plus8(w, h);
+  h[0] = h2u(__hsub2(u2h(h[0]), o1));
+  h[1] = h2u(__hsub2(u2h(h[1]), o16));
+  h[2] = h2u(__hsub2(u2h(h[2]), o1));
+  h[3] = h2u(__hsub2(u2h(h[3]), o16));
 }
-// Four int8 codes of a word: h0 = (b0, b2) 2^-24, h1 = (b1, b3) 2^-24.
+// Four int8 codes of a word plus 128: h0 = (b0, b2) 2^-24, h1 = (b1, b3) 2^-24.
+__device__ __forceinline__ void byte4_plus128(uint32_t w, uint32_t (&h)[2]) {
+  h[0] = and_xor(w, 0x00FF00FFu, 0x00800080u);
+  h[1] = and_xor(w >> 8, 0x00FF00FFu, 0x00800080u);
+}
 __device__ __forceinline__ void byte4(uint32_t w, uint32_t (&h)[2]) {
   const __half2 o = u2h(0x00800080u);
-  h[0] = h2u(__hsub2(u2h(and_xor(w, 0x00FF00FFu, 0x00800080u)), o));
-  h[1] = h2u(__hsub2(u2h(and_xor(w >> 8, 0x00FF00FFu, 0x00800080u)), o));
+  byte4_plus128(w, h);
+  h[0] = h2u(__hsub2(u2h(h[0]), o));
+  h[1] = h2u(__hsub2(u2h(h[1]), o));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -139,7 +158,7 @@ __device__ __forceinline__ int row_exponent(float mx) {
 
 // Byte offset of 16-byte column cc of token row `row` of a stage's codes: rows of up to 128
 // bytes with the TMA swizzle of that width, longer rows as boxes of 128 bytes.
-template <int RB>
+template <int RB, int kTile>
 __device__ __forceinline__ int code_off(int row, int cc) {
   if constexpr (RB == 64) return row * 64 + ((cc ^ ((row >> 1) & 3)) << 4);
   return (cc >> 3) * (kTile * 128) + row * 128 + (((cc & 7) ^ (row & 7)) << 4);
@@ -152,6 +171,7 @@ struct Request {
   int tile0, nt, rt;   // first tile, tiles, row tiles
 };
 
+template <int kTile>
 __device__ __forceinline__ Request request_of(const PagedParams& p, int b) {
   Request r;
   r.qs = b;
@@ -196,6 +216,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
 
 // A CTA's piece [at, end) of the line of tiles, walked segment by segment (a segment: the
 // tiles of one unit). `base` is the place of request b's first tile.
+template <int kTile>
 struct Walk {
   long long at, end, base;
   int b;
@@ -207,7 +228,7 @@ struct Walk {
     if (at >= end) return false;
     while (at >= base + tiles_of(p, r)) {
       base += tiles_of(p, r);
-      r = request_of(p, ++b);
+      r = request_of<kTile>(p, ++b);
     }
     const long long off = at - base;
     u = (int)(off / r.nt);
@@ -220,19 +241,23 @@ struct Walk {
 
 // ---------------------------------------------------------------- the kernel
 template <int D, int G, int BITS>
-__global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
+__global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     attend_paged_kernel(const __grid_constant__ PagedParams p) {
   using C = PCfg<D, G, BITS>;
-  constexpr int NC = C::NC, NG = C::NG, MT = C::MT, RB = C::RB;
+  constexpr int NC = C::NC, NG = C::NG, MT = C::MT, RB = C::RB, kTile = C::kTile;
+  constexpr int KS = C::kSub, WT = 16 * KS;  // 16-token subtiles, and tokens, of a warp in a tile
+  constexpr int TW = MT / kWarps;            // 16-row tiles per warp in the two rotations
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
   float4* obuf = reinterpret_cast<float4*>(smem + C::kStages * C::kStage);
-  float* om = reinterpret_cast<float*>(smem + C::kStages * C::kStage + C::kObuf);  // [8][kOmStride]
-  float* wml = om + C::kOm / 4;                                                    // [warp][m, l][8]
+  uint4* qf = reinterpret_cast<uint4*>(smem + C::kStages * C::kStage + C::kObuf);  // [fragment][lane]
+  float* om = reinterpret_cast<float*>(qf) + C::kQf / 4;                            // [8][kOmStride]
+  float* bias = om + C::kOm / 4;                                                    // [group][c][4]
+  float* wml = bias + C::kBias / 4;                                                 // [warp][m, l][8]
   uint64_t* full = reinterpret_cast<uint64_t*>(wml + C::kMl / 4);
   uint64_t* empty = full + C::kStages;
-  long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [9]
+  long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [5]
   long long* found = scan + kWarps + 1;                                // base of the first request, its index
   int* flag = reinterpret_cast<int*>(found + 2);
   static_assert((2 * C::kStages + kWarps + 1 + 2 + 1) * 8 <= C::kBars, "barrier region");
@@ -251,13 +276,13 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
   // ---- this CTA's piece of the line of tiles
   long long total = 0, mine = 0, upto = 0;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    mine = b0 + tid < p.B ? tiles_of(p, request_of(p, b0 + tid)) : 0;
+    mine = b0 + tid < p.B ? tiles_of(p, request_of<kTile>(p, b0 + tid)) : 0;
     long long sum;
     upto = total + block_scan(mine, scan, &sum);
     total += sum;
   }
   const long long per = max((long long)p.min_tiles, (total + gridDim.x - 1) / gridDim.x);
-  Walk w;
+  Walk<kTile> w;
   w.at = min(total, per * blockIdx.x);
   w.end = min(total, w.at + per);
   if (w.at >= w.end) return;
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
   } else {
     long long before = 0;
     for (int b0 = 0; b0 < p.B && before <= w.at; b0 += kThreads) {
-      mine = b0 + tid < p.B ? tiles_of(p, request_of(p, b0 + tid)) : 0;
+      mine = b0 + tid < p.B ? tiles_of(p, request_of<kTile>(p, b0 + tid)) : 0;
       long long sum;
       upto = before + block_scan(mine, scan, &sum);
       if (mine && w.at >= upto - mine && w.at < upto) {
@@ -282,26 +307,25 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
   __syncthreads();  // also publishes the barriers' initialisation
   w.base = found[0];
   w.b = (int)found[1];
-  w.r = request_of(p, w.b);
-  const int P = 1 << p.page_shift;
+  w.r = request_of<kTile>(p, w.b);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer
-    const int ppt = kTile >> p.page_shift;  // pages per tile, at most 8: one lane each
-    const uint32_t box = (uint32_t)(P * (RB < 128 ? RB : 128));
-    const uint32_t sbytes = (uint32_t)(P * NG * 2);
-    const uint32_t page_bytes = 2 * ((uint32_t)(P * RB) + sbytes);
+    // a tile comes as boxes of min(P, kTile) tokens, at most 8: one lane each
+    const int P = 1 << p.page_shift, bt = min(P, kTile), nb = kTile / bt;
+    const uint32_t box = (uint32_t)(bt * (RB < 128 ? RB : 128));
+    const uint32_t sbytes = (uint32_t)(bt * NG * 2);
+    const uint32_t box_bytes = 2 * ((uint32_t)(bt * RB) + sbytes);
     const uint64_t pol = l2_evict_first_policy();
     int n = 0;
     while (w.next(p)) {
       const int h = w.u / w.r.rt;
       const int32_t* row = p.table + (long long)w.b * p.table_stride;
-      auto entry = [&](int i) {  // the table entry of this lane's page in tile i; -1: nothing to load
-        const int pi = (w.r.tile0 + i) * ppt + lane;
-        const bool want = lane < ppt && i < w.i1 && (long long)pi * P < w.r.kv && ((long long)pi + 1) * P > w.r.t_lo;
+      auto entry = [&](int i) {  // the table entry for this lane's box of tile i; -1: nothing to load
+        const long long t = (long long)(w.r.tile0 + i) * kTile + lane * bt;
         int e = -1;
-        if (want) {
-          e = __ldg(row + pi);
+        if (lane < nb && i < w.i1 && t < w.r.kv && t + bt > w.r.t_lo) {
+          e = __ldg(row + (t >> p.page_shift));
           if (e < 0 || e >= p.num_pages) {
             atomicOr(&g_paged_err, kErrBadPage);
             e = 0;
@@ -320,25 +344,27 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
           return;
         }
         const uint32_t here = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(here) * page_bytes);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(here) * box_bytes);
         __syncwarp();
         if (page >= 0) {
           uint8_t* st = ring + s * C::kStage;
           const int ph = page * p.Hkv + h;
+          const int off = ((w.r.tile0 + i) * kTile + lane * bt) & (P - 1);  // the box's first row of the page
 #pragma unroll
           for (int j = 0; j < (RB + 127) / 128; ++j) {
             uint8_t* kd = st + j * (kTile * 128) + lane * box;
             if (p.rt_max == 1) {  // the pages are read once: out of L2's way
-              tma_load_3d_hint(kd, &p.kmap, &full[s], 128 * j, 0, ph, pol);
-              tma_load_3d_hint(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, 0, ph, pol);
+              tma_load_3d_hint(kd, &p.kmap, &full[s], 128 * j, off, ph, pol);
+              tma_load_3d_hint(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph, pol);
             } else {
-              tma_load_3d(kd, &p.kmap, &full[s], 128 * j, 0, ph);
-              tma_load_3d(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, 0, ph);
+              tma_load_3d(kd, &p.kmap, &full[s], 128 * j, off, ph);
+              tma_load_3d(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph);
             }
           }
           uint8_t* sd = st + 2 * C::kKBytes + lane * sbytes;
-          bulk_load(sd, p.ks + (size_t)ph * (P * NG), sbytes, &full[s]);
-          bulk_load(sd + C::kSBytes, p.vs + (size_t)ph * (P * NG), sbytes, &full[s]);
+          const size_t srow = ((size_t)ph * P + off) * NG;
+          bulk_load(sd, p.ks + srow, sbytes, &full[s]);
+          bulk_load(sd + C::kSBytes, p.vs + srow, sbytes, &full[s]);
         }
         page = coming;
       }
@@ -374,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
           bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) : 0u;
       }
 #pragma unroll
-      for (int t = 0; t < MT / kWarps; ++t) {
+      for (int t = 0; t < TW; ++t) {
         const int mt = warp + kWarps * t;
         float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -390,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       }
     }
     consumers_sync();
-    // ---- (2) this lane's B fragments of the scores (column g), normalised by 2^-e per row
-    uint32_t qf[MT][2];
+    // ---- (2) the B fragments of the scores (column = row of the tile), normalised by 2^-e per
+    // row, and per group the start of its sum: minus what the codes' offset adds to it
     float rowfac[2];  // of the scores' columns 2c, 2c + 1: back to base-2 scores
     {
       const float* qr = om + g * C::kOmStride;
@@ -403,20 +429,60 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       };
       float mx = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < MT; ++ks)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(qr[chan(ks, e)]));
+      for (int k = 0; k < D / 16; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(qr + 16 * k + 4 * c);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+      }
       const int ex = row_exponent(mx);
       const float f = pow2f(-ex), fhi = BITS == 4 ? f * 0.0625f : f;  // the odd pairs' codes stand 16 times too high
 #pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
-        qf[ks][0] = pack_half2(qr[chan(ks, 0)] * f, qr[chan(ks, 1)] * f);
-        qf[ks][1] = pack_half2(qr[chan(ks, 2)] * fhi, qr[chan(ks, 3)] * fhi);
-      }
-#pragma unroll
       for (int e = 0; e < 2; ++e)
         rowfac[e] = p.qfac * 16777216.0f * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+      constexpr float kOff = (BITS == 4 ? 8.0f : 128.0f) / 16777216.0f;
+      constexpr float kPair = BITS == 4 ? 16.0f : 1.0f;
+#pragma unroll
+      for (int t = 0; t < NC / kWarps; ++t) {
+        const int ch = warp + kWarps * t;
+        uint32_t h[4];
+        float sum[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          h[2 * k] = pack_half2(qr[chan(2 * ch + k, 0)] * f, qr[chan(2 * ch + k, 1)] * f);
+          h[2 * k + 1] = pack_half2(qr[chan(2 * ch + k, 2)] * fhi, qr[chan(2 * ch + k, 3)] * fhi);
+          const float2 a = __half22float2(u2h(h[2 * k])), b = __half22float2(u2h(h[2 * k + 1]));
+          sum[k] = -kOff * ((a.x + a.y) + kPair * (b.x + b.y));
+        }
+        auto start = [&](int grp, float v) {  // as both token rows of an accumulator of columns 2c', 2c' + 1
+          float* d = bias + (grp * 4 + (g >> 1)) * 4 + (g & 1);
+          d[0] = v;
+          d[2] = v;
+        };
+        if constexpr (G == 32) {
+          qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+          float v = sum[0] + sum[1];
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          if (c == 0) start(ch, v);
+        } else if constexpr (BITS == 4) {  // lane c's channels lie in half c / 2 of the chunk
+          const uint4 z = make_uint4(0, 0, 0, 0), q4 = make_uint4(h[0], h[1], h[2], h[3]);
+          qf[(2 * ch) * 32 + lane] = c < 2 ? q4 : z;
+          qf[(2 * ch + 1) * 32 + lane] = c < 2 ? z : q4;
+          float v = sum[0] + sum[1];
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          if ((c & 1) == 0) start(2 * ch + (c >> 1), v);
+        } else {
+          qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v = sum[k];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (c == 0) start(2 * ch + k, v);
+          }
+        }
+      }
     }
+    consumers_sync();
     // what rows 2c, 2c + 1 attend: tokens in (lo, hi]
     int hi[2], lo[2];
 #pragma unroll
@@ -435,14 +501,15 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       last_lo = p.window ? (int)max((long long)r.kv - r.qn + tok - p.window, -1ll) : -1;
     }
 
-    // ---- (3) the tiles
+    // ---- (3) the tiles. l and o are held divided by 2^(m + ve)
+    constexpr int kVeMin = -11, kVeMax = 4;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
     float o[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    int ve = -14;                 // V scales seen so far are below 2^ve
-    uint32_t vlim = 0x0400u;      // the fp16 bits of 2^ve
-    uint32_t vinv = 0x74007400u;  // 2^-ve as an fp16 pair
+    int ve = kVeMin;                                  // V scales seen so far are below 2^ve, or ve = kVeMax
+    uint32_t vlim = (uint32_t)(kVeMin + 15) << 10;    // the fp16 bits of 2^ve
+    bool bad_row = false;                             // column g attends a V scale that is not finite
     for (int i = w.i0; i < w.i1; ++i, ++n) {
       const int s = n % C::kStages;
       if (!ok) continue;
@@ -452,22 +519,23 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
         continue;
       }
       const uint8_t* st = ring + s * C::kStage;
-      const int r0 = 16 * warp;                                // the warp's rows of the stage
+      const int r0 = WT * warp;                                // the warp's rows of the stage
       const int t0 = (r.tile0 + i) * kTile + r0;               // and their first token
-      if (t0 >= r.kv || t0 + 16 <= r.t_lo) {
+      if (t0 >= r.kv || t0 + WT <= r.t_lo) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
         continue;
       }
-      const bool edge = t0 + 16 > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
-      const bool cut = t0 + 15 > first_hi || t0 <= last_lo;     // some (token, row) pairs are masked
+      const bool edge = t0 + WT > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
+      const bool cut = t0 + WT - 1 > first_hi || t0 <= last_lo;  // some (token, row) pairs are masked
+      const int lrow = r0 + ((mi & 1) << 3) + (lane & 7);       // this lane's row in the ldmatrix loads
       // ---- scores: C layout (tokens g, g + 8; columns 2c, 2c + 1)
-      float sc[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        const uint8_t* kt = st;
+      float sc[KS][4];
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
         float ska[NG], skb[NG];
         {
-          const uint32_t* sa = reinterpret_cast<const uint32_t*>(st + 2 * C::kKBytes + (r0 + g) * (NG * 2));
+          const uint32_t* sa = reinterpret_cast<const uint32_t*>(st + 2 * C::kKBytes + (r0 + 16 * u + g) * (NG * 2));
           const uint32_t* sb = sa + 8 * (NG / 2);
 #pragma unroll
           for (int j = 0; j < NG / 2; ++j) {
@@ -478,39 +546,40 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
             skb[2 * j + 1] = fb.y;
           }
         }
-        auto add = [&](int grp, const float (&a)[4]) {
-          sc[0] = fmaf(ska[grp], a[0], sc[0]);
-          sc[1] = fmaf(ska[grp], a[1], sc[1]);
-          sc[2] = fmaf(skb[grp], a[2], sc[2]);
-          sc[3] = fmaf(skb[grp], a[3], sc[3]);
+        sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.0f;
+        auto begin = [&](int grp, float (&a)[4]) {
+          const float4 v = *reinterpret_cast<const float4*>(bias + (grp * 4 + c) * 4);
+          a[0] = v.x;
+          a[1] = v.y;
+          a[2] = v.z;
+          a[3] = v.w;
         };
-        const int row = r0 + ((mi & 1) << 3) + (lane & 7);
+        auto add = [&](int grp, const float (&a)[4]) {
+          sc[u][0] = fmaf(ska[grp], a[0], sc[u][0]);
+          sc[u][1] = fmaf(ska[grp], a[1], sc[u][1]);
+          sc[u][2] = fmaf(skb[grp], a[2], sc[u][2]);
+          sc[u][3] = fmaf(skb[grp], a[3], sc[u][3]);
+        };
+        const int row = lrow + 16 * u;
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int gp = 0; gp < NC / 2; ++gp) {  // two 32-channel chunks per ldmatrix
             uint32_t x[4];                        // (tok g | g + 8) of chunk 2 gp, the same of 2 gp + 1
-            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(kt + code_off<RB>(row, 2 * gp + (mi >> 1))));
+            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(st + code_off<RB, kTile>(row, 2 * gp + (mi >> 1))));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int ch = 2 * gp + j;
               uint32_t a[4], b[4];
-              nib8(x[2 * j], a);
-              nib8(x[2 * j + 1], b);
-              if constexpr (G == 32) {
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0], qf[2 * ch][1]);
-                mma_16816(acc, a[2], b[2], a[3], b[3], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
-                add(ch, acc);
-              } else {
-                // lane c's channels (8c .. 8c + 7 of the chunk) lie in its half c / 2
+              nib8_plus8(x[2 * j], a);
+              nib8_plus8(x[2 * j + 1], b);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const uint32_t m = (c >> 1) == k ? 0xffffffffu : 0u;
-                  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                  mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0] & m, qf[2 * ch][1] & m);
-                  mma_16816(acc, a[2], b[2], a[3], b[3], qf[2 * ch + 1][0] & m, qf[2 * ch + 1][1] & m);
-                  add(2 * ch + k, acc);
-                }
+              for (int k = 0; k < 32 / G; ++k) {
+                const int grp = (2 * gp + j) * (32 / G) + k;
+                const uint4 qv = qf[grp * 32 + lane];
+                float acc[4];
+                begin(grp, acc);
+                mma_16816(acc, a[0], b[0], a[1], b[1], qv.x, qv.y);
+                mma_16816(acc, a[2], b[2], a[3], b[3], qv.z, qv.w);
+                add(grp, acc);
               }
             }
           }
@@ -518,42 +587,65 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {  // one 32-channel chunk per ldmatrix
             uint32_t x[4];                   // (tok g | g + 8) of channels 0 - 15, the same of 16 - 31
-            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(kt + code_off<RB>(row, 2 * ch + (mi >> 1))));
+            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(st + code_off<RB, kTile>(row, 2 * ch + (mi >> 1))));
             uint32_t a[2], b[2], a2[2], b2[2];
-            byte4(x[0], a);
-            byte4(x[1], b);
-            byte4(x[2], a2);
-            byte4(x[3], b2);
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_16816(acc, a[0], b[0], a[1], b[1], qf[2 * ch][0], qf[2 * ch][1]);
-            if constexpr (G == 32) {
-              mma_16816(acc, a2[0], b2[0], a2[1], b2[1], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
-              add(ch, acc);
-            } else {
-              float acc2[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16816(acc2, a2[0], b2[0], a2[1], b2[1], qf[2 * ch + 1][0], qf[2 * ch + 1][1]);
+            byte4_plus128(x[0], a);
+            byte4_plus128(x[1], b);
+            byte4_plus128(x[2], a2);
+            byte4_plus128(x[3], b2);
+            const uint4 qv = qf[ch * 32 + lane];
+            float acc[4];
+            begin(ch * (32 / G), acc);
+            mma_16816(acc, a[0], b[0], a[1], b[1], qv.x, qv.y);
+            if constexpr (G == 16) {
               add(2 * ch, acc);
-              add(2 * ch + 1, acc2);
+              begin(2 * ch + 1, acc);
             }
+            mma_16816(acc, a2[0], b2[0], a2[1], b2[1], qv.z, qv.w);
+            add(ch * (32 / G) + (32 / G - 1), acc);
           }
         }
       }
-      sc[0] *= rowfac[0];
-      sc[1] *= rowfac[1];
-      sc[2] *= rowfac[0];
-      sc[3] *= rowfac[1];
       if (cut) {
-        const int ta = t0 + g, tb = ta + 8;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (ta > hi[e] || ta <= lo[e]) sc[e] = -INFINITY;
-          if (tb > hi[e] || tb <= lo[e]) sc[2 + e] = -INFINITY;
+        for (int u = 0; u < KS; ++u) {
+          const int ta = t0 + 16 * u + g, tb = ta + 8;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (ta > hi[e] || ta <= lo[e]) sc[u][e] = -INFINITY;
+            if (tb > hi[e] || tb <= lo[e]) sc[u][2 + e] = -INFINITY;
+          }
         }
       }
+      // ---- V scales: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each subtile
+      const uint8_t* vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
+      uint32_t sw[KS][4][NG / 2];
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < KS; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = 16 * u + 2 * c + (e & 1) + ((e & 2) << 2);
+          const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + x * (NG * 2));
+          const bool live = !edge || (t0 + x < r.kv && t0 + x >= r.t_lo);
+#pragma unroll
+          for (int j = 0; j < NG / 2; ++j) {
+            sw[u][e][j] = live ? sp[j] : 0u;
+            top = __vmaxu2(top, sw[u][e][j]);
+          }
+        }
       // ---- online softmax in base 2: m_run is a ceiling of the scores so far; it moves, by
       // some headroom more than needed, only when a score of this stage passes it
-      const float mx0 = fmaxf(sc[0], sc[2]), mx1 = fmaxf(sc[1], sc[3]);
-      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1])) {
+      float mx0 = sc[0][0], mx1 = sc[0][1];
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        mx0 = fmaxf(mx0, fmaxf(sc[u][0], sc[u][2]));
+        mx1 = fmaxf(mx1, fmaxf(sc[u][1], sc[u][3]));
+      }
+      mx0 *= rowfac[0];
+      mx1 *= rowfac[1];
+      const bool large = max(top & 0xFFFFu, top >> 16) >= vlim && (ve < kVeMax || max(top & 0xFFFFu, top >> 16) >= 0x7C00u);
+      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1] || large)) {
         constexpr float kHeadroom = 3.0f;
         float a = mx0, b = mx1;
 #pragma unroll
@@ -561,10 +653,15 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
           b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
         }
+        uint32_t t = max(top & 0x7FFFu, (top >> 16) & 0x7FFFu);
+        t = __reduce_max_sync(0xffffffffu, t);
+        int nve = ve;
+        if (t >= vlim) nve = max(ve, min((int)(t >> 10) - 14, kVeMax));
         const float m0 = a > m_run[0] ? a + kHeadroom : m_run[0];
         const float m1 = b > m_run[1] ? b + kHeadroom : m_run[1];
-        const float f0 = m0 == m_run[0] ? 1.0f : ex2_approx(m_run[0] - m0);
-        const float f1 = m1 == m_run[1] ? 1.0f : ex2_approx(m_run[1] - m1);
+        const float fv = pow2f(ve - nve);
+        const float f0 = (m0 == m_run[0] ? 1.0f : ex2_approx(m_run[0] - m0)) * fv;
+        const float f1 = (m1 == m_run[1] ? 1.0f : ex2_approx(m_run[1] - m1)) * fv;
         l_run[0] *= f0;
         l_run[1] *= f1;
 #pragma unroll
@@ -576,82 +673,76 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
         }
         m_run[0] = m0;
         m_run[1] = m1;
-      }
-      const float ms0 = m_run[0] == -INFINITY ? 0.0f : m_run[0];
-      const float ms1 = m_run[1] == -INFINITY ? 0.0f : m_run[1];
-      const float p0 = ex2_approx(sc[0] - ms0), p1 = ex2_approx(sc[1] - ms1);
-      const float p2 = ex2_approx(sc[2] - ms0), p3 = ex2_approx(sc[3] - ms1);
-      l_run[0] += p0 + p2;
-      l_run[1] += p1 + p3;
-      // P as the B operand of the output product: (tokens 2c, 2c + 1 | + 8; column g)
-      const uint32_t pb0 = movmatrix_trans(pack_half2(p0, p1)), pb1 = movmatrix_trans(pack_half2(p2, p3));
-      // ---- V scales: tokens 2c, 2c + 1, 2c + 8, 2c + 9
-      const uint8_t* vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
-      {
-        // the largest of the warp's scales: lane l holds half of token l / 2's row
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vsc) + lane * (NG / 4);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < NG / 4; ++j) {
-          const uint32_t u = vw[j] & 0x7FFF7FFFu;
-          top = max(top, max(u & 0xFFFFu, u >> 16));
+        if (nve > ve) {
+          ve = nve;
+          vlim = (uint32_t)(nve + 15) << 10;
         }
-        const int t = t0 + (lane >> 1);
-        if (edge && (t >= r.kv || t < r.t_lo)) top = 0;
-        if (__any_sync(0xffffffffu, top >= vlim)) {
-          const int x = min((int)(__reduce_max_sync(0xffffffffu, top) >> 10), 30);
-          const int nve = x - 14;
-          if (nve > ve) {
-            const float f = pow2f(ve - nve);
+        if (t >= 0x7C00u) {  // a V scale that is not finite: zeros, and no number for the rows that attend its token
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              o[mt][0] *= f;
-              o[mt][1] *= f;
-              o[mt][2] *= f;
-              o[mt][3] *= f;
+          for (int u = 0; u < KS; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              bool bad = false;
+#pragma unroll
+              for (int j = 0; j < NG / 2; ++j)
+                bad = bad || (sw[u][e][j] & 0x7C00u) == 0x7C00u || (sw[u][e][j] & 0x7C000000u) == 0x7C000000u;
+              if (!bad) continue;
+#pragma unroll
+              for (int j = 0; j < NG / 2; ++j) sw[u][e][j] = 0u;
+              const int tk = t0 + 16 * u + 2 * c + (e & 1) + ((e & 2) << 2);
+              int tok, head;
+              q_row(min(g, nrows - 1), tok, head);
+              const int h1 = r.kv - r.qn + tok;
+              if (tk <= h1 && (!p.window || (long long)tk > (long long)h1 - p.window)) bad_row = true;
             }
-            ve = nve;
-            vlim = (uint32_t)(x + 1) << 10;
-            vinv = (uint32_t)__half_as_ushort(__float2half_rn(pow2f(-nve))) * 0x10001u;
-          }
         }
       }
-      uint32_t sw[4][NG / 2];
+      const float ms0 = m_run[0] == -INFINITY ? 0.0f : m_run[0] + (float)ve;
+      const float ms1 = m_run[1] == -INFINITY ? 0.0f : m_run[1] + (float)ve;
+      // P as the B operand of the output product: (tokens 2c, 2c + 1 | + 8; column g)
+      uint32_t pb[KS][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = 2 * c + (e & 1) + ((e & 2) << 2);
-        const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + x * (NG * 2));
-        const bool live = !edge || (t0 + x < r.kv && t0 + x >= r.t_lo);
-#pragma unroll
-        for (int j = 0; j < NG / 2; ++j) sw[e][j] = live ? sp[j] : 0u;
+      for (int u = 0; u < KS; ++u) {
+        const float p0 = ex2_approx(fmaf(sc[u][0], rowfac[0], -ms0)), p1 = ex2_approx(fmaf(sc[u][1], rowfac[1], -ms1));
+        const float p2 = ex2_approx(fmaf(sc[u][2], rowfac[0], -ms0)), p3 = ex2_approx(fmaf(sc[u][3], rowfac[1], -ms1));
+        l_run[0] += p0 + p2;
+        l_run[1] += p1 + p3;
+        pb[u][0] = movmatrix_trans(pack_half2(p0, p1));
+        pb[u][1] = movmatrix_trans(pack_half2(p2, p3));
       }
-      // P times the scale of group grp, as the two B registers
-      auto weighted = [&](int grp, uint32_t& b0, uint32_t& b1) {
-        const uint32_t sel = (grp & 1) ? 0x7632u : 0x5410u;
-        const uint32_t s0 = prmt(sw[0][grp >> 1], sw[1][grp >> 1], sel), s1 = prmt(sw[2][grp >> 1], sw[3][grp >> 1], sel);
-        b0 = h2u(__hmul2(__hmul2(u2h(s0), u2h(vinv)), u2h(pb0)));
-        b1 = h2u(__hmul2(__hmul2(u2h(s1), u2h(vinv)), u2h(pb1)));
-      };
-      // ---- output: O[channel][column] += V[channel][token] P[token][column]
-      {
-        const uint8_t* vt = st + C::kKBytes;
-        const int row = r0 + ((mi & 1) << 3) + (lane & 7);
+      // ---- output: O[channel][column] += V[channel][token] P[token][column] scale; the codes
+      // stand off too high, which a product with a constant takes out again
+      const uint8_t* vt = st + C::kKBytes;
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        // P times the scale of group grp, as the two B registers
+        auto weighted = [&](int grp, uint32_t& b0, uint32_t& b1) {
+          const uint32_t sel = (grp & 1) ? 0x7632u : 0x5410u;
+          const uint32_t s0 = prmt(sw[u][0][grp >> 1], sw[u][1][grp >> 1], sel);
+          const uint32_t s1 = prmt(sw[u][2][grp >> 1], sw[u][3][grp >> 1], sel);
+          b0 = h2u(__hmul2(u2h(s0), u2h(pb[u][0])));
+          b1 = h2u(__hmul2(u2h(s1), u2h(pb[u][1])));
+        };
+        const int row = lrow + 16 * u;
         if constexpr (BITS == 4) {
+          constexpr uint32_t n8 = 0x80088008u, n128 = 0x80808080u;  // -8 2^-24, -128 2^-24
 #pragma unroll
           for (int gp = 0; gp < NC / 2; ++gp) {
             uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of chunk 2 gp, the same of 2 gp + 1
-            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB>(row, 2 * gp + (mi >> 1))));
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB, kTile>(row, 2 * gp + (mi >> 1))));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int ch = 2 * gp + j;
               uint32_t a[4], b[4];  // channels 4g, 4g + 1 (16 times), 4g + 2, 4g + 3 (16 times) of the chunk
-              nib8(x[2 * j], a);
-              nib8(x[2 * j + 1], b);
+              nib8_plus8(x[2 * j], a);
+              nib8_plus8(x[2 * j + 1], b);
               if constexpr (G == 32) {
                 uint32_t b0, b1;
                 weighted(ch, b0, b1);
                 mma_16816(o[2 * ch], a[0], a[1], b[0], b[1], b0, b1);
                 mma_16816(o[2 * ch + 1], a[2], a[3], b[2], b[3], b0, b1);
+                mma_16816(o[2 * ch], n8, n128, n8, n128, b0, b1);
+                mma_16816(o[2 * ch + 1], n8, n128, n8, n128, b0, b1);
               } else {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {  // lane g's channels lie in half g / 4 of the chunk
@@ -660,6 +751,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
                   weighted(2 * ch + k, b0, b1);
                   mma_16816(o[2 * ch], a[0] & m, a[1] & m, b[0] & m, b[1] & m, b0, b1);
                   mma_16816(o[2 * ch + 1], a[2] & m, a[3] & m, b[2] & m, b[3] & m, b0, b1);
+                  mma_16816(o[2 * ch], n8 & m, n128 & m, n8 & m, n128 & m, b0, b1);
+                  mma_16816(o[2 * ch + 1], n8 & m, n128 & m, n8 & m, n128 & m, b0, b1);
                 }
               }
             }
@@ -668,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {
             uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of channels 0 - 15, the same of 16 - 31
-            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB>(row, 2 * ch + (mi >> 1))));
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB, kTile>(row, 2 * ch + (mi >> 1))));
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               uint32_t a[2], b[2], b0, b1;  // channels 2g, 2g + 1 of the half
@@ -691,12 +784,15 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], off);
     }
     consumers_sync();  // q~ has been read
-    if (g == 0) {
-      float* ml = wml + warp * 2 * kRows;
-      ml[2 * c] = m_run[0];
-      ml[2 * c + 1] = m_run[1];
-      ml[kRows + 2 * c] = l_run[0];
-      ml[kRows + 2 * c + 1] = l_run[1];
+    const uint32_t bad_rows = __ballot_sync(0xffffffffu, bad_row);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m_run[e] += (float)ve;  // from here on with V's power of two
+      if ((bad_rows >> (4 * (2 * c + e))) & 15u) l_run[e] = __int_as_float(0x7fc00000);
+      if (g == 0) {
+        wml[warp * 2 * kRows + 2 * c + e] = m_run[e];
+        wml[warp * 2 * kRows + kRows + 2 * c + e] = l_run[e];
+      }
     }
     consumers_sync();
     float M[2], f[2];
@@ -705,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       M[e] = -INFINITY;
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) M[e] = fmaxf(M[e], wml[x * 2 * kRows + 2 * c + e]);
-      f[e] = m_run[e] == -INFINITY ? 0.0f : ex2_approx(m_run[e] - M[e]) * pow2f(24 + ve);
+      f[e] = m_run[e] == -INFINITY ? 0.0f : ex2_approx(m_run[e] - M[e]) * pow2f(24);
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -753,12 +849,10 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       Lr = 0.0f;
 #pragma unroll
       for (int x = 0; x < kWarps; ++x) Mr = fmaxf(Mr, wml[x * 2 * kRows + row]);
-      if (Mr != -INFINITY) {
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          const float mw = wml[x * 2 * kRows + row];
-          if (mw != -INFINITY) Lr = fmaf(wml[x * 2 * kRows + kRows + row], ex2_approx(mw - Mr), Lr);
-        }
+      for (int x = 0; x < kWarps; ++x) {
+        const float mw = wml[x * 2 * kRows + row], lw = wml[x * 2 * kRows + kRows + row];
+        Lr += mw != -INFINITY ? lw * ex2_approx(mw - Mr) : lw;  // nothing attended: 0, or NaN where scores are
       }
     };
     consumers_sync();
@@ -809,7 +903,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
           for (int k = 0; k < np; ++k) Mx = fmaxf(Mx, __ldcg(slot_of(xa + k) + tid));
           for (int k = 0; k < np; ++k) {
             const float mk = __ldcg(slot_of(xa + k) + tid);
-            if (mk != -INFINITY) Lx = fmaf(__ldcg(slot_of(xa + k) + kRows + tid), ex2_approx(mk - Mx), Lx);
+            const float lk = __ldcg(slot_of(xa + k) + kRows + tid);
+            Lx += mk != -INFINITY ? lk * ex2_approx(mk - Mx) : lk;
           }
           Lrow[tid] = Lx;
           wml[tid] = Mx;
@@ -862,9 +957,9 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       }
       const int ex = row_exponent(mx);
       const float fx = inv * pow2f(-ex);
-      float acc[MT / kWarps][4];
+      float acc[TW][4];
 #pragma unroll
-      for (int t = 0; t < MT / kWarps; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+      for (int t = 0; t < TW; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < MT; ++ks) {
         uint32_t bh[2], bl[2];
@@ -877,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
           bl[e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
         }
 #pragma unroll
-        for (int t = 0; t < MT / kWarps; ++t) {
+        for (int t = 0; t < TW; ++t) {
           const uint4 a = __ldg(p.wo + ((warp + kWarps * t) * MT + ks) * 32 + lane);
           mma_16816(acc[t], a.x, a.y, a.z, a.w, bh[0], bh[1]);
           mma_16816(acc[t], a.x, a.y, a.z, a.w, bl[0], bl[1]);
@@ -888,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kMinBlocks))
       for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
       __half* xb = reinterpret_cast<__half*>(obuf);  // [8][D + 8]
 #pragma unroll
-      for (int t = 0; t < MT / kWarps; ++t) {
+      for (int t = 0; t < TW; ++t) {
         const int s0 = 16 * (warp + kWarps * t) + g;
         __half* x0 = xb + (2 * c) * (D + 8) + s0;
         x0[0] = __float2half_rn(acc[t][0] * fo[0]);
@@ -926,7 +1021,7 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   const int P = 1 << a.page_shift;
   const uint64_t dims[3] = {(uint64_t)C::RB, (uint64_t)P, (uint64_t)a.num_pages * a.Hkv};
   const uint64_t strides[2] = {(uint64_t)C::RB, (uint64_t)C::RB * P};
-  const uint32_t box[3] = {(uint32_t)(C::RB < 128 ? C::RB : 128), (uint32_t)P, 1u};
+  const uint32_t box[3] = {(uint32_t)(C::RB < 128 ? C::RB : 128), (uint32_t)std::min(P, C::kTile), 1u};
   const CUtensorMapSwizzle sw = C::RB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   kvq_status st = encode_tiled_new(&p.kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.kc, dims, strides, box, sw, "K pages");
   if (st == KVQ_OK)
@@ -963,8 +1058,8 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.cnt = reinterpret_cast<int*>(ws);
   p.part = reinterpret_cast<float*>(ws + kCntBytes);
   // no more CTAs than pieces of min_tiles tiles if every request were as long as it may be
-  const long long most = (long long)a.B * a.Hkv * p.rt_max * std::max(1, (p.max_kv + kTile - 1) / kTile);
-  const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kMinBlocks);
+  const long long most = (long long)a.B * a.Hkv * p.rt_max * std::max(1, (p.max_kv + C::kTile - 1) / C::kTile);
+  const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kCtas);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::min<long long>(slots, (most + p.min_tiles - 1) / p.min_tiles));
   cfg.blockDim = dim3(kThreads);
