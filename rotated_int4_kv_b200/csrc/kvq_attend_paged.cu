@@ -118,15 +118,6 @@ __device__ __forceinline__ void nib8_plus8(uint32_t w, uint32_t (&h)[4]) {
   h[2] = and_xor(w8, 0x000F000Fu, 0x00080008u);
   h[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
 }
-// The same without the offset.
-__device__ __forceinline__ void nib8(uint32_t w, uint32_t (&h)[4]) {
-  const __half2 o1 = u2h(0x00080008u), o16 = u2h(0x00800080u);  // 8 2^-24, 128 2^-24
-  nib8_plus8(w, h);
-  h[0] = h2u(__hsub2(u2h(h[0]), o1));
-  h[1] = h2u(__hsub2(u2h(h[1]), o16));
-  h[2] = h2u(__hsub2(u2h(h[2]), o1));
-  h[3] = h2u(__hsub2(u2h(h[3]), o16));
-}
 // Four int8 codes of a word plus 128: h0 = (b0, b2) 2^-24, h1 = (b1, b3) 2^-24.
 __device__ __forceinline__ void byte4_plus128(uint32_t w, uint32_t (&h)[2]) {
   h[0] = and_xor(w, 0x00FF00FFu, 0x00800080u);
@@ -248,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   constexpr int KS = C::kSub, WT = 16 * KS;  // 16-token subtiles, and tokens, of a warp in a tile
   constexpr int TW = MT / kWarps;            // 16-row tiles per warp in the two rotations
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // an offset, not a rounded pointer: the compiler then knows every access below as shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ring = smem;
   float4* obuf = reinterpret_cast<float4*>(smem + C::kStages * C::kStage);
   uint4* qf = reinterpret_cast<uint4*>(smem + C::kStages * C::kStage + C::kObuf);  // [fragment][lane]
@@ -260,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [5]
   long long* found = scan + kWarps + 1;                                // base of the first request, its index
   int* flag = reinterpret_cast<int*>(found + 2);
-  static_assert((2 * C::kStages + kWarps + 1 + 2 + 1) * 8 <= C::kBars, "barrier region");
+  uint4* consts = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(full) + C::kBars - 16);
+  static_assert((2 * C::kStages + kWarps + 1 + 2 + 1) * 8 <= C::kBars - 16, "barrier region");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -269,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       mbar_init(&empty[s], kWarps);
     }
     fence_mbarrier_init();
+    *consts = make_uint4(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);  // -8 2^-24 and -128 2^-24, rows g and g + 8
   }
   grid_dep_launch();
   grid_dep_wait();  // lengths, table, pages, queries and the workspace may come from the kernel before
@@ -508,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     int ve = kVeMin;                                  // V scales seen so far are below 2^ve, or ve = kVeMax
-    uint32_t vlim = (uint32_t)(kVeMin + 15) << 10;    // the fp16 bits of 2^ve
+    uint32_t vlim = (uint32_t)(kVeMin + 15) << 10;    // the fp16 bits of 2^ve; above every scale from kVeMax on
     bool bad_row = false;                             // column g attends a V scale that is not finite
     for (int i = w.i0; i < w.i1; ++i, ++n) {
       const int s = n % C::kStages;
@@ -617,23 +611,49 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           }
         }
       }
-      // ---- V scales: tokens 2c, 2c + 1, 2c + 8, 2c + 9 of each subtile
-      const uint8_t* vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
-      uint32_t sw[KS][4][NG / 2];
+      // ---- V scales: a token per lane (two lanes where the warp has 16) for the largest of them.
+      // Those of tokens that hold no attended data, and those that are not finite, are made
+      // zeros in place (this warp alone reads them)
+      uint8_t* vsc = ring + s * C::kStage + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
       uint32_t top = 0;
+      {
+        constexpr int LW = NG / 2 * WT / 32;  // 32-bit words of a lane
+        uint32_t* vw = reinterpret_cast<uint32_t*>(vsc) + lane * LW;
+        uint32_t x[LW];
 #pragma unroll
-      for (int u = 0; u < KS; ++u)
+        for (int k = 0; k < LW; ++k) x[k] = vw[k];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int x = 16 * u + 2 * c + (e & 1) + ((e & 2) << 2);
-          const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + x * (NG * 2));
-          const bool live = !edge || (t0 + x < r.kv && t0 + x >= r.t_lo);
+        for (int k = 0; k < LW; ++k) top = __vmaxu2(top, x[k]);
+        const int t = t0 + lane * WT / 32;
+        const bool dead = edge && (t >= r.kv || t < r.t_lo);
+        const bool odd = !dead && max(top & 0xFFFFu, top >> 16) >= 0x7C00u;  // not finite, or a sign
+        if (__any_sync(0xffffffffu, dead || odd)) {
+          bool bad = false;
+          top = 0;
 #pragma unroll
-          for (int j = 0; j < NG / 2; ++j) {
-            sw[u][e][j] = live ? sp[j] : 0u;
-            top = __vmaxu2(top, sw[u][e][j]);
+          for (int k = 0; k < LW; ++k) {
+            if (odd && ((x[k] & 0x7C00u) == 0x7C00u || (x[k] & 0x7C000000u) == 0x7C000000u)) bad = true;
+            top = __vmaxu2(top, x[k] & 0x7FFF7FFFu);
+          }
+          if (dead || bad) {
+            top = 0;
+#pragma unroll
+            for (int k = 0; k < LW; ++k) vw[k] = 0;
+          }
+          uint32_t bads = __ballot_sync(0xffffffffu, bad);
+          fence_proxy_async_smem();  // before the producer's next copy into these rows
+          __syncwarp();
+          while (bads) {
+            const int tk = t0 + (__ffs(bads) - 1) * WT / 32;
+            bads &= bads - 1;
+            int tok, head;
+            q_row(min(g, nrows - 1), tok, head);
+            const int h1 = r.kv - r.qn + tok;
+            if (tk <= h1 && (!p.window || (long long)tk > (long long)h1 - p.window)) bad_row = true;
           }
         }
+        top = max(top & 0xFFFFu, top >> 16);
+      }
       // ---- online softmax in base 2: m_run is a ceiling of the scores so far; it moves, by
       // some headroom more than needed, only when a score of this stage passes it
       float mx0 = sc[0][0], mx1 = sc[0][1];
@@ -644,8 +664,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       }
       mx0 *= rowfac[0];
       mx1 *= rowfac[1];
-      const bool large = max(top & 0xFFFFu, top >> 16) >= vlim && (ve < kVeMax || max(top & 0xFFFFu, top >> 16) >= 0x7C00u);
-      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1] || large)) {
+      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1] || top >= vlim)) {
         constexpr float kHeadroom = 3.0f;
         float a = mx0, b = mx1;
 #pragma unroll
@@ -653,8 +672,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
           b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
         }
-        uint32_t t = max(top & 0x7FFFu, (top >> 16) & 0x7FFFu);
-        t = __reduce_max_sync(0xffffffffu, t);
+        const uint32_t t = __reduce_max_sync(0xffffffffu, top);
         int nve = ve;
         if (t >= vlim) nve = max(ve, min((int)(t >> 10) - 14, kVeMax));
         const float m0 = a > m_run[0] ? a + kHeadroom : m_run[0];
@@ -673,29 +691,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         }
         m_run[0] = m0;
         m_run[1] = m1;
-        if (nve > ve) {
-          ve = nve;
-          vlim = (uint32_t)(nve + 15) << 10;
-        }
-        if (t >= 0x7C00u) {  // a V scale that is not finite: zeros, and no number for the rows that attend its token
-#pragma unroll
-          for (int u = 0; u < KS; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              bool bad = false;
-#pragma unroll
-              for (int j = 0; j < NG / 2; ++j)
-                bad = bad || (sw[u][e][j] & 0x7C00u) == 0x7C00u || (sw[u][e][j] & 0x7C000000u) == 0x7C000000u;
-              if (!bad) continue;
-#pragma unroll
-              for (int j = 0; j < NG / 2; ++j) sw[u][e][j] = 0u;
-              const int tk = t0 + 16 * u + 2 * c + (e & 1) + ((e & 2) << 2);
-              int tok, head;
-              q_row(min(g, nrows - 1), tok, head);
-              const int h1 = r.kv - r.qn + tok;
-              if (tk <= h1 && (!p.window || (long long)tk > (long long)h1 - p.window)) bad_row = true;
-            }
-        }
+        ve = nve;
+        vlim = ve < kVeMax ? (uint32_t)(ve + 15) << 10 : 0xFFFFu;
       }
       const float ms0 = m_run[0] == -INFINITY ? 0.0f : m_run[0] + (float)ve;
       const float ms1 = m_run[1] == -INFINITY ? 0.0f : m_run[1] + (float)ve;
@@ -713,19 +710,27 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       // ---- output: O[channel][column] += V[channel][token] P[token][column] scale; the codes
       // stand off too high, which a product with a constant takes out again
       const uint8_t* vt = st + C::kKBytes;
+      const uint4 off = *consts;  // read here: four registers in order, not four moves for every product
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
+        // the scales of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+        uint32_t sw[4][NG / 2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + (16 * u + 2 * c + (e & 1) + ((e & 2) << 2)) * (NG * 2));
+#pragma unroll
+          for (int j = 0; j < NG / 2; ++j) sw[e][j] = sp[j];
+        }
         // P times the scale of group grp, as the two B registers
         auto weighted = [&](int grp, uint32_t& b0, uint32_t& b1) {
           const uint32_t sel = (grp & 1) ? 0x7632u : 0x5410u;
-          const uint32_t s0 = prmt(sw[u][0][grp >> 1], sw[u][1][grp >> 1], sel);
-          const uint32_t s1 = prmt(sw[u][2][grp >> 1], sw[u][3][grp >> 1], sel);
+          const uint32_t s0 = prmt(sw[0][grp >> 1], sw[1][grp >> 1], sel);
+          const uint32_t s1 = prmt(sw[2][grp >> 1], sw[3][grp >> 1], sel);
           b0 = h2u(__hmul2(u2h(s0), u2h(pb[u][0])));
           b1 = h2u(__hmul2(u2h(s1), u2h(pb[u][1])));
         };
         const int row = lrow + 16 * u;
         if constexpr (BITS == 4) {
-          constexpr uint32_t n8 = 0x80088008u, n128 = 0x80808080u;  // -8 2^-24, -128 2^-24
 #pragma unroll
           for (int gp = 0; gp < NC / 2; ++gp) {
             uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of chunk 2 gp, the same of 2 gp + 1
@@ -741,8 +746,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
                 weighted(ch, b0, b1);
                 mma_16816(o[2 * ch], a[0], a[1], b[0], b[1], b0, b1);
                 mma_16816(o[2 * ch + 1], a[2], a[3], b[2], b[3], b0, b1);
-                mma_16816(o[2 * ch], n8, n128, n8, n128, b0, b1);
-                mma_16816(o[2 * ch + 1], n8, n128, n8, n128, b0, b1);
+                mma_16816(o[2 * ch], off.x, off.y, off.z, off.w, b0, b1);
+                mma_16816(o[2 * ch + 1], off.x, off.y, off.z, off.w, b0, b1);
               } else {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {  // lane g's channels lie in half g / 4 of the chunk
@@ -751,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
                   weighted(2 * ch + k, b0, b1);
                   mma_16816(o[2 * ch], a[0] & m, a[1] & m, b[0] & m, b[1] & m, b0, b1);
                   mma_16816(o[2 * ch + 1], a[2] & m, a[3] & m, b[2] & m, b[3] & m, b0, b1);
-                  mma_16816(o[2 * ch], n8 & m, n128 & m, n8 & m, n128 & m, b0, b1);
-                  mma_16816(o[2 * ch + 1], n8 & m, n128 & m, n8 & m, n128 & m, b0, b1);
+                  mma_16816(o[2 * ch], off.x & m, off.y & m, off.z & m, off.w & m, b0, b1);
+                  mma_16816(o[2 * ch + 1], off.x & m, off.y & m, off.z & m, off.w & m, b0, b1);
                 }
               }
             }

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
   constexpr int NG = D / G, RB = D * BITS / 8;
   constexpr int kBlkQ = 128 * 128, kBlkT = T * 128;  // bytes of a 64-channel block of Q, of a tile
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // an offset, not a rounded pointer: the compiler then knows every access below as shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kQ;
   uint8_t* sV = sK + 2 * C::kTile;
