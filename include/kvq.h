@@ -384,8 +384,9 @@ kvq_status kvq_attend_decode_ref(const uint16_t* q, const uint16_t* k, const uin
  *      slot           int32: page * P + place in the page; num_pages * P <= 2^31 - 1
  * K and V pages share one table. Lengths, tables and slots are device data, so the host
  * checks cannot see them; what a kernel does with an entry outside its range is said at
- * each call, and none reads or writes outside the buffers given. Every call is one launch
- * on `stream` (kvq_encode_paged: one per two jobs) and may be captured into a CUDA graph.
+ * each call, and none reads or writes outside the buffers given. Every call only launches
+ * kernels on `stream` (kvq_attend_paged two or three, kvq_encode_paged one per two jobs, the
+ * others one) and may be captured into a CUDA graph.
  */
 
 /*
@@ -473,8 +474,8 @@ kvq_status kvq_decode_paged(const kvq_plan* plan, const uint8_t* codes, const ui
  *   softmax_scale  <= 0 selects 1/sqrt(D).
  *   out        fp16 [n_q, Hq, D]. A query with nothing to attend to gets zeros; rows of
  *              tokens that belong to no request are left as they were.
- *   workspace  >= kvq_paged_workspace_size bytes, zero before its first use (every call
- *              leaves its counters zero); not to be used by two calls at once.
+ *   workspace  >= kvq_paged_workspace_size bytes, with any contents; not to be used by two
+ *              calls at once.
  * A table entry outside [0, num_pages) raises device error flag 8 (kvq_poll_device_errors)
  * and page 0 is read in its place; entries of pages with no attended token are not read.
  * Codes and scales behind a request's last token may hold anything.

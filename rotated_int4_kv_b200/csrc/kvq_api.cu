@@ -820,7 +820,7 @@ kvq_status kvq_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint1
 
 size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 128 && D != 256) || n_q < 0 || max_q_len < 1) return 0;
-  return kvq::paged_workspace_bytes(Hq, Hkv, max_q_len);
+  return kvq::paged_workspace_bytes(B, Hq, Hkv, D, n_q, max_q_len);
 }
 
 kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,
@@ -854,7 +854,7 @@ kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16
       return fail(KVQ_ERR_ALIGNMENT, "attend_paged: query strides must be multiples of 8 elements");
     if ((n_q > 1 && q_token_stride < 0) || (Hq > 1 && q_head_stride < 0))
       return fail(KVQ_ERR_INVALID_ARG, "attend_paged: negative query stride");
-    const size_t need = kvq::paged_workspace_bytes(Hq, Hkv, max_q_len);
+    const size_t need = kvq::paged_workspace_bytes(B, Hq, Hkv, pk->D, n_q, max_q_len);
     if (!ws || ws_bytes < need) return fail(KVQ_ERR_WORKSPACE, "attend_paged: workspace missing or too small");
     if (!kvq::aligned16(ws)) return fail(KVQ_ERR_ALIGNMENT, "attend_paged: workspace must be 16-byte aligned");
     st = kvq::check_plan_device(pk);

@@ -5,36 +5,38 @@
 //   o = sum_t softmax(score)_t (c_V scale_V)_t,   out = diag(s_V) Q^T Lambda_V^-1 o.
 //
 // Work. A unit is (request, KV head, tile of 8 query rows), a query row one (query token,
-// head of the KV head's group); its tokens are taken in tiles of 128. The tiles of all units
-// form one line, requests after requests, and every CTA of a persistent grid takes an equal
-// piece of it, however ragged the lengths are: a piece is the end of one unit, some whole
-// units, the beginning of another. The lengths live on the GPU, so every CTA adds them up
-// for itself (one block scan). Units cut by a piece's border are joined through the
-// workspace: each CTA writes its softmax partial (m, l, o), the last one to arrive at the
-// unit's counter (found by an atomic, nobody waits) merges them in CTA order, so the result
-// does not depend on who was last.
+// head of the KV head's group). Three kernels, each started early by the one in front:
+//   rotate  a block per unit prepares its queries (q~ as product fragments);
+//   attend  the tiles of all units (128 tokens; 64 where rows are longer) form one line,
+//           requests after requests, and every CTA of a persistent grid takes an equal piece
+//           of it, however ragged the lengths are: the end of one unit, some whole units, the
+//           beginning of another. The lengths live on the GPU, so every CTA adds them up for
+//           itself (one block scan). It leaves a partial (m, l, o) per piece of a unit;
+//   join    a block per unit adds its partials in CTA order and un-rotates the output.
+// One kernel that rotated, merged (last arrival at a counter) and un-rotated inside the
+// pieces took 24 us beside the loads instead of 16: 64 ragged requests 88 -> 66 us, 4 x 128K
+// tokens 137 -> 125 us, one request of 700 tokens 13.0 -> 11.5 us.
 //
-// A CTA is one producer warp and eight consumer warps. The producer streams a tile's pages
-// into a ring of stages: per page one TMA box of K codes and one of V codes (swizzled for
-// ldmatrix), and the scale rows as plain bulk copies. Consumer warp w takes tokens 16 w ..
-// 16 w + 15 of a stage, all channels, and keeps its own softmax state and output; the warps
-// are joined when a unit ends, while the producer already loads the next unit's tiles.
+// A CTA of attend is one producer warp and four consumer warps. The producer streams a tile's
+// pages into a ring of stages: per page one TMA box of K codes and one of V codes (swizzled for
+// ldmatrix), and the scale rows as plain bulk copies. Consumer warp w takes the w-th quarter of
+// a tile's tokens, all channels, and keeps its own softmax state and output; the warps are
+// joined when a unit ends, while the producer already loads the next unit's tiles.
 //
 // Products are mma.m16n8k16 with tokens (scores) or channels (output) as rows and the 8
-// query rows as columns: the loop is bound by issue slots and HBM, not by the tensor cores.
-//   * A code enters as the fp16 subnormal c 2^-24 (int4: nibble + 8 in the low bits of an
-//     fp16 word, or 16 times that in the next four, minus the offset; both exact), one
-//     logical and one fp16 operation per pair; the powers of two are taken out of the
-//     query's fragments and of the sums.
+// query rows as columns. At 4.9 TB/s per further token (75 % of the copy rate) the loop is
+// bound by instruction issue (about 310 per 16 tokens of 128 channels, 150 of them on the
+// integer pipe), not by the tensor cores (25 %).
+//   * A code enters as a fp16 subnormal (code + 8) 2^-24 (int4: nibble + 8 in the low bits of
+//     an fp16 word, or 16 times that in the next four): one logical operation per pair. The
+//     offset is taken out by the accumulators' start in the scores and by a product with a
+//     constant in the output, the powers of two by the query's fragments and at the end.
 //   * q~ is one fp16 rounding per element after a power-of-two normalisation per row
 //     (2^-12 relative on average, so a score's error is about 2^-12 of |q||k|/sqrt(D), below
 //     what the fp16 rounding of the caller's q has put there).
-//   * P is fp16 (2^-11 relative per weight, its sum l is in fp32 of the unrounded values)
-//     times the V scale over a power of two that bounds the scales seen so far, so that
-//     neither large nor small V leave the fp16 range.
-// The query's rotation and the output's un-rotation are products with a per-plan matrix
-// that was laid out as fragments when the plan was made; they are read through L2 by the
-// warp that multiplies with them, 32 KB (D = 128) per unit, and take no shared memory.
+//   * P is fp16 (2^-12 relative on average; its sum l is in fp32 of the unrounded values),
+//     divided by a power of two that bounds the V scales seen so far, so that its product
+//     with them (one more rounding) stays within fp16 for large and small V.
 #include <algorithm>
 
 #include "kvq_internal.h"
@@ -63,15 +65,15 @@ struct PCfg {
   static constexpr int kKBytes = kTile * RB;
   static constexpr int kSBytes = kTile * NG * 2;
   static constexpr int kStage = 2 * (kKBytes + kSBytes);
-  static constexpr int kObuf = (kWarps / 2) * kRows * D * 4;  // half of the warps' outputs
-  static constexpr int kOmStride = D + 4;                     // q~ and the unit's output, fp32, padded rows
-  static constexpr int kOm = kRows * kOmStride * 4;
+  static constexpr int kObuf = kWarps * (kWarps - 1) * (MT / kWarps) * 32 * 16;  // the warps' outputs, less each one's own quarter
+  static constexpr int kOmStride = D + 4;                     // q~, fp32, padded rows
   static constexpr int kQn = BITS == 4 ? NG : NC;             // query fragments: 16 bytes per lane each
   static constexpr int kQf = kQn * 32 * 16;
   static constexpr int kBias = NG * 4 * 16;
+  static constexpr int kPrep = kQf + kBias + kRows * 4;       // a unit's prepared query
   static constexpr int kMl = kWarps * 2 * kRows * 4;
   static constexpr int kBars = 256;
-  static constexpr int kFixed = kObuf + kOm + kQf + kBias + kMl + kBars + 1024;
+  static constexpr int kFixed = kObuf + kPrep + kMl + kBars + 1024;
   static constexpr int kRoom = (kCtas == 3 ? 75 : 113) * 1024 - kFixed;
   static constexpr int kStages = kRoom / kStage < 4 ? kRoom / kStage : 4;
   static constexpr int kSmem = kStages * kStage + kFixed;
@@ -90,8 +92,10 @@ struct PagedParams {
   const uint4* wq;
   const uint4* wo;
   uint16_t* out;
-  float* part;
-  int* cnt;
+  uint8_t* qprep;          // [unit] prepared queries
+  float* part;             // [2 CTA + (0, 1)] partials of units that are cut
+  float* part_unit;        // [unit] partials of whole units
+  int2* desc;              // [unit] the first CTA's slot and the number of partials (0: whole)
   long long q_ts, q_hs, table_stride;
   float qfac, ofac;        // sigma log2(e) times the query matrix' scale; the output matrix' scale
   int B, n_q, Hq, Hkv, Gq, rt_max, max_q, max_kv, num_pages, page_shift, window, min_tiles;
@@ -230,6 +234,128 @@ struct Walk {
   }
 };
 
+// ---------------------------------------------------------------- first kernel: the queries
+// Block u: the 8 query rows of unit u, rotated (a product with the plan's matrix, laid out as
+// fragments when the plan was made) and laid out as the score products' B fragments
+// (column = row of the tile), normalised by 2^-e per row, with per group the start of its sum
+// (minus what the codes' offset adds to it) and per row the factor back to base-2 scores.
+// A block reads the matrix (32 KB at D = 128) through L2; at D = 128 before it waits for the
+// kernel in front. Done here once per unit, not in every piece of it, and beside the main
+// kernel's start.
+template <int D, int G, int BITS>
+__global__ void __launch_bounds__(kWarps * 32) rotate_paged_kernel(const __grid_constant__ PagedParams p) {
+  using C = PCfg<D, G, BITS>;
+  constexpr int NC = C::NC, MT = C::MT, TW = MT / kWarps;
+  __shared__ __align__(16) float om[kRows * C::kOmStride];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  constexpr bool kAhead = D == 128;
+  uint4 wf[kAhead ? TW : 1][MT];
+  auto load_matrix = [&](int t, uint4 (&f)[MT]) {
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) f[ks] = __ldg(p.wq + ((warp + kWarps * t) * MT + ks) * 32 + lane);
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t) load_matrix(t, wf[t]);
+  }
+  grid_dep_wait();
+  grid_dep_launch();  // after the wait: what the main kernel reads before its own wait is complete
+  const Request r = request_of<C::kTile>(p, b);
+  const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
+  if (nrows <= 0) return;
+  uint32_t bq[MT][2];
+  {
+    const int y = rt * kRows + (g < nrows ? g : 0), tok = y / p.Gq, head = h * p.Gq + (y - tok * p.Gq);
+    const uint16_t* src = p.q + (long long)(r.qs + tok) * p.q_ts + (long long)head * p.q_hs;
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) : 0u;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    const int mt = warp + kWarps * t;
+    if constexpr (!kAhead) load_matrix(t, wf[0]);
+    float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) {
+      const uint4 a = wf[kAhead ? t : 0][ks];
+      mma_16816((ks & 1) ? a1 : a0, a.x, a.y, a.z, a.w, bq[ks][0], bq[ks][1]);
+    }
+    float* o0 = om + (2 * c) * C::kOmStride + 16 * mt + g;
+    o0[0] = a0[0] + a1[0];
+    o0[C::kOmStride] = a0[1] + a1[1];
+    o0[8] = a0[2] + a1[2];
+    o0[C::kOmStride + 8] = a0[3] + a1[3];
+  }
+  __syncthreads();
+  uint4* qf = reinterpret_cast<uint4*>(p.qprep + (size_t)unit * C::kPrep);
+  float* bias = reinterpret_cast<float*>(qf) + C::kQf / 4;
+  float* rowfac = bias + C::kBias / 4;
+  const float* qr = om + g * C::kOmStride;
+  // K step ks of the codes: int4 chunk ks / 2, channels 8c + (0, 4 | 1, 5) or (2, 6 | 3, 7);
+  // int8 channels 16 ks + 4c + (0, 2 | 1, 3)
+  auto chan = [&](int ks, int e) {
+    if constexpr (BITS == 4) return 32 * (ks >> 1) + 8 * c + ((ks & 1) ? 2 : 0) + (e >> 1) + ((e & 1) ? 4 : 0);
+    return 16 * ks + 4 * c + (e >> 1) + ((e & 1) ? 2 : 0);
+  };
+  float mx = 0.0f;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(qr + 16 * k + 4 * c);
+    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+  }
+  const int ex = row_exponent(mx);
+  const float f = pow2f(-ex), fhi = BITS == 4 ? f * 0.0625f : f;  // the odd pairs' codes stand 16 times too high
+  if (warp == 0 && c == 0) rowfac[g] = p.qfac * 16777216.0f * pow2f(ex);
+  constexpr float kOff = (BITS == 4 ? 8.0f : 128.0f) / 16777216.0f;
+  constexpr float kPair = BITS == 4 ? 16.0f : 1.0f;
+#pragma unroll
+  for (int t = 0; t < NC / kWarps; ++t) {
+    const int ch = warp + kWarps * t;
+    uint32_t h[4];
+    float sum[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      h[2 * k] = pack_half2(qr[chan(2 * ch + k, 0)] * f, qr[chan(2 * ch + k, 1)] * f);
+      h[2 * k + 1] = pack_half2(qr[chan(2 * ch + k, 2)] * fhi, qr[chan(2 * ch + k, 3)] * fhi);
+      const float2 a = __half22float2(u2h(h[2 * k])), b = __half22float2(u2h(h[2 * k + 1]));
+      sum[k] = -kOff * ((a.x + a.y) + kPair * (b.x + b.y));
+    }
+    auto start = [&](int grp, float v) {  // as both token rows of an accumulator of columns 2c', 2c' + 1
+      float* d = bias + (grp * 4 + (g >> 1)) * 4 + (g & 1);
+      d[0] = v;
+      d[2] = v;
+    };
+    if constexpr (G == 32) {
+      qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+      float v = sum[0] + sum[1];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      v += __shfl_xor_sync(0xffffffffu, v, 2);
+      if (c == 0) start(ch, v);
+    } else if constexpr (BITS == 4) {  // lane c's channels lie in half c / 2 of the chunk
+      const uint4 z = make_uint4(0, 0, 0, 0), q4 = make_uint4(h[0], h[1], h[2], h[3]);
+      qf[(2 * ch) * 32 + lane] = c < 2 ? q4 : z;
+      qf[(2 * ch + 1) * 32 + lane] = c < 2 ? z : q4;
+      float v = sum[0] + sum[1];
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      if ((c & 1) == 0) start(2 * ch + (c >> 1), v);
+    } else {
+      qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float v = sum[k];
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        if (c == 0) start(2 * ch + k, v);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- the kernel
 template <int D, int G, int BITS>
 __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
@@ -243,17 +369,16 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* ring = smem;
   float4* obuf = reinterpret_cast<float4*>(smem + C::kStages * C::kStage);
-  uint4* qf = reinterpret_cast<uint4*>(smem + C::kStages * C::kStage + C::kObuf);  // [fragment][lane]
-  float* om = reinterpret_cast<float*>(qf) + C::kQf / 4;                            // [8][kOmStride]
-  float* bias = om + C::kOm / 4;                                                    // [group][c][4]
-  float* wml = bias + C::kBias / 4;                                                 // [warp][m, l][8]
+  uint4* qf = reinterpret_cast<uint4*>(smem + C::kStages * C::kStage + C::kObuf);  // the unit's prepared query: [fragment][lane],
+  float* bias = reinterpret_cast<float*>(qf) + C::kQf / 4;                          // [group][c][4],
+  float* rowf = bias + C::kBias / 4;                                                // [8]
+  float* wml = rowf + kRows;                                                        // [warp][m, l][8]
   uint64_t* full = reinterpret_cast<uint64_t*>(wml + C::kMl / 4);
   uint64_t* empty = full + C::kStages;
   long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [5]
   long long* found = scan + kWarps + 1;                                // base of the first request, its index
-  int* flag = reinterpret_cast<int*>(found + 2);
   uint4* consts = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(full) + C::kBars - 16);
-  static_assert((2 * C::kStages + kWarps + 1 + 2 + 1) * 8 <= C::kBars - 16, "barrier region");
+  static_assert((2 * C::kStages + kWarps + 1 + 2) * 8 <= C::kBars - 16, "barrier region");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -265,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     *consts = make_uint4(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);  // -8 2^-24 and -128 2^-24, rows g and g + 8
   }
   grid_dep_launch();
-  grid_dep_wait();  // lengths, table, pages, queries and the workspace may come from the kernel before
+  // Only the prepared queries come from the kernel in front: it started this one when it had
+  // itself waited for everything before it.
 
   // ---- this CTA's piece of the line of tiles
   long long total = 0, mine = 0, upto = 0;
@@ -279,7 +405,10 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   Walk<kTile> w;
   w.at = min(total, per * blockIdx.x);
   w.end = min(total, w.at + per);
-  if (w.at >= w.end) return;
+  if (w.at >= w.end) {
+    grid_dep_wait();  // the kernel after this one counts on the one in front as well
+    return;
+  }
   if (p.B <= kThreads) {
     if (mine && w.at >= upto - mine && w.at < upto) {
       found[0] = upto - mine;
@@ -370,113 +499,37 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   const int g = lane >> 2, c = lane & 3, mi = lane >> 3;
   int n = 0;        // tiles taken so far
   bool ok = true;   // false after a wait ran out: the rest is passed over, every barrier still met
+  grid_dep_wait();
   while (w.next(p)) {
     const Request& r = w.r;
     const int h = w.u / r.rt, rt = w.u - h * r.rt;
     const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
+    const size_t unit = ((size_t)w.b * p.Hkv + h) * p.rt_max + rt;
     // row x of the tile: query token (rt * 8 + x) / Gq, head of the group the remainder
     auto q_row = [&](int x, int& tok, int& head) {
       const int y = rt * kRows + x;
       tok = y / p.Gq;
       head = h * p.Gq + (y - tok * p.Gq);
     };
-
-    // ---- (1) rotate the rows: X[channel][row] = Wq q, channel tiles over the warps
+    // ---- the unit's prepared query
     {
-      int tok, head;
-      q_row(g < nrows ? g : 0, tok, head);
-      const uint16_t* src = p.q + (long long)(r.qs + tok) * p.q_ts + (long long)head * p.q_hs;
-      uint32_t bq[MT][2];
+      constexpr int NV = (C::kPrep / 16 + kWarps * 32 - 1) / (kWarps * 32);
+      const uint4* src = reinterpret_cast<const uint4*>(p.qprep + unit * C::kPrep);
+      uint4 v[NV];
 #pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) : 0u;
+      for (int k = 0; k < NV; ++k) {
+        const int x = tid + k * kWarps * 32;
+        if (x < C::kPrep / 16) v[k] = __ldcg(src + x);
       }
+      consumers_sync();  // the segment before has been read to its end
 #pragma unroll
-      for (int t = 0; t < TW; ++t) {
-        const int mt = warp + kWarps * t;
-        float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ks = 0; ks < MT; ++ks) {
-          const uint4 a = __ldg(p.wq + (mt * MT + ks) * 32 + lane);
-          mma_16816((ks & 1) ? a1 : a0, a.x, a.y, a.z, a.w, bq[ks][0], bq[ks][1]);
-        }
-        float* o0 = om + (2 * c) * C::kOmStride + 16 * mt + g;
-        o0[0] = a0[0] + a1[0];
-        o0[C::kOmStride] = a0[1] + a1[1];
-        o0[8] = a0[2] + a1[2];
-        o0[C::kOmStride + 8] = a0[3] + a1[3];
+      for (int k = 0; k < NV; ++k) {
+        const int x = tid + k * kWarps * 32;
+        if (x < C::kPrep / 16) qf[x] = v[k];
       }
     }
     consumers_sync();
-    // ---- (2) the B fragments of the scores (column = row of the tile), normalised by 2^-e per
-    // row, and per group the start of its sum: minus what the codes' offset adds to it
-    float rowfac[2];  // of the scores' columns 2c, 2c + 1: back to base-2 scores
-    {
-      const float* qr = om + g * C::kOmStride;
-      // K step ks of the codes: int4 chunk ks / 2, channels 8c + (0, 4 | 1, 5) or (2, 6 | 3, 7);
-      // int8 channels 16 ks + 4c + (0, 2 | 1, 3)
-      auto chan = [&](int ks, int e) {
-        if constexpr (BITS == 4) return 32 * (ks >> 1) + 8 * c + ((ks & 1) ? 2 : 0) + (e >> 1) + ((e & 1) ? 4 : 0);
-        return 16 * ks + 4 * c + (e >> 1) + ((e & 1) ? 2 : 0);
-      };
-      float mx = 0.0f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(qr + 16 * k + 4 * c);
-        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-      }
-      const int ex = row_exponent(mx);
-      const float f = pow2f(-ex), fhi = BITS == 4 ? f * 0.0625f : f;  // the odd pairs' codes stand 16 times too high
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        rowfac[e] = p.qfac * 16777216.0f * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
-      constexpr float kOff = (BITS == 4 ? 8.0f : 128.0f) / 16777216.0f;
-      constexpr float kPair = BITS == 4 ? 16.0f : 1.0f;
-#pragma unroll
-      for (int t = 0; t < NC / kWarps; ++t) {
-        const int ch = warp + kWarps * t;
-        uint32_t h[4];
-        float sum[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          h[2 * k] = pack_half2(qr[chan(2 * ch + k, 0)] * f, qr[chan(2 * ch + k, 1)] * f);
-          h[2 * k + 1] = pack_half2(qr[chan(2 * ch + k, 2)] * fhi, qr[chan(2 * ch + k, 3)] * fhi);
-          const float2 a = __half22float2(u2h(h[2 * k])), b = __half22float2(u2h(h[2 * k + 1]));
-          sum[k] = -kOff * ((a.x + a.y) + kPair * (b.x + b.y));
-        }
-        auto start = [&](int grp, float v) {  // as both token rows of an accumulator of columns 2c', 2c' + 1
-          float* d = bias + (grp * 4 + (g >> 1)) * 4 + (g & 1);
-          d[0] = v;
-          d[2] = v;
-        };
-        if constexpr (G == 32) {
-          qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
-          float v = sum[0] + sum[1];
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          if (c == 0) start(ch, v);
-        } else if constexpr (BITS == 4) {  // lane c's channels lie in half c / 2 of the chunk
-          const uint4 z = make_uint4(0, 0, 0, 0), q4 = make_uint4(h[0], h[1], h[2], h[3]);
-          qf[(2 * ch) * 32 + lane] = c < 2 ? q4 : z;
-          qf[(2 * ch + 1) * 32 + lane] = c < 2 ? z : q4;
-          float v = sum[0] + sum[1];
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          if ((c & 1) == 0) start(2 * ch + (c >> 1), v);
-        } else {
-          qf[ch * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v = sum[k];
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if (c == 0) start(2 * ch + k, v);
-          }
-        }
-      }
-    }
-    consumers_sync();
+    const float rowfac[2] = {rowf[2 * c], rowf[2 * c + 1]};  // of the scores' columns 2c, 2c + 1
     // what rows 2c, 2c + 1 attend: tokens in (lo, hi]
     int hi[2], lo[2];
 #pragma unroll
@@ -782,13 +835,13 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       if (lane == 0) mbar_arrive(&empty[s]);
     }
 
-    // ---- (4) join the warps: M, L, and O = sum of o 2^(m - M), in true units
+    // ---- join the warps: M, L, and O = sum of o 2^(m - M), in true units; a quarter of the
+    // channels per warp
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       l_run[0] += __shfl_xor_sync(0xffffffffu, l_run[0], off);
       l_run[1] += __shfl_xor_sync(0xffffffffu, l_run[1], off);
     }
-    consumers_sync();  // q~ has been read
     const uint32_t bad_rows = __ballot_sync(0xffffffffu, bad_row);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -800,222 +853,225 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       }
     }
     consumers_sync();
-    float M[2], f[2];
+    float f[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      M[e] = -INFINITY;
+      float M = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) M[e] = fmaxf(M[e], wml[x * 2 * kRows + 2 * c + e]);
-      f[e] = m_run[e] == -INFINITY ? 0.0f : ex2_approx(m_run[e] - M[e]) * pow2f(24);
+      for (int x = 0; x < kWarps; ++x) M = fmaxf(M, wml[x * 2 * kRows + 2 * c + e]);
+      f[e] = m_run[e] == -INFINITY ? 0.0f : ex2_approx(m_run[e] - M) * pow2f(24);
     }
+    float own[TW][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const float odd = BITS == 4 ? 0.0625f : 1.0f;  // rows g + 8 hold the codes that stood 16 times too high
-      o[mt][0] *= f[0];
-      o[mt][1] *= f[1];
-      o[mt][2] *= f[0] * odd;
-      o[mt][3] *= f[1] * odd;
-    }
-    if (warp >= kWarps / 2) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        obuf[((warp - kWarps / 2) * MT + mt) * 32 + lane] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
-    }
-    consumers_sync();
-    if (warp < kWarps / 2) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float4& v = obuf[(warp * MT + mt) * 32 + lane];
-        const float4 u = v;
-        v = make_float4(o[mt][0] + u.x, o[mt][1] + u.y, o[mt][2] + u.z, o[mt][3] + u.w);
-      }
-    }
-    consumers_sync();
-    for (int x = tid; x < MT * 32; x += kWarps * 32) {
-      float4 v = obuf[x];
-#pragma unroll
-      for (int k = 1; k < kWarps / 2; ++k) {
-        const float4 u = obuf[k * MT * 32 + x];
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
-      }
-      const int mt = x >> 5, gg = (x & 31) >> 2, cc = x & 3;
-      // the channels of tile mt's rows g and g + 8
-      const int ch = BITS == 4 ? (mt >> 1) * 32 + 4 * gg + ((mt & 1) ? 2 : 0) : 16 * mt + 2 * gg;
-      float* d0 = om + (2 * cc) * C::kOmStride + ch;
-      *reinterpret_cast<float2*>(d0) = make_float2(v.x, v.z);
-      *reinterpret_cast<float2*>(d0 + C::kOmStride) = make_float2(v.y, v.w);
-    }
-    // M and L of row `row`, from the warps
-    auto joined = [&](int row, float& Mr, float& Lr) {
-      Mr = -INFINITY;
-      Lr = 0.0f;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) Mr = fmaxf(Mr, wml[x * 2 * kRows + row]);
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        const float mw = wml[x * 2 * kRows + row], lw = wml[x * 2 * kRows + kRows + row];
-        Lr += mw != -INFINITY ? lw * ex2_approx(mw - Mr) : lw;  // nothing attended: 0, or NaN where scores are
-      }
-    };
-    consumers_sync();
-    float* Lrow = wml + kWarps * kRows;  // the unit's L per row (over the warps' values, once they are read)
-    const bool whole = w.i0 == 0 && w.i1 == r.nt;
-    float Lr = 0.0f, Mr = 0.0f;
-    if (tid < kRows) joined(tid, Mr, Lr);
-    consumers_sync();
-    bool store = true;
-    if (whole) {
-      if (tid < kRows) Lrow[tid] = Lr;
-    } else {
-      // ---- (5) this CTA's partial of a unit that other CTAs share. The unit's tiles are
-      // [u0, u0 + nt) of the line; CTA x holds [x per, (x + 1) per) of it; a CTA's slot 0 is
-      // for the segment that starts its piece, slot 1 for the one that ends it.
-      const long long u0 = w.base + (long long)w.u * r.nt;
-      auto slot_of = [&](long long x) { return p.part + (2 * x + (x * per >= u0 ? 0 : 1)) * C::PART; };
-      float* mine_p = slot_of(blockIdx.x);
-      if (tid < kRows) {
-        __stcg(mine_p + tid, Mr);
-        __stcg(mine_p + kRows + tid, Lr);
-      }
-      for (int x = tid; x < kRows * D / 4; x += kWarps * 32) {
-        const int row = x / (D / 4), k = x - row * (D / 4);
-        __stcg(reinterpret_cast<float4*>(mine_p + 2 * kRows) + x,
-               *reinterpret_cast<const float4*>(om + row * C::kOmStride + 4 * k));
-      }
-      consumers_sync();
-      const long long xa = u0 / per, xb = (u0 + r.nt - 1) / per;
-      if (tid == 0) {
-        int* cnt = p.cnt + xa;  // no two units that are cut have the same first CTA
-        __threadfence();
-        const int before = atomicAdd(cnt, 1);
-        const int last = before == (int)(xb - xa);
-        if (last) {
-          *cnt = 0;  // every CTA of the unit has been here
-          __threadfence();
-        }
-        *flag = last;
-      }
-      consumers_sync();
-      store = *flag != 0;
-      if (store) {
-        // merge in CTA order: first the maxima and sums (a thread per row), then the outputs
-        const int np = (int)(xb - xa + 1);
-        if (tid < kRows) {
-          float Mx = -INFINITY, Lx = 0.0f;
-          for (int k = 0; k < np; ++k) Mx = fmaxf(Mx, __ldcg(slot_of(xa + k) + tid));
-          for (int k = 0; k < np; ++k) {
-            const float mk = __ldcg(slot_of(xa + k) + tid);
-            const float lk = __ldcg(slot_of(xa + k) + kRows + tid);
-            Lx += mk != -INFINITY ? lk * ex2_approx(mk - Mx) : lk;
-          }
-          Lrow[tid] = Lx;
-          wml[tid] = Mx;
-        }
-        consumers_sync();
-        for (int x = tid; x < kRows * D / 4; x += kWarps * 32) {
-          const int row = x / (D / 4), k4 = x - row * (D / 4);
-          const float Mx = wml[row];
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k0 = 0; k0 < np; k0 += 4) {  // four partials' loads in flight
-            float4 v[4];
-            float mk[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k0 + k < np) {
-                const float* sp = slot_of(xa + k0 + k);
-                mk[k] = __ldcg(sp + row);
-                v[k] = __ldcg(reinterpret_cast<const float4*>(sp + 2 * kRows) + x);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (k0 + k < np && mk[k] != -INFINITY) {
-                const float fk = ex2_approx(mk[k] - Mx);
-                acc.x = fmaf(fk, v[k].x, acc.x);
-                acc.y = fmaf(fk, v[k].y, acc.y);
-                acc.z = fmaf(fk, v[k].z, acc.z);
-                acc.w = fmaf(fk, v[k].w, acc.w);
-              }
-            }
-          }
-          *reinterpret_cast<float4*>(om + row * C::kOmStride + 4 * k4) = acc;
-        }
-      }
-    }
-    consumers_sync();
-    if (store) {
-      // ---- (6) out = Wo (o / L): samples as rows; o / L enters as an fp16 hi + lo pair
-      const float L = Lrow[g];
-      const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // nothing attended: zeros (NaN stays)
-      const float* orow = om + g * C::kOmStride;
-      float mx = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
-          mx = fmaxf(mx, fmaxf(fabsf(v.x * inv), fabsf(v.y * inv)));
-        }
-      }
-      const int ex = row_exponent(mx);
-      const float fx = inv * pow2f(-ex);
-      float acc[TW][4];
-#pragma unroll
-      for (int t = 0; t < TW; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
-        uint32_t bh[2], bl[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
-          const __half2 hv = __floats2half2_rn(v.x * fx, v.y * fx);
-          const float2 hf = __half22float2(hv);
-          bh[e] = h2u(hv);
-          bl[e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
-        }
-#pragma unroll
-        for (int t = 0; t < TW; ++t) {
-          const uint4 a = __ldg(p.wo + ((warp + kWarps * t) * MT + ks) * 32 + lane);
-          mma_16816(acc[t], a.x, a.y, a.z, a.w, bh[0], bh[1]);
-          mma_16816(acc[t], a.x, a.y, a.z, a.w, bl[0], bl[1]);
-        }
-      }
-      float fo[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
-      __half* xb = reinterpret_cast<__half*>(obuf);  // [8][D + 8]
+    for (int q = 0; q < kWarps; ++q) {
+      float4* dst = obuf + ((q * (kWarps - 1) + ((warp - q - 1) & (kWarps - 1))) * TW) * 32 + lane;
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
-        const int s0 = 16 * (warp + kWarps * t) + g;
-        __half* x0 = xb + (2 * c) * (D + 8) + s0;
-        x0[0] = __float2half_rn(acc[t][0] * fo[0]);
-        x0[D + 8] = __float2half_rn(acc[t][1] * fo[1]);
-        x0[8] = __float2half_rn(acc[t][2] * fo[0]);
-        x0[D + 8 + 8] = __float2half_rn(acc[t][3] * fo[1]);
-      }
-      consumers_sync();
-      for (int x = tid; x < nrows * (D / 8); x += kWarps * 32) {
-        const int row = x / (D / 8), k = x - row * (D / 8);
-        int tok, head;
-        q_row(row, tok, head);
-        *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
-            *reinterpret_cast<const uint4*>(xb + row * (D + 8) + 8 * k);
+        const float odd = BITS == 4 ? 0.0625f : 1.0f;  // rows g + 8 hold the codes that stood 16 times too high
+        float (&v)[4] = o[q * TW + t];
+        v[0] *= f[0];
+        v[1] *= f[1];
+        v[2] *= f[0] * odd;
+        v[3] *= f[1] * odd;
+        if (q != warp) {
+          dst[t * 32] = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) own[t][k] = v[k];
+        }
       }
     }
-    consumers_sync();  // om, wml and obuf are free for the next segment
+    consumers_sync();
+    // ---- the segment's partial: its unit's own when the unit is whole; else a slot of this CTA,
+    // the first for the segment that starts its piece, the second for one that ends it. The
+    // unit's tiles are [u0, u0 + nt) of the line; CTA x holds [x per, (x + 1) per) of it.
+    const bool whole = w.i0 == 0 && w.i1 == r.nt;
+    const long long u0 = w.base + (long long)w.u * r.nt, x0 = (long long)blockIdx.x * per;
+    const int slot = 2 * (int)blockIdx.x + (x0 >= u0 ? 0 : 1);
+    float* dst = whole ? p.part_unit + unit * C::PART : p.part + (size_t)slot * C::PART;
+    if (tid < kRows) {
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) M = fmaxf(M, wml[x * 2 * kRows + tid]);
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) {
+        const float mw = wml[x * 2 * kRows + tid], lw = wml[x * 2 * kRows + kRows + tid];
+        L += mw != -INFINITY ? lw * ex2_approx(mw - M) : lw;  // nothing attended: 0, or NaN where scores are
+      }
+      dst[tid] = M;
+      dst[kRows + tid] = L;
+    }
+    if (tid == 0 && w.i0 == 0)
+      p.desc[unit] = whole ? make_int2(0, 0) : make_int2(slot, (int)((u0 + r.nt - 1) / per - blockIdx.x) + 1);
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      const float4* src = obuf + (warp * (kWarps - 1) * TW + t) * 32 + lane;
+#pragma unroll
+      for (int k = 0; k < kWarps - 1; ++k) {
+        const float4 v = src[k * TW * 32];
+        own[t][0] += v.x;
+        own[t][1] += v.y;
+        own[t][2] += v.z;
+        own[t][3] += v.w;
+      }
+      const int mt = warp * TW + t;  // the channels of tile mt's rows g and g + 8
+      const int ch = BITS == 4 ? (mt >> 1) * 32 + 4 * g + ((mt & 1) ? 2 : 0) : 16 * mt + 2 * g;
+      float* d0 = dst + 2 * kRows + (2 * c) * D + ch;
+      if (2 * c < nrows) *reinterpret_cast<float2*>(d0) = make_float2(own[t][0], own[t][2]);
+      if (2 * c + 1 < nrows) *reinterpret_cast<float2*>(d0 + D) = make_float2(own[t][1], own[t][3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- last kernel: partials to outputs
+// Block u: the partials of unit u in CTA order, then out = Wo (o / l) with o as an fp16 hi + lo
+// pair (samples as rows, query rows as columns). A few KB per unit through L2: bound by the
+// latency of the chain lengths -> partials -> output; the matrix is loaded before the wait for
+// the main kernel at D = 128.
+template <int D, int BITS>
+__global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int MT = D / 16, TW = MT / kWarps, ST = D + 4, PART = 2 * kRows + kRows * D;
+  __shared__ __align__(16) float om[kRows * ST];
+  __shared__ __align__(16) __half xb[kRows * (D + 8)];
+  __shared__ float red[2][16][kRows], wts[kMaxCtas * kRows];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  constexpr bool kAhead = D == 128;
+  uint4 wf[kAhead ? TW : 1][MT];
+  auto load_matrix = [&](int t, uint4 (&f)[MT]) {
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) f[ks] = __ldg(p.wo + ((warp + kWarps * t) * MT + ks) * 32 + lane);
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int t = 0; t < TW; ++t) load_matrix(t, wf[t]);
+  }
+  grid_dep_launch();
+  grid_dep_wait();
+  const Request r = request_of<128>(p, b);
+  const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
+  if (nrows <= 0) return;
+  const int2 d = __ldcg(p.desc + unit);
+  const int np = max(1, min(d.y, kMaxCtas));
+  // the first CTA's slot, then the first slots of the CTAs after it
+  auto part = [&](int k) {
+    return d.y == 0 ? p.part_unit + (size_t)unit * PART : p.part + (size_t)(k == 0 ? d.x : (d.x & ~1) + 2 * k) * PART;
+  };
+  {
+    const int row = tid & 7, k0 = tid >> 3;
+    float M = -INFINITY, L = 0.0f;
+    for (int k = k0; k < np; k += 16) M = fmaxf(M, __ldcg(part(k) + row));
+    red[0][k0][row] = M;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) M = fmaxf(M, red[0][k][row]);
+    for (int k = k0; k < np; k += 16) {
+      const float m = __ldcg(part(k) + row), l = __ldcg(part(k) + kRows + row);
+      const float f = m != -INFINITY ? ex2_approx(m - M) : 0.0f;
+      L += m != -INFINITY ? l * f : l;
+      wts[k * kRows + row] = f;
+    }
+    red[1][k0][row] = L;
+    __syncthreads();
+  }
+  {
+    constexpr int NX = kRows * D / 4 / (kWarps * 32);  // float4 values of a thread
+    float4 acc[NX];
+#pragma unroll
+    for (int x = 0; x < NX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8 / NX > 2 ? 8 / NX : 2;         // partials in flight
+    for (int k0 = 0; k0 < np; k0 += U) {
+      float4 v[U][NX];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+          if (k0 + k < np) v[k][x] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + 2 * kRows) + tid + x * kWarps * 32);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          const int row = (tid + x * kWarps * 32) / (D / 4);
+          const float f = k0 + k < np ? wts[(k0 + k) * kRows + row] : 0.0f;
+          if (f != 0.0f) {
+            acc[x].x = fmaf(f, v[k][x].x, acc[x].x);
+            acc[x].y = fmaf(f, v[k][x].y, acc[x].y);
+            acc[x].z = fmaf(f, v[k][x].z, acc[x].z);
+            acc[x].w = fmaf(f, v[k][x].w, acc[x].w);
+          }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const int y = tid + x * kWarps * 32, row = y / (D / 4);
+      // rows behind the tile's last were not written
+      *reinterpret_cast<float4*>(om + row * ST + 4 * (y - row * (D / 4))) = row < nrows ? acc[x] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __syncthreads();
+  float L = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) L += red[1][k][g];
+  const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // nothing attended: zeros (NaN stays)
+  const float* orow = om + g * ST;
+  float mx = 0.0f;
+#pragma unroll
+  for (int x = 0; x < D / 16; ++x) {
+    const float4 v = *reinterpret_cast<const float4*>(orow + 16 * x + 4 * c);
+    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+  }
+  const int ex = row_exponent(mx * inv);
+  const float fx = inv * pow2f(-ex);
+  float acc[TW][4] = {};
+  uint32_t bh2[MT][2], bl2[MT][2];
+#pragma unroll
+  for (int ks = 0; ks < MT; ++ks)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
+      const __half2 hv = __floats2half2_rn(v.x * fx, v.y * fx);
+      const float2 hf = __half22float2(hv);
+      bh2[ks][e] = h2u(hv);
+      bl2[ks][e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
+    }
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    if constexpr (!kAhead) load_matrix(t, wf[0]);
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) {
+      const uint4 a = wf[kAhead ? t : 0][ks];
+      mma_16816(acc[t], a.x, a.y, a.z, a.w, bh2[ks][0], bh2[ks][1]);
+      mma_16816(acc[t], a.x, a.y, a.z, a.w, bl2[ks][0], bl2[ks][1]);
+    }
+  }
+  float fo[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    __half* x0 = xb + (2 * c) * (D + 8) + 16 * (warp + kWarps * t) + g;
+    x0[0] = __float2half_rn(acc[t][0] * fo[0]);
+    x0[D + 8] = __float2half_rn(acc[t][1] * fo[1]);
+    x0[8] = __float2half_rn(acc[t][2] * fo[0]);
+    x0[D + 8 + 8] = __float2half_rn(acc[t][3] * fo[1]);
+  }
+  __syncthreads();
+  for (int x = tid; x < nrows * (D / 8); x += kWarps * 32) {
+    const int row = x / (D / 8), k = x - row * (D / 8);
+    const int y = rt * kRows + row, tok = y / p.Gq, head = h * p.Gq + (y - tok * p.Gq);
+    *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
+        *reinterpret_cast<const uint4*>(xb + row * (D + 8) + 8 * k);
   }
 }
 
 // ---------------------------------------------------------------- host side
 constexpr int kMinTilesPerCta = 2;
-// Workspace: a counter per CTA, at the start whatever the geometry (calls of different
-// geometries, and the prompt kernel, may follow one another in one workspace and find the
-// counters zero), then the partials.
-constexpr size_t kCntBytes = (kMaxCtas * 4 + 255) / 256 * 256;
+// Workspace: the partials of cut units, then per unit its prepared query, partial and
+// description. Nothing in it outlives a call.
 constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (2 * kRows + kRows * kMaxD) * 4;
+// of a unit, for every form of a head_dim: fragments, starts and factors; m, l, o; description
+constexpr size_t prep_bytes(int D) { return (size_t)(D / 16) * 512 + (D / 16) * 64 + kRows * 4; }
+constexpr size_t unit_bytes(int D) { return prep_bytes(D) + (2 * kRows + kRows * D) * 4 + 16; }
 // Query rows of a request from which on the prompt kernel takes a call.
 constexpr int kPromptRows = 48;
 
@@ -1059,16 +1115,18 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.page_shift = a.page_shift;
   p.window = a.window;
   p.min_tiles = kMinTilesPerCta;
-  char* ws = reinterpret_cast<char*>(a.ws);
-  p.cnt = reinterpret_cast<int*>(ws);
-  p.part = reinterpret_cast<float*>(ws + kCntBytes);
+  const size_t units = (size_t)a.B * a.Hkv * p.rt_max;
+  static_assert(C::kPrep <= prep_bytes(D), "workspace");
+  p.part = reinterpret_cast<float*>(a.ws);
+  p.part_unit = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + kPartBytes);
+  p.qprep = reinterpret_cast<uint8_t*>(p.part_unit + units * C::PART);
+  p.desc = reinterpret_cast<int2*>(p.qprep + units * C::kPrep);
   // no more CTAs than pieces of min_tiles tiles if every request were as long as it may be
-  const long long most = (long long)a.B * a.Hkv * p.rt_max * std::max(1, (p.max_kv + C::kTile - 1) / C::kTile);
+  const long long most = (long long)units * std::max(1, (p.max_kv + C::kTile - 1) / C::kTile);
   const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kCtas);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(slots, (most + p.min_tiles - 1) / p.min_tiles));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = strm;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1076,7 +1134,19 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e = allow_smem<attend_paged_kernel<D, G, BITS>>(a.pk->device, C::kSmem);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, attend_paged_kernel<D, G, BITS>, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, rotate_paged_kernel<D, G, BITS>, p);
+  if (e == cudaSuccess) {
+    cfg.gridDim = dim3((unsigned)std::min<long long>(slots, (most + p.min_tiles - 1) / p.min_tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    e = cudaLaunchKernelEx(&cfg, attend_paged_kernel<D, G, BITS>, p);
+  }
+  if (e == cudaSuccess) {
+    cfg.gridDim = dim3((unsigned)units);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, join_paged_kernel<D, BITS>, p);
+  }
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("attend_paged launch: ") + cudaGetErrorString(e));
   return KVQ_OK;
 }
@@ -1085,12 +1155,14 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
 
 bool paged_uses_prompt(int Hq, int Hkv, int max_q_len) { return (long long)max_q_len * (Hq / Hkv) >= kPromptRows; }
 
-size_t paged_workspace_bytes(int Hq, int Hkv, int max_q_len) {
-  return kCntBytes + (paged_uses_prompt(Hq, Hkv, max_q_len) ? std::max(kPartBytes, prompt_part_bytes()) : kPartBytes);
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
+  if (paged_uses_prompt(Hq, Hkv, max_q_len)) return prompt_part_bytes();
+  const size_t rt = ((size_t)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv) + kRows - 1) / kRows;
+  return kPartBytes + (size_t)B * Hkv * rt * unit_bytes(D);
 }
 
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s) {
-  if (paged_uses_prompt(a.Hq, a.Hkv, a.max_q_len)) return launch_attend_prompt(a, reinterpret_cast<char*>(a.ws) + kCntBytes, s);
+  if (paged_uses_prompt(a.Hq, a.Hkv, a.max_q_len)) return launch_attend_prompt(a, a.ws, s);
   return dispatch_dgb(a.pk->D, a.pk->G, a.pk->bits, [&](auto d, auto g, auto b) {
     return run_paged<decltype(d)::value, decltype(g)::value, decltype(b)::value>(a, s);
   });

@@ -226,7 +226,7 @@ struct PagedAttendHost {
   void* ws;
   size_t ws_bytes;
 };
-size_t paged_workspace_bytes(int Hq, int Hkv, int max_q_len);
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len);
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s);
 uint32_t paged_error_flags(bool clear);
 // Rows (query tokens x heads of a KV head's group) of a request above which the prompt kernel

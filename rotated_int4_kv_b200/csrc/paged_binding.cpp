@@ -418,8 +418,7 @@ PyObject* attend_paged(PyObject*, PyObject* const* a, Py_ssize_t na) {
     const at::Tensor* ws = &made_ws;
     if (a[15] == Py_None) {
       const size_t need = kvq_paged_workspace_size(std::max(B, 1), Hq, (int)std::max<int64_t>(k.H, 1), (int)D, n, (int)std::max<int64_t>(max_q, 1));
-      made_ws = at::zeros({(int64_t)std::max<size_t>(need, 16)},
-                          at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev));
+      made_ws = fresh({(int64_t)std::max<size_t>(need, 16)}, at::kByte, dev);
     } else {
       ws = &cuda(a[15], "workspace", at::kByte, dev);
     }

@@ -90,10 +90,10 @@ def paged_workspace_size(B: int, Hq: int, Hkv: int, head_dim: int, n_tokens: int
 
 def make_paged_workspace(B: int, Hq: int, Hkv: int, head_dim: int, n_tokens: int = None, max_q_len: int = 1,
                          device=None, stream=None) -> torch.Tensor:
-    """A zero-initialised workspace for :func:`attend_paged` with up to ``B`` requests, ``n_tokens``
+    """A workspace for :func:`attend_paged` with up to ``B`` requests, ``n_tokens``
     query tokens and ``max_q_len`` of one request. Calls that may overlap need one each."""
     n = max(16, paged_workspace_size(B, Hq, Hkv, head_dim, B if n_tokens is None else n_tokens, max_q_len))
-    return _new(torch.zeros, n, torch.uint8, device or torch.device("cuda"), stream)
+    return _new(torch.empty, n, torch.uint8, device or torch.device("cuda"), stream)
 
 
 def attend_paged(pk: Plan, pv: Plan, q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, q_starts=None,

@@ -364,7 +364,7 @@ def test_attend_paged_workspace_serves_any_geometry(kvq):
     cs = [Cache(kvq, [900, 33], [1, 1], *h, 32, 4, "srft", 16) for h in HEADS]
     cs += [Cache(kvq, [900, 333], [60, 150], *h, 32, 4, "srft", 16) for h in HEADS[:4]]
     n = max(kvq.paged_workspace_size(2, h[0], h[1], h[2], 400, 400) for h in HEADS)
-    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ws = torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")   # any contents will do
     for _ in range(2):
         for c in cs:
             c.check(c.run(kvq, max_q_len=max(c.q_lens), workspace=ws))
