@@ -385,8 +385,8 @@ kvq_status kvq_attend_decode_ref(const uint16_t* q, const uint16_t* k, const uin
  * K and V pages share one table. Lengths, tables and slots are device data, so the host
  * checks cannot see them; what a kernel does with an entry outside its range is said at
  * each call, and none reads or writes outside the buffers given. Every call only launches
- * kernels on `stream` (kvq_attend_paged two or three, kvq_encode_paged one per two jobs, the
- * others one) and may be captured into a CUDA graph.
+ * kernels on `stream` (kvq_attend_paged two or three, kvq_encode_paged one per two jobs,
+ * kvq_page_plan one or two, the others one) and may be captured into a CUDA graph.
  */
 
 /*
@@ -454,7 +454,7 @@ kvq_status kvq_encode_paged(const kvq_paged_encode_job* jobs, int njobs, int n, 
 
 /*
  * kvq_decode_paged -- kvq_decode of the rows at n slots (any order, repeats allowed):
- * out fp16 [n, Hkv, D]; a slot outside the pages gives zeros. n * Hkv <= 2^31 - 129.
+ * out fp16 [n, Hkv, D]; a slot outside the pages gives zeros. n * Hkv <= 2^31 - 1024.
  * Always the tensor-core decode. Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, DEVICE, CUDA.
  */
 kvq_status kvq_decode_paged(const kvq_plan* plan, const uint8_t* codes, const uint16_t* scales, int num_pages,

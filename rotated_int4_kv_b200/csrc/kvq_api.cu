@@ -806,7 +806,7 @@ kvq_status kvq_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint1
     if (n < 0) return fail(KVQ_ERR_INVALID_ARG, "decode_paged: n < 0");
     kvq_status st = check_pages("decode_paged", num_pages, page_size, Hkv);
     if (st != KVQ_OK) return st;
-    if ((long long)n * Hkv > 0x7fffffffll - 128) return fail(KVQ_ERR_UNSUPPORTED, "decode_paged: n * Hkv too large");
+    if ((long long)n * Hkv > 0x7fffffffll - 1023) return fail(KVQ_ERR_UNSUPPORTED, "decode_paged: n * Hkv too large");
     if (n == 0) return KVQ_OK;
     if (!codes || !scales || !slots || !out) return fail(KVQ_ERR_INVALID_ARG, "decode_paged: null buffer");
     if (!kvq::aligned16(codes) || !kvq::aligned16(scales) || !kvq::aligned16(out))

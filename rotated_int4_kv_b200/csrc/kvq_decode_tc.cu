@@ -20,7 +20,7 @@
 // (T_box * BH_box = 128 rows, T_box the power of two >= n up to 128), so that its code
 // rows arrive by one TMA tensor load and its output rows leave by TMA tensor stores.
 // Pages (PG): the rows are (token, head) pairs of a slot map, scattered over the cache, so
-// each dequantiser thread brings its own row's codes and scales by async copies of 16 (8)
+// each dequantiser warp brings its rows' codes and scales by async copies of 16 (8)
 // bytes, a tile ahead of their use; a slot outside the pages reads as zeros.
 // Roles (one CTA per SM, persistent over a contiguous range of tiles):
 //   warp 0      TMA: W_dec (resident for the whole launch, 32 or 128 KB), then the code
@@ -84,14 +84,17 @@ struct DtCfg {
   // the dequantisers' scale rows of the next tile, one per vector (async copies), where the
   // shared memory allows; otherwise they load them into registers
   template <int G>
-  static constexpr int kScaleSlot = (kBase + kDtRows * (D / G) * 2 <= kLimit) ? kDtRows * (D / G) * 2 : 0;
+  static constexpr int kScaleSlot = (kBase + kDtRows * (D / G) * 2 + kDtRows * 4 <= kLimit) ? kDtRows * (D / G) * 2 : 0;
   // 1024 bytes of slack for aligning the base where they fit; without them the kernel checks
   // that the base is 1024-byte aligned and refuses to run (error flag) if it is not
   template <int G>
-  static constexpr int kSlack = (kBase + kScaleSlot<G> + 1024 <= kLimit) ? 1024 : 0;
+  static constexpr int kSlack = (kBase + kScaleSlot<G> + kDtRows * 4 + 1024 <= kLimit) ? 1024 : 0;
   template <int G>
   static constexpr int kSmem = kBase + kScaleSlot<G> + kSlack<G>;
-  static_assert(kBase <= kLimit, "shared memory");
+  // pages: the slot-map entries of the next tile but one, behind everything else
+  template <int G>
+  static constexpr int kSmemPaged = kSmem<G> + kDtRows * 4;
+  static_assert(kBase + kDtRows * 4 <= kLimit, "shared memory");
 };
 
 struct DtParams {
@@ -106,21 +109,36 @@ struct DtParams {
   const uint8_t* codes;
   long long n_slots;
   int H, page_shift;
+  int tok_step, head_step;  // kDtRows / H, kDtRows % H
 };
 
 // The cache row of row (bh, t) of the job, -1 where there is none.
-template <bool PG>
 __device__ __forceinline__ long long dt_cache_row(const DtParams& P, int bh, int t) {
-  if (!(bh < P.BH && t < P.n)) return -1;
-  if constexpr (PG) {
-    const int tok = t / P.H, slot = __ldg(P.slots + tok);
-    if (slot < 0 || slot >= P.n_slots) return -1;
-    return (((long long)(slot >> P.page_shift) * P.H + (t - tok * P.H)) << P.page_shift) +
-           (slot & ((1 << P.page_shift) - 1));
-  } else {
-    return (long long)bh * P.T_cap + P.t0 + t;
-  }
+  return bh < P.BH && t < P.n ? (long long)bh * P.T_cap + P.t0 + t : -1;
 }
+
+// Pages: a thread's row from tile to tile, as token and head (without a division per tile).
+struct DtCursor {
+  int t, tok, head;
+  __device__ __forceinline__ void start(const DtParams& P, int t_) {
+    t = t_;
+    tok = t / P.H;
+    head = t - tok * P.H;
+  }
+  __device__ __forceinline__ void next(const DtParams& P) {
+    t += kDtRows;
+    tok += P.tok_step;
+    head += P.head_step;
+    if (head >= P.H) {
+      head -= P.H;
+      ++tok;
+    }
+  }
+  __device__ __forceinline__ long long cache_row(const DtParams& P, int slot) const {
+    if (t >= P.n || slot < 0 || slot >= P.n_slots) return -1;
+    return (((long long)(slot >> P.page_shift) * P.H + head) << P.page_shift) + (slot & ((1 << P.page_shift) - 1));
+  }
+};
 
 // A tile's first (b, h) and first token (relative to t0).
 __device__ __forceinline__ void dt_tile_origin(const DtParams& P, int tile, int& bh0, int& tt0) {
@@ -202,18 +220,22 @@ __device__ __forceinline__ uint4 code_piece(const uint8_t* slot, int r, int c) {
   }
 }
 
-// Async copies of a cache row's codes into row r of a code slot (the layout of code_piece).
+// Async copies of the codes of a warp's 32 cache rows (lane l holds row l's) into rows
+// 32 q .. 32 q + 31 of a code slot (the layout of code_piece): neighbouring lanes take
+// neighbouring 16-byte pieces of a row.
 template <int D, int BITS>
-__device__ __forceinline__ void cp_async_codes(uint8_t* slot, int r, const DtParams& P, long long crow) {
+__device__ __forceinline__ void cp_async_codes(uint8_t* slot, int q, int lane, const DtParams& P, long long crow) {
   using C = DtCfg<D, BITS>;
-  const bool in = crow >= 0;
-  const uint8_t* src = in ? P.codes + crow * C::kRowBytes : P.codes;
+  constexpr int PC = C::kRowBytes / 16;
 #pragma unroll
-  for (int c = 0; c < C::kRowBytes / 16; ++c) {
+  for (int k = 0; k < PC; ++k) {
+    const int l = (32 * k + lane) / PC, c = lane % PC, r = 32 * q + l;
+    const long long row = __shfl_sync(0xffffffffu, crow, l);
+    const bool in = row >= 0;
+    const uint8_t* src = in ? P.codes + row * C::kRowBytes + 16 * c : P.codes;
     const int off = C::kBoxRow == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
                                      : (c >> 3) * (kDtRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot + off)), "l"(src + 16 * c),
-                 "r"(in ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot + off)), "l"(src), "r"(in ? 16 : 0)
                  : "memory");
   }
 }
@@ -367,7 +389,16 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     auto row_of = [&](int i) {
       int bh0, tt0;
       dt_tile_origin(P, t_begin + i, bh0, tt0);
-      return dt_cache_row<PG>(P, bh0 + bh_l, tt0 + t_l);
+      return dt_cache_row(P, bh0 + bh_l, tt0 + t_l);
+    };
+    // pages: this row's slot-map entry comes by an async copy as well, two tiles ahead
+    DtCursor cur;
+    int32_t* slot_s = reinterpret_cast<int32_t*>(sm + C::template kSmem<G> - C::template kSlack<G>) + row;
+    auto fetch_slot = [&](const DtCursor& k) {
+      const bool in = k.t < P.n;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(slot_s)), "l"(P.slots + (in ? k.tok : 0)),
+                   "r"(in ? 4 : 0)
+                   : "memory");
     };
     auto next_scales = [&](long long crow) {
       if constexpr (kSS > 0) {
@@ -379,6 +410,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     // (pages: the wait also covers this row's codes of the same tile)
     auto take_scales = [&](long long crow, uint32_t (&sc)[NS]) {
       if constexpr (kSS > 0 || PG) cp_async_wait_all();
+      if constexpr (PG) __syncwarp();  // the warp's codes came by all its lanes
       if constexpr (kSS > 0) {
 #pragma unroll
         for (int j = 0; j < NS; ++j) sc[j] = srow[j];
@@ -386,14 +418,20 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
         load_scales<NS>(P, crow, sc);
       }
     };
-    // the cache row of tile i, and (pages: a slot map away) that of tile i + 1
-    long long crow = ntile > 0 ? row_of(0) : -1, nrow = -1;
+    long long crow = -1;  // the cache row of tile i + 1
     uint32_t sg[2 * NS];
     if (ntile > 0) {
       uint32_t sc[NS];
-      if constexpr (PG) cp_async_codes<D, BITS>(sC, row, P, crow);
+      if constexpr (PG) {
+        cur.start(P, t_begin * kDtRows + row);
+        crow = cur.cache_row(P, cur.t < P.n ? __ldg(P.slots + cur.tok) : -1);
+        cp_async_codes<D, BITS>(sC, warp - 2, lane, P, crow);
+        cur.next(P);
+        fetch_slot(cur);
+      } else {
+        crow = row_of(0);
+      }
       next_scales(crow);
-      if (ntile > 1) nrow = row_of(1);
       take_scales(crow, sc);
       factors(sc, sg);
     }
@@ -406,15 +444,22 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
           break;
         }
       }
-      crow = nrow;
       if (i + 1 < ntile) {
-        // pages: this thread alone reads and writes its row of the slots; the slot that the
-        // next tile's codes go to was read in the tile before this one
-        if constexpr (PG && C::kCSlots == 2)
-          cp_async_codes<D, BITS>(sC + ((i + 1) % 2) * C::kCodeTile, row, P, crow);
+        if constexpr (PG) {
+          crow = cur.cache_row(P, *slot_s);
+          cur.next(P);
+          fetch_slot(cur);
+          // this warp alone reads and writes its rows of the slots; the slot that the next
+          // tile's codes go to was read in the tile before this one
+          if constexpr (C::kCSlots == 2) {
+            __syncwarp();
+            cp_async_codes<D, BITS>(sC + ((i + 1) % 2) * C::kCodeTile, warp - 2, lane, P, crow);
+          }
+        } else {
+          crow = row_of(i + 1);
+        }
         next_scales(crow);
       }
-      if (i + 2 < ntile) nrow = row_of(i + 2);
       bool ok = true;
       // CPS K chunks per step: one wait for their ring slots, one proxy fence and CPS
       // arrivals per step, their conversions interleaved (more independent work per warp).
@@ -502,7 +547,10 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
         // the next tile's factors, after this tile's last arrival: a release arrival waits
         // for every load of its thread still in flight
         // (pages with one code slot: its values are all in use by now, the next ones may come)
-        if constexpr (PG && C::kCSlots == 1) cp_async_codes<D, BITS>(sC, row, P, crow);
+        if constexpr (PG && C::kCSlots == 1) {
+          __syncwarp();
+          cp_async_codes<D, BITS>(sC, warp - 2, lane, P, crow);
+        }
         uint32_t sn[NS];
         take_scales(crow, sn);
         factors(sn, sg);
@@ -522,11 +570,25 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     const int w_bh = (32 * q) >> P.t_shift, w_t = (32 * q) & (P.T_box - 1);
     int nst = 0;  // staging tiles written by this warp
     float alpha = 1.0f;  // 2^e of this thread's row; the next tile's is formed when a tile ends
-    if (ntile > 0) {
+    auto row_of = [&](int i) {
       int bh0, tt0;
+      dt_tile_origin(P, t_begin + i, bh0, tt0);
+      return dt_cache_row(P, bh0 + bh_l, tt0 + t_l);
+    };
+    // pages: the next tile's cache row is a slot-map entry away, which is read a tile early
+    DtCursor cur;
+    int nslot = -1;
+    auto slot_of = [&](const DtCursor& k) { return k.t < P.n ? __ldg(P.slots + k.tok) : -1; };
+    if (ntile > 0) {
       uint32_t sc[NS];
-      dt_tile_origin(P, t_begin, bh0, tt0);
-      load_scales<NS>(P, dt_cache_row<PG>(P, bh0 + bh_l, tt0 + t_l), sc);
+      if constexpr (PG) {
+        cur.start(P, t_begin * kDtRows + row);
+        load_scales<NS>(P, cur.cache_row(P, slot_of(cur)), sc);
+        cur.next(P);
+        nslot = slot_of(cur);
+      } else {
+        load_scales<NS>(P, row_of(0), sc);
+      }
       row_norm<NS>(sc, alpha);
     }
     for (int i = 0; i < ntile; ++i) {
@@ -535,9 +597,13 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       dt_tile_origin(P, t_begin + i, bh0, tt0);
       uint32_t sn[NS];  // the next tile's scales (the epilogue is not on the critical path)
       if (i + 1 < ntile) {
-        int nb, nt;
-        dt_tile_origin(P, t_begin + i + 1, nb, nt);
-        load_scales<NS>(P, dt_cache_row<PG>(P, nb + bh_l, nt + t_l), sn);
+        if constexpr (PG) {
+          load_scales<NS>(P, cur.cache_row(P, nslot), sn);
+          cur.next(P);
+          nslot = slot_of(cur);
+        } else {
+          load_scales<NS>(P, row_of(i + 1), sn);
+        }
       }
       const bool any = bh0 + w_bh < P.BH && tt0 + w_t < P.n;  // some row of the warp's box is in the job
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], (i >> 1) & 1))) {
@@ -691,12 +757,12 @@ namespace {
 template <int D, int G, int BITS>
 cudaError_t dt_launch_paged(const DtParams& P, int device, cudaStream_t strm) {
   using C = DtCfg<D, BITS>;
-  const cudaError_t e = allow_smem<decode_tc_kernel<D, BITS, G, true>>(device, C::template kSmem<G>);
+  const cudaError_t e = allow_smem<decode_tc_kernel<D, BITS, G, true>>(device, C::template kSmemPaged<G>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(std::min(P.ntiles, num_sms(device)));
   cfg.blockDim = dim3(kDtThreads);
-  cfg.dynamicSmemBytes = C::template kSmem<G>;
+  cfg.dynamicSmemBytes = C::template kSmemPaged<G>;
   cfg.stream = strm;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -725,6 +791,8 @@ kvq_status launch_decode_paged(const kvq_plan* p, const uint8_t* codes, const ui
   P.n_slots = (long long)num_pages << page_shift;
   P.H = H;
   P.page_shift = page_shift;
+  P.tok_step = kDtRows / H;
+  P.head_step = kDtRows % H;
   const uint64_t bd[2] = {(uint64_t)D, (uint64_t)D};
   const uint64_t bs[1] = {(uint64_t)D * 2};
   const uint32_t bb[2] = {64u, (uint32_t)D};

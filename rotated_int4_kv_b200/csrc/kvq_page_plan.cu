@@ -9,13 +9,14 @@
 // position kv + j, slot = page * P + position % P. Integers only; every output is a
 // function of the inputs alone (no atomics), so two calls on the same inputs agree.
 //
-// The work is a few hundred KB at most, so the time is latency: one launch, one
-// thread-block cluster. Every CTA scans all requests itself (B <= 16384: a block scan of at
-// most 16 requests per thread) into its shared memory, a cluster barrier then separates all
-// reads of the lengths and of the free-list head from the writes that may alias them, and
-// the cluster's warps share the table entries (a warp per request) and the tokens (32 at a
-// time, the owning request by binary search over the starts in shared memory). A split into
-// a scan kernel and a fill kernel would cost a second launch.
+// The work is a few hundred KB at most, so the time is latency: every CTA scans all requests
+// itself (B <= 16384: a block scan of at most 16 requests per thread) into its shared memory,
+// and the CTAs share the table entries (a warp per request) and the tokens (one per thread,
+// the owning request by binary search over the starts in shared memory). Lengths and the
+// free-list head may be updated in place: a CTA must not overwrite what another has yet to
+// read, so with more than one CTA they are then written by a second launch of one CTA. 2048
+// requests with 190 thousand tokens: 33 us with one cluster of 8 CTAs and a cluster barrier in
+// place of the second launch, 8 us with a CTA per 2048 tokens.
 #include <algorithm>
 
 #include "kvq_internal.h"
@@ -26,8 +27,7 @@ namespace kvq {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCluster = 8;       // CTAs at most (portable cluster size)
-constexpr int kPlanPerCta = 4096;     // tokens or requests per CTA before another joins
+constexpr int kPlanPerCta = 2048;     // tokens or requests per CTA before another joins
 
 struct PagePlanParams {
   const int32_t* kv_lens;
@@ -43,6 +43,7 @@ struct PagePlanParams {
   int32_t* info;
   long long table_stride;
   int B, max_pages, n_free, page_shift, n_slots;
+  bool fill, move;  // write tables, slots, starts and info; write lengths and the head
 };
 
 __device__ __forceinline__ int32_t sat32(long long v) { return v > 0x7fffffffll ? 0x7fffffff : (int32_t)v; }
@@ -128,14 +129,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     if (ref) atomicAdd(&refused, ref);
   }
   __syncthreads();
-  // every CTA has read the lengths and the head: from here on they may be overwritten
-  if (gridDim.x > 1) {
-    cluster_arrive_relaxed();
-    cluster_wait();
-  }
   const int nthreads = (int)gridDim.x * kPlanThreads, gt = (int)blockIdx.x * kPlanThreads + tid;
-  if (gt == 0) {
-    p.free_head_out[0] = head + (int)served_pages;
+  if (gt == 0 && p.move) p.free_head_out[0] = head + (int)served_pages;
+  if (gt == 0 && p.fill) {
     p.q_starts[p.B] = sat32(total);
     p.info[0] = sat32(total);
     p.info[1] = (int)served_pages;
@@ -146,9 +142,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   // request has in full (its length fits its table, so it is below the saturation)
   auto q_of = [&](int b) { return (b + 1 < p.B ? (long long)s_start[b + 1] : (long long)sat32(total)) - s_start[b]; };
   for (int b = gt; b < p.B; b += nthreads) {
-    p.q_starts[b] = s_start[b];
-    p.kv_out[b] = s_first[b] >= 0 ? (int32_t)(s_kv[b] + q_of(b)) : s_kv[b];
+    if (p.fill) p.q_starts[b] = s_start[b];
+    if (p.move) p.kv_out[b] = s_first[b] >= 0 ? (int32_t)(s_kv[b] + q_of(b)) : s_kv[b];
   }
+  if (!p.fill) return;
   // new table entries: a warp per request
   for (int b = gt >> 5; b < p.B; b += nthreads >> 5) {
     const int first = s_first[b];
@@ -222,25 +219,34 @@ kvq_status launch_page_plan(const int32_t* kv_lens, const int32_t* q_lens, int B
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = allow_smem<page_plan_kernel>(device, kMaxPlanRequests * 12);
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("page_plan: ") + cudaGetErrorString(e));
-  const PagePlanParams p{kv_lens, q_lens,   table,  free_pages, free_head,    free_head_out, slots,     positions,
-                         q_starts, kv_out, info,   table_stride, B,           max_pages,     n_free,    page_shift,
-                         n_slots};
-  const int ctas = std::min(kPlanCluster, std::max(1, (std::max(B, n_slots) + kPlanPerCta - 1) / kPlanPerCta));
+  PagePlanParams p{kv_lens,  q_lens, table, free_pages, free_head,  free_head_out, slots,   positions, q_starts,
+                   kv_out,   info,   table_stride,  B,  max_pages,  n_free,        page_shift, n_slots, true, true};
+  const int ctas = std::min(num_sms(device), std::max(1, (std::max(B, n_slots) + kPlanPerCta - 1) / kPlanPerCta));
+  auto meet = [](const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+  };
+  const size_t lens = (size_t)B * 4;
+  const bool in_place = meet(kv_out, lens, kv_lens, lens) || meet(kv_out, lens, q_lens, lens) ||
+                        meet(free_head_out, 4, free_head, 4);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (size_t)B * 12;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
+  p.move = ctas == 1 || !in_place;
   e = cudaLaunchKernelEx(&cfg, page_plan_kernel, p);
+  if (e == cudaSuccess && !p.move) {
+    p.fill = false;
+    p.move = true;
+    cfg.gridDim = dim3(1);
+    e = cudaLaunchKernelEx(&cfg, page_plan_kernel, p);
+  }
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("page_plan launch: ") + cudaGetErrorString(e));
   return KVQ_OK;
 }
