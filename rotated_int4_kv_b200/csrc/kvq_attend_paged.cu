@@ -114,13 +114,14 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t mask, uint32_t 
 }
 
 // Eight int4 codes of a word plus 8, as fp16 pairs: h0 = (n0, n4) 2^-24, h1 = (n1, n5) 2^-20,
-// h2 = (n2, n6) 2^-24, h3 = (n3, n7) 2^-20 (subnormals, exact).
-__device__ __forceinline__ void nib8_plus8(uint32_t w, uint32_t (&h)[4]) {
+// h2 = (n2, n6) 2^-24, h3 = (n3, n7) 2^-20 (subnormals, exact). x1 = 0x00080008 and
+// x16 = 0x00800080 come in registers: an instruction holds one constant, the mask.
+__device__ __forceinline__ void nib8_plus8(uint32_t w, uint32_t x1, uint32_t x16, uint32_t (&h)[4]) {
   const uint32_t w8 = w >> 8;
-  h[0] = and_xor(w, 0x000F000Fu, 0x00080008u);
-  h[1] = and_xor(w, 0x00F000F0u, 0x00800080u);
-  h[2] = and_xor(w8, 0x000F000Fu, 0x00080008u);
-  h[3] = and_xor(w8, 0x00F000F0u, 0x00800080u);
+  h[0] = and_xor(w, 0x000F000Fu, x1);
+  h[1] = and_xor(w, 0x00F000F0u, x16);
+  h[2] = and_xor(w8, 0x000F000Fu, x1);
+  h[3] = and_xor(w8, 0x00F000F0u, x16);
 }
 // Four int8 codes of a word plus 128: h0 = (b0, b2) 2^-24, h1 = (b1, b3) 2^-24.
 __device__ __forceinline__ void byte4_plus128(uint32_t w, uint32_t (&h)[2]) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   long long* scan = reinterpret_cast<long long*>(empty + C::kStages);  // [5]
   long long* found = scan + kWarps + 1;                                // base of the first request, its index
   uint4* consts = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(full) + C::kBars - 16);
-  static_assert((2 * C::kStages + kWarps + 1 + 2) * 8 <= C::kBars - 16, "barrier region");
+  static_assert((2 * C::kStages + kWarps + 1 + 2) * 8 <= C::kBars - 24, "barrier region");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -387,6 +388,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       mbar_init(&empty[s], kWarps);
     }
     fence_mbarrier_init();
+    reinterpret_cast<uint32_t*>(consts)[-2] = 0x00080008u;
+    reinterpret_cast<uint32_t*>(consts)[-1] = 0x00800080u;
     *consts = make_uint4(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);  // -8 2^-24 and -128 2^-24, rows g and g + 8
   }
   grid_dep_launch();
@@ -499,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   const int g = lane >> 2, c = lane & 3, mi = lane >> 3;
   int n = 0;        // tiles taken so far
   bool ok = true;   // false after a wait ran out: the rest is passed over, every barrier still met
+  const uint32_t x1 = reinterpret_cast<volatile uint32_t*>(consts)[-2], x16 = reinterpret_cast<volatile uint32_t*>(consts)[-1];
   grid_dep_wait();
   while (w.next(p)) {
     const Request& r = w.r;
@@ -616,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t a[4], b[4];
-              nib8_plus8(x[2 * j], a);
-              nib8_plus8(x[2 * j + 1], b);
+              nib8_plus8(x[2 * j], x1, x16, a);
+              nib8_plus8(x[2 * j + 1], x1, x16, b);
 #pragma unroll
               for (int k = 0; k < 32 / G; ++k) {
                 const int grp = (2 * gp + j) * (32 / G) + k;
@@ -792,8 +796,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
             for (int j = 0; j < 2; ++j) {
               const int ch = 2 * gp + j;
               uint32_t a[4], b[4];  // channels 4g, 4g + 1 (16 times), 4g + 2, 4g + 3 (16 times) of the chunk
-              nib8_plus8(x[2 * j], a);
-              nib8_plus8(x[2 * j + 1], b);
+              nib8_plus8(x[2 * j], x1, x16, a);
+              nib8_plus8(x[2 * j + 1], x1, x16, b);
               if constexpr (G == 32) {
                 uint32_t b0, b1;
                 weighted(ch, b0, b1);

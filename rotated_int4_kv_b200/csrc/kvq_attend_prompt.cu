@@ -63,10 +63,18 @@ struct PrCfg {
   static constexpr int CW = BITS;               // 32-bit words of an item's codes
   static constexpr int kQ = NQ * 128 * D * 2;
   static constexpr int kTile = T * D * 2;
+  // codes on their way, per dequantiser thread: a ring of half tiles (NJ / 2 items), the next
+  // tile's scales (4 bytes per item of K and V), the table entries of the tile after it
+  static constexpr int NS = BITS == 4 ? 4 : 3;
+  static constexpr int kHalf = NJ / 2 * CW * 4 * ND * 32;
+  static constexpr int kRing = NS * kHalf;
+  static constexpr int kScales = 2 * NJ * 4 * ND * 32;
+  static constexpr int kEnt = NJ * 4 * ND * 32;
   static constexpr int kScan = kPrThreads * 8;
   static constexpr int kFlags = kFlagRing * 5 * 4;
   static constexpr int kBars = 256;
-  static constexpr int kSmem = kQ + 4 * kTile + kScan + kFlags + kBars + 1024;
+  static_assert(kScan <= kTile, "the scan uses the K tiles");
+  static constexpr int kSmem = kQ + 4 * kTile + kRing + kScales + kEnt + kFlags + kBars + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // TMEM columns
   static constexpr int kO = 0;                  // O of block q at q * D
@@ -262,18 +270,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kQ;
   uint8_t* sV = sK + 2 * C::kTile;
-  long long* scan = reinterpret_cast<long long*>(sV + 2 * C::kTile);
-  uint32_t* flags = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(scan) + C::kScan);  // [ring][5]
+  uint8_t* sRing = sV + 2 * C::kTile;
+  uint32_t* sScale = reinterpret_cast<uint32_t*>(sRing + C::kRing);
+  int32_t* sEnt = reinterpret_cast<int32_t*>(sRing + C::kRing + C::kScales);
+  long long* scan = reinterpret_cast<long long*>(sK);  // before the first tile
+  uint32_t* flags = reinterpret_cast<uint32_t*>(sRing + C::kRing + C::kScales + C::kEnt);  // [ring][5]
   uint64_t* kfull = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(flags) + C::kFlags);
   uint64_t* kempty = kfull + 2;
   uint64_t* vfull = kempty + 2;
   uint64_t* vempty = vfull + 2;
   uint64_t* aready = vempty + 2;  // [NQ] an A operand (raw query, q~, o) is in sQ
   uint64_t* sfull = aready + 2;   // [block or buffer] S (or a rotation's result) is in TMEM
-  uint64_t* pfull = sfull + 2;    // [block or buffer] P is in TMEM
-  uint64_t* odone = pfull + 2;    // [NQ] a P V product has been added
+  uint64_t* pfull = sfull + 2;    // [block or buffer][half] P is in TMEM
+  uint64_t* odone = pfull + 4;    // [NQ] a P V product has been added
   uint64_t* mdone = odone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
+  uint32_t* consts = tmem_slot + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -284,10 +296,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       mbar_init(&vempty[s], 1);
       mbar_init(&aready[s], 4);
       mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], 4);
+      mbar_init(&pfull[2 * s], 4);
+      mbar_init(&pfull[2 * s + 1], 4);
       mbar_init(&odone[s], 1);
     }
     mbar_init(mdone, 1);
+    consts[0] = BITS == 4 ? 0x64086408u : 0x64806480u;  // 1032 (1152) as fp16 pairs
+    consts[1] = 0x64806480u;                            // 1024 + 16 * 8
     fence_mbarrier_init();
   }
   for (int x = tid; x < kFlagRing * 5; x += kPrThreads) flags[x] = 0;
@@ -305,6 +320,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
   long long per;
   const bool any = find_piece<R, T>(p, scan, w, per);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();  // the scan's place is free
   bool ok = true;  // false after a wait ran out: the role goes through its loops without work
 
   if (any && warp < 4 * NQ) {
@@ -403,15 +419,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
 #pragma unroll 1
         for (int c = 0; c < T; c += 32) {
           float v[32];
-          tmem_ld32(ts + c, v);
-          tmem_ld_wait();
-          tmem_regs_fence(v);
+          tmem_ld32_now(ts + c, v);
           if (cut) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
           }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+          for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
         }
         mx *= f;
         // the product before this tile's: every phase of odone is waited for, or a parity could
@@ -445,15 +459,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           for (int t = 0; t < T; ++t)
             if (((fl[1 + (t >> 5)] >> (t & 31)) & 1) && t0 + t <= hi && t0 + t > lo) row_nan = true;
         }
-        // P
+        // P, in two halves: the product starts on the first while the second is made
         const float ms = m_run == -INFINITY ? 0.0f : m_run;
         float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < T; c += 32) {
           float v[32];
-          tmem_ld32(ts + c, v);
-          tmem_ld_wait();
-          tmem_regs_fence(v);
+          tmem_ld32_now(ts + c, v);
           if (cut) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
@@ -466,13 +478,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             l1 += b;
             h[k] = pack_half2(a, b);
           }
-          tmem_st16(ts + c / 2, h);
+          tmem_st16(ts + c / 2, h);  // over columns that have been read
+          if (c + 32 == T / 2 || c + 32 == T) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            // a barrier per half: a warp may be at its second while another is at its first
+            if (lane == 0) mbar_arrive(&pfull[2 * idx + (c + 32 == T)]);
+          }
         }
         l_run += l0 + l1;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[idx]);
       }
       wait(&odone[qb], (no + n - 1) & 1);
       no += n;
@@ -574,6 +589,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         announce(&kfull[kc & 1]);
       }
     };
+    // read, not written out: an instruction holds one constant, the mask
+    const uint32_t x1 = *reinterpret_cast<volatile uint32_t*>(consts), x16 = *reinterpret_cast<volatile uint32_t*>(consts + 1);
     // item j of this thread: row it_row(j) of a tile, 32 channels from 32 it_chunk(j)
     auto it_row = [&](int j) { return ((dw + ND * j) % (T / 8)) * 8 + (lane & 7); };
     auto it_chunk = [&](int j) { return ((dw + ND * j) / (T / 8)) * 4 + (lane >> 3); };
@@ -598,74 +615,120 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         if constexpr (BITS == 4) {
           const uint32_t x = it.c[k], x8 = x >> 8;
           const __half2 o1 = pu2h(0x64086408u), o16 = pu2h(0xD480D480u), i16 = pu2h(0x2C002C00u);  // 1032, -72, 1/16
-          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x, 0x000F000Fu, 0x64086408u)), o1), s));
-          o.y = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x, 0x00F000F0u, 0x64806480u)), i16, o16), s));
-          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x8, 0x000F000Fu, 0x64086408u)), o1), s));
-          o.w = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x8, 0x00F000F0u, 0x64806480u)), i16, o16), s));
+          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x, 0x000F000Fu, x1)), o1), s));
+          o.y = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x, 0x00F000F0u, x16)), i16, o16), s));
+          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(x8, 0x000F000Fu, x1)), o1), s));
+          o.w = ph2u(__hmul2(__hfma2(pu2h(mask_xor(x8, 0x00F000F0u, x16)), i16, o16), s));
         } else {
           const __half2 o1 = pu2h(0x64806480u);  // 1152
           const uint32_t a = it.c[2 * k], b = it.c[2 * k + 1];
-          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a, 0x00FF00FFu, 0x64806480u)), o1), s));
-          o.y = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a >> 8, 0x00FF00FFu, 0x64806480u)), o1), s));
-          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b, 0x00FF00FFu, 0x64806480u)), o1), s));
-          o.w = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b >> 8, 0x00FF00FFu, 0x64806480u)), o1), s));
+          o.x = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a, 0x00FF00FFu, x1)), o1), s));
+          o.y = ph2u(__hmul2(__hsub2(pu2h(mask_xor(a >> 8, 0x00FF00FFu, x1)), o1), s));
+          o.z = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b, 0x00FF00FFu, x1)), o1), s));
+          o.w = ph2u(__hmul2(__hsub2(pu2h(mask_xor(b >> 8, 0x00FF00FFu, x1)), o1), s));
         }
         *reinterpret_cast<uint4*>(dst + ((((ch & 1) * 4 + k) ^ (r & 7)) << 4)) = o;
       }
     };
+    // What a thread converts it fetches itself, by async copies: an arrival at a barrier would
+    // wait for loads in flight, not for these. Half h (four per tile: K, K, V, V) goes to ring
+    // slot h % NS and is issued NS - 1 halves ahead; the scales of tile i + 1 and the table
+    // entries of tile i + 2 go with tile i's first half.
+    constexpr int NS = C::NS, HJ = NJ / 2, NT = ND * 32;
+    uint8_t* ring = sRing + dtid * 16;
+    uint32_t* scale_s = sScale + dtid;
+    int32_t* ent_s = sEnt + dtid;
+    auto copy16 = [&](uint8_t* dst, const uint8_t* src, bool in) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+    };
+    auto copy4 = [&](void* dst, const void* src, bool in) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     while (w.next(p)) {
       const int n = w.i1 - w.i0;
-      matrix(p.wq);
       const int32_t* trow = p.table + (long long)w.b * p.table_stride;
       const int t_first = (w.tile0 + w.i0) * T;
       const int t_hi = w.hi, t_lo = w.lo;
-      // the cache row of item j in tile i, -1: no token that the unit attends
-      auto entry = [&](int i, int j) {
-        const int t = t_first + i * T + it_row(j);
-        return i < n && t >= t_lo && t < t_hi ? __ldg(trow + (t >> p.page_shift)) : -1;
+      // item j of tile i: its token, and whether the unit attends it
+      auto token = [&](int i, int j) { return t_first + i * T + it_row(j); };
+      auto live = [&](int i, int j) {
+        const int t = token(i, j);
+        return i < n && t >= t_lo && t < t_hi;
       };
-      auto cache_row = [&](int i, int j, int e) -> long long {
-        const int t = t_first + i * T + it_row(j);
-        if (!(i < n && t >= t_lo && t < t_hi)) return -1;
+      auto cache_row = [&](int i, int j, int e) -> long long {  // e: its table entry; -1 where there is no token
+        if (!live(i, j)) return -1;
         if (e < 0 || e >= p.num_pages) {
           atomicOr(&g_prompt_err, kErrBadPage);
           e = 0;
         }
-        return (((long long)e * p.Hkv + w.h) << p.page_shift) + (t & P1);
+        return (((long long)e * p.Hkv + w.h) << p.page_shift) + (token(i, j) & P1);
       };
-      auto load_codes = [&](const uint8_t* base, long long r, int j, Item& it) {
-        const uint4* src = reinterpret_cast<const uint4*>(base + r * RB + it_chunk(j) * (4 * BITS));
+      long long rows[2][NJ];  // of this tile and the next
+      auto fetch_entries = [&](int i) {
 #pragma unroll
-        for (int x = 0; x < C::CW / 4; ++x) {
-          const uint4 v = r >= 0 ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-          it.c[4 * x] = v.x;
-          it.c[4 * x + 1] = v.y;
-          it.c[4 * x + 2] = v.z;
-          it.c[4 * x + 3] = v.w;
+        for (int j = 0; j < NJ; ++j) {
+          const bool in = live(i, j);
+          copy4(ent_s + j * NT, trow + (in ? token(i, j) >> p.page_shift : 0), in);
         }
       };
-      auto load_scale = [&](const uint16_t* base, long long r, int j, Item& it) {
-        const uint16_t* src = base + r * NG + it_chunk(j) * (32 / G);
-        it.s = r < 0 ? 0u : G == 32 ? (uint32_t)__ldg(src) : __ldg(reinterpret_cast<const uint32_t*>(src));
+      auto take_entries = [&](int i, long long (&r)[NJ]) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) r[j] = cache_row(i, j, ent_s[j * NT]);
       };
-      Item k[NJ], v[NJ];
-      long long rows[NJ];   // of the next tile
-      int ent[NJ];          // table entries of the tile after it
+      auto fetch_scales = [&](const long long (&r)[NJ]) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const long long at = max(r[j], 0ll) * NG + (G == 32 ? it_chunk(j) & ~1 : 2 * it_chunk(j));
+          copy4(scale_s + (2 * j) * NT, p.ks + at, r[j] >= 0);
+          copy4(scale_s + (2 * j + 1) * NT, p.vs + at, r[j] >= 0);
+        }
+      };
+      auto fetch_half = [&](int h, const long long (&r)[NJ]) {
+        const uint8_t* base = (h & 2) ? p.vc : p.kc;
+        uint8_t* dst = ring + (h % NS) * C::kHalf;
+#pragma unroll
+        for (int x = 0; x < HJ; ++x) {
+          const long long row = (h & 1) ? r[HJ + x] : r[x];
+          const int ch = (h & 1) ? it_chunk(HJ + x) : it_chunk(x);
+#pragma unroll
+          for (int y = 0; y < C::CW / 4; ++y)
+            copy16(dst + (x * (C::CW / 4) + y) * NT * 16, base + max(row, 0ll) * RB + ch * (4 * BITS) + 16 * y, row >= 0);
+        }
+      };
+      // the start: entries of tiles 0 and 1, scales of tile 0, the first halves
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        rows[j] = cache_row(0, j, entry(0, j));
-        load_codes(p.kc, rows[j], j, k[j]);
-        load_scale(p.ks, rows[j], j, k[j]);
-        load_scale(p.vs, rows[j], j, v[j]);
-        load_codes(p.vc, rows[j], j, v[j]);
-        ent[j] = entry(1, j);
+        rows[0][j] = cache_row(0, j, live(0, j) ? __ldg(trow + (token(0, j) >> p.page_shift)) : -1);
+        rows[1][j] = -1;
       }
+      fetch_entries(1);
+      fetch_scales(rows[0]);
+      commit();
+      matrix(p.wq);
+      // halves 0 .. NS - 2, a group each
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        rows[j] = cache_row(1, j, ent[j]);
-        ent[j] = entry(2, j);
+      for (int h = 0; h < NS - 1; ++h) {
+        fetch_half(h, rows[0]);
+        commit();
       }
+      asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
       for (int i = 0; i < n; ++i, ++kt, ++kc, ++vc) {
+        uint32_t ksc[NJ], vsc[NJ];
+        // ---- half 4 i: this tile's scales and the next one's entries are here (their group is
+        // older than the halves in flight)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          ksc[j] = scale_s[(2 * j) * NT];
+          vsc[j] = scale_s[(2 * j + 1) * NT];
+          if (G == 32) {
+            ksc[j] = (it_chunk(j) & 1) ? ksc[j] >> 16 : ksc[j] & 0xFFFFu;
+            vsc[j] = (it_chunk(j) & 1) ? vsc[j] >> 16 : vsc[j] & 0xFFFFu;
+          }
+        }
+        take_entries(i + 1, rows[1]);
+        fetch_scales(rows[1]);
+        fetch_entries(i + 2);
         // ---- scales that need care: bit 0 large K, bit 1 large V, bit 2 V not finite
         uint32_t* fl = flags + (kt % kFlagRing) * 5;
         {
@@ -673,7 +736,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           uint32_t kx = 0, vx = 0;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            const uint32_t a = k[j].s & 0x7FFF7FFFu, b = v[j].s & 0x7FFF7FFFu;
+            const uint32_t a = ksc[j] & 0x7FFF7FFFu, b = vsc[j] & 0x7FFF7FFFu;
             kx = max(kx, max(a & 0xFFFFu, a >> 16));
             vx = max(vx, max(b & 0xFFFFu, b >> 16));
           }
@@ -681,8 +744,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             if (vx >= 0x7C00u) {
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {
-                if ((v[j].s & 0x7C00u) == 0x7C00u || (v[j].s & 0x7C000000u) == 0x7C000000u) {
-                  v[j].s = 0;
+                if ((vsc[j] & 0x7C00u) == 0x7C00u || (vsc[j] & 0x7C000000u) == 0x7C000000u) {
+                  vsc[j] = 0;
                   atomicOr(&fl[1 + (it_row(j) >> 5)], 1u << (it_row(j) & 31));
                 }
               }
@@ -693,57 +756,75 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         asm volatile("bar.sync 1, %0;" ::"n"(ND * 32) : "memory");
         const uint32_t flag = *reinterpret_cast<volatile uint32_t*>(fl);
         if (dtid < 5) flags[((kt + kFlagRing / 2) % kFlagRing) * 5 + dtid] = 0;  // last read four tiles ago
-        // ---- K
-        wait(kempty, kc);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) convert(sK + (kc & 1) * C::kTile, j, k[j], flag & 1);
-        announce(&kfull[kc & 1]);
-        uint32_t vsc[NJ];
+        for (int part = 0; part < 4; ++part) {
+          const int h = 4 * i + part;
+          // half h has landed; the next one goes to the slot that the half before this left
+          asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+          Item it[HJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          vsc[j] = v[j].s;
-          load_codes(p.kc, rows[j], j, k[j]);
-          load_scale(p.ks, rows[j], j, k[j]);
-          load_scale(p.vs, rows[j], j, v[j]);
+          for (int x = 0; x < HJ; ++x)
+#pragma unroll
+            for (int y = 0; y < C::CW / 4; ++y) {
+              const uint4 v = *reinterpret_cast<const uint4*>(ring + (h % NS) * C::kHalf + (x * (C::CW / 4) + y) * NT * 16);
+              it[x].c[4 * y] = v.x;
+              it[x].c[4 * y + 1] = v.y;
+              it[x].c[4 * y + 2] = v.z;
+              it[x].c[4 * y + 3] = v.w;
+            }
+          if (part + NS - 1 < 4) fetch_half(h + NS - 1, rows[0]);
+          else fetch_half(h + NS - 1, rows[1]);
+          commit();
+          if (part == 0) wait(kempty, kc);
+          if (part == 2) wait(vempty, vc);
+          uint8_t* tile = part < 2 ? sK + (kc & 1) * C::kTile : sV + (vc & 1) * C::kTile;
+#pragma unroll
+          for (int x = 0; x < HJ; ++x) {
+            const int j = (part & 1) * HJ + x;
+            it[x].s = part < 2 ? ksc[j] : vsc[j];
+            convert(tile, j, it[x], part < 2 ? flag & 1 : flag & 2);
+          }
+          if (part == 1) announce(&kfull[kc & 1]);
+          if (part == 3) announce(&vfull[vc & 1]);
         }
-        // ---- V
-        wait(vempty, vc);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          Item it = v[j];
-          it.s = vsc[j];
-          convert(sV + (vc & 1) * C::kTile, j, it, flag & 2);
-        }
-        announce(&vfull[vc & 1]);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          load_codes(p.vc, rows[j], j, v[j]);
-          rows[j] = cache_row(i + 2, j, ent[j]);
-          ent[j] = entry(i + 3, j);
-        }
+        for (int j = 0; j < NJ; ++j) rows[0][j] = rows[1][j];
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (w.i0 == 0 && w.i1 == w.nt) matrix(p.wo);
     }
-  } else if (any && lane == 0) {
+  } else if (any) {
     // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks and waits, an elected lane issues each batch of eight products:
+    // the operands' descriptors stay in the warp's uniform registers. (One lane doing all of
+    // it took 106 cycles per product, most of them to move descriptors there; a product itself
+    // takes 64.)
     constexpr uint32_t id_s = umma_idesc_f16(128, T), id_o = umma_idesc_f16(128, D) | kUmmaTransposeB;
+    const uint32_t q_lo = (uint32_t)umma_desc_sw128(smem_u32(sQ)), k_lo = (uint32_t)umma_desc_sw128(smem_u32(sK));
+    const uint32_t v_lo = (uint32_t)umma_desc_mn_sw128(smem_u32(sV), kBlkT);
+    constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // bits 32 .. 63 of all three
     int kc = 0, vc = 0;
     uint32_t na[2] = {0, 0}, np[2] = {0, 0};
     auto wait = [&](uint64_t* bar, uint32_t ph) {
-      if (ok && !mbar_wait_bounded(bar, ph)) {
-        atomicOr(&g_prompt_err, kErrTimeoutLoad);
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, ph))) {
+        if (lane == 0) atomicOr(&g_prompt_err, kErrTimeoutLoad);
         ok = false;
       }
       tc_fence_after();
       return ok;
     };
-    // columns d (+)= A block q of sQ times the K ring's tile
-    auto product = [&](uint32_t d, int q, int slot) {
-      const uint32_t a = smem_u32(sQ + q * (128 * D * 2)), b = smem_u32(sK + slot * C::kTile);
+    // columns d = A block q of sQ times the K ring's tile; then arrivals at `done` (and `done2`)
+    auto product = [&](uint32_t d, int q, int slot, uint64_t* done, uint64_t* done2) {
+      const uint32_t a = q_lo + (uint32_t)(q * (128 * D * 2) >> 4), b = k_lo + (uint32_t)(slot * C::kTile >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        umma_f16(d, umma_desc_sw128(a + (ks >> 2) * kBlkQ + (ks & 3) * 32), umma_desc_sw128(b + (ks >> 2) * kBlkT + (ks & 3) * 32),
-                 id_s, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_f16_lo(d, a + (((ks >> 2) * kBlkQ + (ks & 3) * 32) >> 4), b + (((ks >> 2) * kBlkT + (ks & 3) * 32) >> 4), kHi, id_s,
+                      ks > 0);
+        if (done) umma_commit(done);
+        if (done2) umma_commit(done2);
+      }
+      __syncwarp();
     };
     while (w.next(p)) {
       const int n = w.i1 - w.i0;
@@ -751,54 +832,49 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       auto rotate = [&]() {  // the A operands times a rotation matrix
         for (int q = 0; q < nq; ++q) wait(&aready[q], na[q]++ & 1);
         for (int t = 0; t < NW; ++t, ++kc) {
-          if (wait(&kfull[kc & 1], (kc >> 1) & 1)) {
-            for (int q = 0; q < nq; ++q) product(tmem + (D == 128 ? C::kS + q * T : C::kO + t * T), q, kc & 1);
-            umma_commit(&kempty[kc & 1]);
-          }
+          if (!wait(&kfull[kc & 1], (kc >> 1) & 1)) continue;
+          for (int q = 0; q < nq; ++q)
+            product(tmem + (D == 128 ? C::kS + q * T : C::kO + t * T), q, kc & 1, t == NW - 1 ? &sfull[NQ == 2 ? q : 0] : nullptr,
+                    q == nq - 1 ? &kempty[kc & 1] : nullptr);
         }
-        if (ok)
-          for (int q = 0; q < nq; ++q) umma_commit(&sfull[NQ == 2 ? q : 0]);
       };
       rotate();
       for (int q = 0; q < nq; ++q) wait(&aready[q], na[q]++ & 1);
       for (int s = 0; s < SB && s < n; ++s, ++kc) {
         if (!wait(&kfull[kc & 1], (kc >> 1) & 1)) continue;
-        for (int q = 0; q < nq; ++q) {
-          product(tmem + C::kS + (NQ == 2 ? q : s) * T, q, kc & 1);
-          umma_commit(&sfull[NQ == 2 ? q : s]);
-        }
-        umma_commit(&kempty[kc & 1]);
+        for (int q = 0; q < nq; ++q)
+          product(tmem + C::kS + (NQ == 2 ? q : s) * T, q, kc & 1, &sfull[NQ == 2 ? q : s], q == nq - 1 ? &kempty[kc & 1] : nullptr);
       }
       for (int i = 0; i < n; ++i, ++vc) {
         const bool more = i + SB < n;
         wait(&vfull[vc & 1], (vc >> 1) & 1);
-        const uint32_t vb = smem_u32(sV + (vc & 1) * C::kTile);
+        const uint32_t vb = v_lo + (uint32_t)((vc & 1) * C::kTile >> 4);
         for (int q = 0; q < nq; ++q) {
           const int idx = NQ == 2 ? q : (i & 1);
           const uint32_t ts = tmem + C::kS + idx * T;
-          if (wait(&pfull[idx], np[idx]++ & 1)) {
 #pragma unroll
-            for (int kk = 0; kk < T / 16; ++kk)
-              umma_f16_ts(tmem + C::kO + q * D, ts + 8 * kk, umma_desc_mn_sw128(vb + kk * 2048, kBlkT), id_o, i > 0 || kk > 0);
-            umma_commit(&odone[q]);
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(&pfull[2 * idx + half], np[idx] & 1)) continue;
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = half * (T / 32); kk < (half + 1) * (T / 32); ++kk)
+                umma_f16_ts_lo(tmem + C::kO + q * D, ts + 8 * kk, vb + (kk * 2048 >> 4), kHi, id_o, i > 0 || kk > 0);
+              if (half) umma_commit(&odone[q]);
+              if (half && q == nq - 1) umma_commit(&vempty[vc & 1]);
+            }
+            __syncwarp();
           }
+          ++np[idx];
           if (more) {
             if (q == 0) wait(&kfull[kc & 1], (kc >> 1) & 1);
-            if (ok) {
-              product(ts, q, kc & 1);
-              umma_commit(&sfull[idx]);
-            }
+            if (ok) product(ts, q, kc & 1, &sfull[idx], q == nq - 1 ? &kempty[kc & 1] : nullptr);
           }
         }
-        if (ok) umma_commit(&vempty[vc & 1]);
-        if (more) {
-          if (ok) umma_commit(&kempty[kc & 1]);
-          ++kc;
-        }
+        if (more) ++kc;
       }
       if (w.i0 == 0 && w.i1 == w.nt) rotate();
     }
-    umma_commit(mdone);
+    if (elect_one()) umma_commit(mdone);
     if (!mbar_wait_bounded(mdone, 0)) atomicOr(&g_prompt_err, kErrTimeoutLoad);
   }
   tc_fence_before();
