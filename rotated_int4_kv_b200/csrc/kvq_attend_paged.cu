@@ -53,6 +53,13 @@ constexpr int kWarps = 4;       // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kMaxCtas = 3 * 160;  // partial slots in the workspace: two per CTA
 
+// Warps of a block of the first and the last kernel. At D = 256 a warp per 16 rows of the
+// matrix halves the time of a block (drafts on 16K caches 24.9 -> 21.2 us); at D = 128 four
+// warps with two such tiles each are better where there are many blocks (64.6 against 68.1 us
+// for 512 units).
+template <int D>
+constexpr int kUnitWarps = D == 128 ? 4 : 16;
+
 template <int D, int G, int BITS>
 struct PCfg {
   static constexpr int NC = D / 32;               // 32-channel chunks of a row
@@ -240,26 +247,21 @@ struct Walk {
 // fragments when the plan was made) and laid out as the score products' B fragments
 // (column = row of the tile), normalised by 2^-e per row, with per group the start of its sum
 // (minus what the codes' offset adds to it) and per row the factor back to base-2 scores.
-// A block reads the matrix (32 KB at D = 128) through L2; at D = 128 before it waits for the
-// kernel in front. Done here once per unit, not in every piece of it, and beside the main
+// A block reads the matrix (32 or 128 KB) through L2 before it waits for the kernel in front,
+// Done here once per unit, not in every piece of it, and beside the main
 // kernel's start.
 template <int D, int G, int BITS>
-__global__ void __launch_bounds__(kWarps * 32) rotate_paged_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const __grid_constant__ PagedParams p) {
   using C = PCfg<D, G, BITS>;
-  constexpr int NC = C::NC, MT = C::MT, TW = MT / kWarps;
+  constexpr int NC = C::NC, MT = C::MT, NWARP = kUnitWarps<D>, TW = MT / NWARP;
   __shared__ __align__(16) float om[kRows * C::kOmStride];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
-  constexpr bool kAhead = D == 128;
-  uint4 wf[kAhead ? TW : 1][MT];
-  auto load_matrix = [&](int t, uint4 (&f)[MT]) {
+  uint4 wf[TW][MT];
 #pragma unroll
-    for (int ks = 0; ks < MT; ++ks) f[ks] = __ldg(p.wq + ((warp + kWarps * t) * MT + ks) * 32 + lane);
-  };
-  if constexpr (kAhead) {
+  for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int t = 0; t < TW; ++t) load_matrix(t, wf[t]);
-  }
+    for (int ks = 0; ks < MT; ++ks) wf[t][ks] = __ldg(p.wq + ((warp + NWARP * t) * MT + ks) * 32 + lane);
   grid_dep_wait();
   grid_dep_launch();  // after the wait: what the main kernel reads before its own wait is complete
   const Request r = request_of<C::kTile>(p, b);
@@ -278,15 +280,11 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_paged_kernel(const __grid_
   }
 #pragma unroll
   for (int t = 0; t < TW; ++t) {
-    const int mt = warp + kWarps * t;
-    if constexpr (!kAhead) load_matrix(t, wf[0]);
     float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < MT; ++ks) {
-      const uint4 a = wf[kAhead ? t : 0][ks];
-      mma_16816((ks & 1) ? a1 : a0, a.x, a.y, a.z, a.w, bq[ks][0], bq[ks][1]);
-    }
-    float* o0 = om + (2 * c) * C::kOmStride + 16 * mt + g;
+    for (int ks = 0; ks < MT; ++ks)
+      mma_16816((ks & 1) ? a1 : a0, wf[t][ks].x, wf[t][ks].y, wf[t][ks].z, wf[t][ks].w, bq[ks][0], bq[ks][1]);
+    float* o0 = om + (2 * c) * C::kOmStride + 16 * (warp + NWARP * t) + g;
     o0[0] = a0[0] + a1[0];
     o0[C::kOmStride] = a0[1] + a1[1];
     o0[8] = a0[2] + a1[2];
@@ -314,9 +312,9 @@ __global__ void __launch_bounds__(kWarps * 32) rotate_paged_kernel(const __grid_
   if (warp == 0 && c == 0) rowfac[g] = p.qfac * 16777216.0f * pow2f(ex);
   constexpr float kOff = (BITS == 4 ? 8.0f : 128.0f) / 16777216.0f;
   constexpr float kPair = BITS == 4 ? 16.0f : 1.0f;
-#pragma unroll
-  for (int t = 0; t < NC / kWarps; ++t) {
-    const int ch = warp + kWarps * t;
+  static_assert(NC <= NWARP, "a chunk per warp");
+  if (warp < NC) {
+    const int ch = warp;
     uint32_t h[4];
     float sum[2];
 #pragma unroll
@@ -931,25 +929,20 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 // Block u: the partials of unit u in CTA order, then out = Wo (o / l) with o as an fp16 hi + lo
 // pair (samples as rows, query rows as columns). A few KB per unit through L2: bound by the
 // latency of the chain lengths -> partials -> output; the matrix is loaded before the wait for
-// the main kernel at D = 128.
+// the main kernel.
 template <int D, int BITS>
-__global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_constant__ PagedParams p) {
-  constexpr int MT = D / 16, TW = MT / kWarps, ST = D + 4, PART = 2 * kRows + kRows * D;
+__global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int MT = D / 16, NWARP = kUnitWarps<D>, TW = MT / NWARP, NT = NWARP * 32, ST = D + 4, PART = 2 * kRows + kRows * D;
   __shared__ __align__(16) float om[kRows * ST];
   __shared__ __align__(16) __half xb[kRows * (D + 8)];
-  __shared__ float red[2][16][kRows], wts[kMaxCtas * kRows];
+  __shared__ float red[2][NT / 8][kRows], wts[kMaxCtas * kRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
-  constexpr bool kAhead = D == 128;
-  uint4 wf[kAhead ? TW : 1][MT];
-  auto load_matrix = [&](int t, uint4 (&f)[MT]) {
+  uint4 wf[TW][MT];
 #pragma unroll
-    for (int ks = 0; ks < MT; ++ks) f[ks] = __ldg(p.wo + ((warp + kWarps * t) * MT + ks) * 32 + lane);
-  };
-  if constexpr (kAhead) {
+  for (int t = 0; t < TW; ++t)
 #pragma unroll
-    for (int t = 0; t < TW; ++t) load_matrix(t, wf[t]);
-  }
+    for (int ks = 0; ks < MT; ++ks) wf[t][ks] = __ldg(p.wo + ((warp + NWARP * t) * MT + ks) * 32 + lane);
   grid_dep_launch();
   grid_dep_wait();
   const Request r = request_of<128>(p, b);
@@ -964,12 +957,12 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
   {
     const int row = tid & 7, k0 = tid >> 3;
     float M = -INFINITY, L = 0.0f;
-    for (int k = k0; k < np; k += 16) M = fmaxf(M, __ldcg(part(k) + row));
+    for (int k = k0; k < np; k += NT / 8) M = fmaxf(M, __ldcg(part(k) + row));
     red[0][k0][row] = M;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 16; ++k) M = fmaxf(M, red[0][k][row]);
-    for (int k = k0; k < np; k += 16) {
+    for (int k = 0; k < NT / 8; ++k) M = fmaxf(M, red[0][k][row]);
+    for (int k = k0; k < np; k += NT / 8) {
       const float m = __ldcg(part(k) + row), l = __ldcg(part(k) + kRows + row);
       const float f = m != -INFINITY ? ex2_approx(m - M) : 0.0f;
       L += m != -INFINITY ? l * f : l;
@@ -979,24 +972,22 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
     __syncthreads();
   }
   {
-    constexpr int NX = kRows * D / 4 / (kWarps * 32);  // float4 values of a thread
+    constexpr int NX = kRows * D / 4 / NT, U = 8 / NX;  // float4 values of a thread, partials in flight
     float4 acc[NX];
 #pragma unroll
     for (int x = 0; x < NX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 8 / NX > 2 ? 8 / NX : 2;         // partials in flight
     for (int k0 = 0; k0 < np; k0 += U) {
       float4 v[U][NX];
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int x = 0; x < NX; ++x)
-          if (k0 + k < np) v[k][x] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + 2 * kRows) + tid + x * kWarps * 32);
+          if (k0 + k < np) v[k][x] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + 2 * kRows) + tid + x * NT);
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
-          const int row = (tid + x * kWarps * 32) / (D / 4);
-          const float f = k0 + k < np ? wts[(k0 + k) * kRows + row] : 0.0f;
+          const float f = k0 + k < np ? wts[(k0 + k) * kRows + (tid + x * NT) / (D / 4)] : 0.0f;
           if (f != 0.0f) {
             acc[x].x = fmaf(f, v[k][x].x, acc[x].x);
             acc[x].y = fmaf(f, v[k][x].y, acc[x].y);
@@ -1007,7 +998,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
     }
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
-      const int y = tid + x * kWarps * 32, row = y / (D / 4);
+      const int y = tid + x * NT, row = y / (D / 4);
       // rows behind the tile's last were not written
       *reinterpret_cast<float4*>(om + row * ST + 4 * (y - row * (D / 4))) = row < nrows ? acc[x] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -1015,7 +1006,7 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
   __syncthreads();
   float L = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) L += red[1][k][g];
+  for (int k = 0; k < NT / 8; ++k) L += red[1][k][g];
   const float inv = L > 0.0f || L != L ? 1.0f / L : 0.0f;  // nothing attended: zeros (NaN stays)
   const float* orow = om + g * ST;
   float mx = 0.0f;
@@ -1027,25 +1018,21 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
   const int ex = row_exponent(mx * inv);
   const float fx = inv * pow2f(-ex);
   float acc[TW][4] = {};
-  uint32_t bh2[MT][2], bl2[MT][2];
 #pragma unroll
-  for (int ks = 0; ks < MT; ++ks)
+  for (int ks = 0; ks < MT; ++ks) {
+    uint32_t hi[2], lo[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const float2 v = *reinterpret_cast<const float2*>(orow + 16 * ks + 8 * e + 2 * c);
       const __half2 hv = __floats2half2_rn(v.x * fx, v.y * fx);
       const float2 hf = __half22float2(hv);
-      bh2[ks][e] = h2u(hv);
-      bl2[ks][e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
+      hi[e] = h2u(hv);
+      lo[e] = pack_half2(v.x * fx - hf.x, v.y * fx - hf.y);
     }
 #pragma unroll
-  for (int t = 0; t < TW; ++t) {
-    if constexpr (!kAhead) load_matrix(t, wf[0]);
-#pragma unroll
-    for (int ks = 0; ks < MT; ++ks) {
-      const uint4 a = wf[kAhead ? t : 0][ks];
-      mma_16816(acc[t], a.x, a.y, a.z, a.w, bh2[ks][0], bh2[ks][1]);
-      mma_16816(acc[t], a.x, a.y, a.z, a.w, bl2[ks][0], bl2[ks][1]);
+    for (int t = 0; t < TW; ++t) {
+      mma_16816(acc[t], wf[t][ks].x, wf[t][ks].y, wf[t][ks].z, wf[t][ks].w, hi[0], hi[1]);
+      mma_16816(acc[t], wf[t][ks].x, wf[t][ks].y, wf[t][ks].z, wf[t][ks].w, lo[0], lo[1]);
     }
   }
   float fo[2];
@@ -1053,14 +1040,14 @@ __global__ void __launch_bounds__(kWarps * 32) join_paged_kernel(const __grid_co
   for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
 #pragma unroll
   for (int t = 0; t < TW; ++t) {
-    __half* x0 = xb + (2 * c) * (D + 8) + 16 * (warp + kWarps * t) + g;
+    __half* x0 = xb + (2 * c) * (D + 8) + 16 * (warp + NWARP * t) + g;
     x0[0] = __float2half_rn(acc[t][0] * fo[0]);
     x0[D + 8] = __float2half_rn(acc[t][1] * fo[1]);
     x0[8] = __float2half_rn(acc[t][2] * fo[0]);
     x0[D + 8 + 8] = __float2half_rn(acc[t][3] * fo[1]);
   }
   __syncthreads();
-  for (int x = tid; x < nrows * (D / 8); x += kWarps * 32) {
+  for (int x = tid; x < nrows * (D / 8); x += NT) {
     const int row = x / (D / 8), k = x - row * (D / 8);
     const int y = rt * kRows + row, tok = y / p.Gq, head = h * p.Gq + (y - tok * p.Gq);
     *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
@@ -1130,7 +1117,7 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   const int slots = std::min(kMaxCtas, num_sms(a.pk->device) * C::kCtas);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)units);
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kUnitWarps<D> * 32);
   cfg.stream = strm;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1147,7 +1134,7 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   }
   if (e == cudaSuccess) {
     cfg.gridDim = dim3((unsigned)units);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(kUnitWarps<D> * 32);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, join_paged_kernel<D, BITS>, p);
   }
