@@ -167,6 +167,30 @@ __device__ __forceinline__ int code_off(int row, int cc) {
   return (cc >> 3) * (kTile * 128) + row * 128 + (((cc & 7) ^ (row & 7)) << 4);
 }
 
+// Loads from shared memory by 32-bit address (the loop below keeps no 64-bit pointers).
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      const uint4 u = lds128(a + 4 * k);
+      v[k] = u.x;
+      v[k + 1] = u.y;
+      v[k + 2] = u.z;
+      v[k + 3] = u.w;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- the requests
 struct Request {
   int qs, qn, kv;      // first query token, query tokens, cached tokens
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     const uint32_t box = (uint32_t)(bt * (RB < 128 ? RB : 128));
     const uint32_t sbytes = (uint32_t)(bt * NG * 2);
     const uint32_t box_bytes = 2 * ((uint32_t)(bt * RB) + sbytes);
-    const uint64_t pol = l2_evict_first_policy();
+    const uint64_t pol = p.rt_max == 1 ? l2_evict_first_policy() : l2_normal_policy();
     int n = 0;
     while (w.next(p)) {
       const int h = w.u / w.r.rt;
@@ -470,25 +494,26 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         const uint32_t here = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(here) * box_bytes);
         __syncwarp();
-        if (page >= 0) {
-          uint8_t* st = ring + s * C::kStage;
-          const int ph = page * p.Hkv + h;
-          const int off = ((w.r.tile0 + i) * kTile + lane * bt) & (P - 1);  // the box's first row of the page
+        const int t0 = (w.r.tile0 + i) * kTile;
+#pragma unroll 1
+        for (int x = 0; x < nb; ++x) {
+          if (!((here >> x) & 1)) continue;
+          const int ph = __shfl_sync(0xffffffffu, page, x) * p.Hkv + h;
+          if (elect_one()) {
+            uint8_t* st = ring + s * C::kStage;
+            const int off = (t0 + x * bt) & (P - 1);  // the box's first row of the page
 #pragma unroll
-          for (int j = 0; j < (RB + 127) / 128; ++j) {
-            uint8_t* kd = st + j * (kTile * 128) + lane * box;
-            if (p.rt_max == 1) {  // the pages are read once: out of L2's way
+            for (int j = 0; j < (RB + 127) / 128; ++j) {
+              uint8_t* kd = st + j * (kTile * 128) + x * box;
               tma_load_3d_hint(kd, &p.kmap, &full[s], 128 * j, off, ph, pol);
               tma_load_3d_hint(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph, pol);
-            } else {
-              tma_load_3d(kd, &p.kmap, &full[s], 128 * j, off, ph);
-              tma_load_3d(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph);
             }
+            uint8_t* sd = st + 2 * C::kKBytes + x * sbytes;
+            const size_t srow = ((size_t)ph * P + off) * NG;
+            bulk_load(sd, p.ks + srow, sbytes, &full[s]);
+            bulk_load(sd + C::kSBytes, p.vs + srow, sbytes, &full[s]);
           }
-          uint8_t* sd = st + 2 * C::kKBytes + lane * sbytes;
-          const size_t srow = ((size_t)ph * P + off) * NG;
-          bulk_load(sd, p.ks + srow, sbytes, &full[s]);
-          bulk_load(sd + C::kSBytes, p.vs + srow, sbytes, &full[s]);
+          __syncwarp();
         }
         page = coming;
       }
@@ -501,6 +526,17 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
   int n = 0;        // tiles taken so far
   bool ok = true;   // false after a wait ran out: the rest is passed over, every barrier still met
   const uint32_t x1 = reinterpret_cast<volatile uint32_t*>(consts)[-2], x16 = reinterpret_cast<volatile uint32_t*>(consts)[-1];
+  // shared-memory addresses of this lane: ring, query fragments, starts, constant, K scales of row
+  // g, and the 16-byte columns of its ldmatrix rows (row + 16 leaves the swizzle as it is)
+  const uint32_t ring_a = smem_u32(ring), qf_a = smem_u32(qf + lane), bias_a = smem_u32(bias + c * 4), consts_a = smem_u32(consts);
+  const uint32_t ks_off = (WT * warp + g) * (NG * 2);
+  const int lrow = WT * warp + ((mi & 1) << 3) + (lane & 7);
+  uint32_t code_off_[RB == 64 ? 2 : 4];
+#pragma unroll
+  for (int k = 0; k < (RB == 64 ? 2 : 4); ++k) code_off_[k] = code_off<RB, kTile>(lrow, 2 * k + (mi >> 1));
+  auto code_at = [&](int u, int k) {  // columns 2 k, 2 k + 1 of the rows of subtile u
+    return code_off_[k % (RB == 64 ? 2 : 4)] + (k / 4) * (kTile * 128) + 16 * u * (RB < 128 ? RB : 128);
+  };
   grid_dep_wait();
   while (w.next(p)) {
     const Request& r = w.r;
@@ -567,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         ok = false;
         continue;
       }
-      const uint8_t* st = ring + s * C::kStage;
+      const uint32_t st = ring_a + s * C::kStage;               // shared-memory address of the stage
       const int r0 = WT * warp;                                // the warp's rows of the stage
       const int t0 = (r.tile0 + i) * kTile + r0;               // and their first token
       if (t0 >= r.kv || t0 + WT <= r.t_lo) {
@@ -577,15 +613,16 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       }
       const bool edge = t0 + WT > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
       const bool cut = t0 + WT - 1 > first_hi || t0 <= last_lo;  // some (token, row) pairs are masked
-      const int lrow = r0 + ((mi & 1) << 3) + (lane & 7);       // this lane's row in the ldmatrix loads
       // ---- scores: C layout (tokens g, g + 8; columns 2c, 2c + 1)
       float sc[KS][4];
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         float ska[NG], skb[NG];
         {
-          const uint32_t* sa = reinterpret_cast<const uint32_t*>(st + 2 * C::kKBytes + (r0 + 16 * u + g) * (NG * 2));
-          const uint32_t* sb = sa + 8 * (NG / 2);
+          uint32_t sa[NG / 2], sb[NG / 2];
+          const uint32_t at = st + ks_off + 2 * C::kKBytes + 16 * u * (NG * 2);
+          lds_words(at, sa);
+          lds_words(at + 8 * (NG * 2), sb);
 #pragma unroll
           for (int j = 0; j < NG / 2; ++j) {
             const float2 fa = __half22float2(u2h(sa[j])), fb = __half22float2(u2h(sb[j]));
@@ -597,11 +634,11 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         }
         sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.0f;
         auto begin = [&](int grp, float (&a)[4]) {
-          const float4 v = *reinterpret_cast<const float4*>(bias + (grp * 4 + c) * 4);
-          a[0] = v.x;
-          a[1] = v.y;
-          a[2] = v.z;
-          a[3] = v.w;
+          const uint4 v = lds128(bias_a + grp * 64);
+          a[0] = __uint_as_float(v.x);
+          a[1] = __uint_as_float(v.y);
+          a[2] = __uint_as_float(v.z);
+          a[3] = __uint_as_float(v.w);
         };
         auto add = [&](int grp, const float (&a)[4]) {
           sc[u][0] = fmaf(ska[grp], a[0], sc[u][0]);
@@ -609,12 +646,11 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           sc[u][2] = fmaf(skb[grp], a[2], sc[u][2]);
           sc[u][3] = fmaf(skb[grp], a[3], sc[u][3]);
         };
-        const int row = lrow + 16 * u;
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int gp = 0; gp < NC / 2; ++gp) {  // two 32-channel chunks per ldmatrix
             uint32_t x[4];                        // (tok g | g + 8) of chunk 2 gp, the same of 2 gp + 1
-            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(st + code_off<RB, kTile>(row, 2 * gp + (mi >> 1))));
+            ldmatrix_x4(x[0], x[1], x[2], x[3], st + code_at(u, gp));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t a[4], b[4];
@@ -623,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
               for (int k = 0; k < 32 / G; ++k) {
                 const int grp = (2 * gp + j) * (32 / G) + k;
-                const uint4 qv = qf[grp * 32 + lane];
+                const uint4 qv = lds128(qf_a + grp * 512);
                 float acc[4];
                 begin(grp, acc);
                 mma_16816(acc, a[0], b[0], a[1], b[1], qv.x, qv.y);
@@ -636,13 +672,13 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {  // one 32-channel chunk per ldmatrix
             uint32_t x[4];                   // (tok g | g + 8) of channels 0 - 15, the same of 16 - 31
-            ldmatrix_x4(x[0], x[1], x[2], x[3], smem_u32(st + code_off<RB, kTile>(row, 2 * ch + (mi >> 1))));
+            ldmatrix_x4(x[0], x[1], x[2], x[3], st + code_at(u, ch));
             uint32_t a[2], b[2], a2[2], b2[2];
             byte4_plus128(x[0], a);
             byte4_plus128(x[1], b);
             byte4_plus128(x[2], a2);
             byte4_plus128(x[3], b2);
-            const uint4 qv = qf[ch * 32 + lane];
+            const uint4 qv = lds128(qf_a + ch * 512);
             float acc[4];
             begin(ch * (32 / G), acc);
             mma_16816(acc, a[0], b[0], a[1], b[1], qv.x, qv.y);
@@ -669,14 +705,13 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       // ---- V scales: a token per lane (two lanes where the warp has 16) for the largest of them.
       // Those of tokens that hold no attended data, and those that are not finite, are made
       // zeros in place (this warp alone reads them)
-      uint8_t* vsc = ring + s * C::kStage + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
+      const uint32_t vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
       uint32_t top = 0;
       {
         constexpr int LW = NG / 2 * WT / 32;  // 32-bit words of a lane
-        uint32_t* vw = reinterpret_cast<uint32_t*>(vsc) + lane * LW;
+        const uint32_t vw = vsc + lane * (LW * 4);
         uint32_t x[LW];
-#pragma unroll
-        for (int k = 0; k < LW; ++k) x[k] = vw[k];
+        lds_words(vw, x);
 #pragma unroll
         for (int k = 0; k < LW; ++k) top = __vmaxu2(top, x[k]);
         const int t = t0 + lane * WT / 32;
@@ -693,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           if (dead || bad) {
             top = 0;
 #pragma unroll
-            for (int k = 0; k < LW; ++k) vw[k] = 0;
+            for (int k = 0; k < LW; ++k) asm volatile("st.shared.u32 [%0], %1;" ::"r"(vw + 4 * k), "r"(0) : "memory");
           }
           uint32_t bads = __ballot_sync(0xffffffffu, bad);
           fence_proxy_async_smem();  // before the producer's next copy into these rows
@@ -764,17 +799,14 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       }
       // ---- output: O[channel][column] += V[channel][token] P[token][column] scale; the codes
       // stand off too high, which a product with a constant takes out again
-      const uint8_t* vt = st + C::kKBytes;
-      const uint4 off = *consts;  // read here: four registers in order, not four moves for every product
+      const uint4 off = lds128(consts_a);  // read here: four registers in order, not four moves for every product
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         // the scales of tokens 2c, 2c + 1, 2c + 8, 2c + 9
         uint32_t sw[4][NG / 2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t* sp = reinterpret_cast<const uint32_t*>(vsc + (16 * u + 2 * c + (e & 1) + ((e & 2) << 2)) * (NG * 2));
-#pragma unroll
-          for (int j = 0; j < NG / 2; ++j) sw[e][j] = sp[j];
+          lds_words(vsc + (2 * c) * (NG * 2) + (16 * u + (e & 1) + ((e & 2) << 2)) * (NG * 2), sw[e]);
         }
         // P times the scale of group grp, as the two B registers
         auto weighted = [&](int grp, uint32_t& b0, uint32_t& b1) {
@@ -784,12 +816,11 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           b0 = h2u(__hmul2(u2h(s0), u2h(pb[u][0])));
           b1 = h2u(__hmul2(u2h(s1), u2h(pb[u][1])));
         };
-        const int row = lrow + 16 * u;
         if constexpr (BITS == 4) {
 #pragma unroll
           for (int gp = 0; gp < NC / 2; ++gp) {
             uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of chunk 2 gp, the same of 2 gp + 1
-            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB, kTile>(row, 2 * gp + (mi >> 1))));
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], st + C::kKBytes + code_at(u, gp));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int ch = 2 * gp + j;
@@ -821,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
           for (int ch = 0; ch < NC; ++ch) {
             uint32_t x[4];  // transposed: (tokens 2c.. | 2c + 8..) of channels 0 - 15, the same of 16 - 31
-            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], smem_u32(vt + code_off<RB, kTile>(row, 2 * ch + (mi >> 1))));
+            ldmatrix_x4_trans(x[0], x[1], x[2], x[3], st + C::kKBytes + code_at(u, ch));
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               uint32_t a[2], b[2], b0, b1;  // channels 2g, 2g + 1 of the half
