@@ -465,7 +465,9 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     const uint32_t sbytes = (uint32_t)(bt * NG * 2);
     const uint32_t box_bytes = 2 * ((uint32_t)(bt * RB) + sbytes);
     const uint64_t pol = p.rt_max == 1 ? l2_evict_first_policy() : l2_normal_policy();
-    int n = 0;
+    int s = 0;               // the stage, and the phase of its barriers
+    uint32_t phase = 0;
+    bool first = true;       // the ring's first round: its stages are free
     while (w.next(p)) {
       const int h = w.u / w.r.rt;
       const int32_t* row = p.table + (long long)w.b * p.table_stride;
@@ -482,11 +484,9 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         return e;
       };
       int page = entry(w.i0);
-      for (int i = w.i0; i < w.i1; ++i, ++n) {
-        const int s = n % C::kStages;
+      for (int i = w.i0; i < w.i1; ++i) {
         const int coming = entry(i + 1);
-        bool ok = true;
-        if (n >= C::kStages) ok = mbar_wait_bounded(&empty[s], ((n / C::kStages) - 1) & 1);
+        const bool ok = first || mbar_wait_bounded(&empty[s], phase ^ 1);
         if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) atomicOr(&g_paged_err, kErrTimeoutLoad);
           return;
@@ -516,6 +516,11 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           __syncwarp();
         }
         page = coming;
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1;
+          first = false;
+        }
       }
     }
     return;
@@ -523,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3, mi = lane >> 3;
-  int n = 0;        // tiles taken so far
+  int s = 0;        // the stage, and the phase of its barriers
+  uint32_t phase = 0;
   bool ok = true;   // false after a wait ran out: the rest is passed over, every barrier still met
   const uint32_t x1 = reinterpret_cast<volatile uint32_t*>(consts)[-2], x16 = reinterpret_cast<volatile uint32_t*>(consts)[-1];
   // shared-memory addresses of this lane: ring, query fragments, starts, constant, K scales of row
@@ -595,23 +601,28 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     int ve = kVeMin;                                  // V scales seen so far are below 2^ve, or ve = kVeMax
     uint32_t vlim = (uint32_t)(kVeMin + 15) << 10;    // the fp16 bits of 2^ve; above every scale from kVeMax on
     bool bad_row = false;                             // column g attends a V scale that is not finite
-    for (int i = w.i0; i < w.i1; ++i, ++n) {
-      const int s = n % C::kStages;
-      if (!ok) continue;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (n / C::kStages) & 1))) {
+    float ms0 = 0.0f, ms1 = 0.0f;                     // m + ve, 0 while nothing has been attended
+    auto release = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+    };
+    int t0 = (r.tile0 + w.i0) * kTile + WT * warp;               // the warp's first token of the tile
+    for (int i = w.i0; i < w.i1 && ok; ++i, t0 += kTile) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], phase))) {
         if (lane == 0) atomicOr(&g_paged_err, kErrTimeoutLoad);
         ok = false;
+        break;
+      }
+      const bool edge = t0 + WT > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
+      if (edge && (t0 >= r.kv || t0 + WT <= r.t_lo)) {          // none does
+        release();
         continue;
       }
       const uint32_t st = ring_a + s * C::kStage;               // shared-memory address of the stage
-      const int r0 = WT * warp;                                // the warp's rows of the stage
-      const int t0 = (r.tile0 + i) * kTile + r0;               // and their first token
-      if (t0 >= r.kv || t0 + WT <= r.t_lo) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        continue;
-      }
-      const bool edge = t0 + WT > r.kv || t0 < r.t_lo;          // some rows hold no attended token's data
       const bool cut = t0 + WT - 1 > first_hi || t0 <= last_lo;  // some (token, row) pairs are masked
       // ---- scores: C layout (tokens g, g + 8; columns 2c, 2c + 1)
       float sc[KS][4];
@@ -705,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       // ---- V scales: a token per lane (two lanes where the warp has 16) for the largest of them.
       // Those of tokens that hold no attended data, and those that are not finite, are made
       // zeros in place (this warp alone reads them)
-      const uint32_t vsc = st + 2 * C::kKBytes + C::kSBytes + r0 * (NG * 2);
+      const uint32_t vsc = st + 2 * C::kKBytes + C::kSBytes + WT * warp * (NG * 2);
       uint32_t top = 0;
       {
         constexpr int LW = NG / 2 * WT / 32;  // 32-bit words of a lane
@@ -781,11 +792,11 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         }
         m_run[0] = m0;
         m_run[1] = m1;
+        ms0 = m0 == -INFINITY ? 0.0f : m0 + (float)nve;
+        ms1 = m1 == -INFINITY ? 0.0f : m1 + (float)nve;
         ve = nve;
         vlim = ve < kVeMax ? (uint32_t)(ve + 15) << 10 : 0xFFFFu;
       }
-      const float ms0 = m_run[0] == -INFINITY ? 0.0f : m_run[0] + (float)ve;
-      const float ms1 = m_run[1] == -INFINITY ? 0.0f : m_run[1] + (float)ve;
       // P as the B operand of the output product: (tokens 2c, 2c + 1 | + 8; column g)
       uint32_t pb[KS][2];
 #pragma unroll
@@ -864,8 +875,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      release();
     }
 
     // ---- join the warps: M, L, and O = sum of o 2^(m - M), in true units; a quarter of the
