@@ -38,6 +38,7 @@
 //     divided by a power of two that bounds the V scales seen so far, so that its product
 //     with them (one more rounding) stays within fp16 for large and small V.
 #include <algorithm>
+#include <cmath>
 
 #include "kvq_internal.h"
 #include "kvq_ptx.cuh"
@@ -1013,7 +1014,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
     __syncthreads();
   }
   {
-    constexpr int NX = kRows * D / 4 / NT, U = 8 / NX;  // float4 values of a thread, partials in flight
+    constexpr int NX = kRows * D / 4 / NT, U = 8;  // float4 values of a thread, partials in flight
     float4 acc[NX];
 #pragma unroll
     for (int x = 0; x < NX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1097,15 +1098,14 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
 }
 
 // ---------------------------------------------------------------- host side
-constexpr int kMinTilesPerCta = 2;
 // Workspace: the partials of cut units, then per unit its prepared query, partial and
 // description. Nothing in it outlives a call.
 constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (2 * kRows + kRows * kMaxD) * 4;
 // of a unit, for every form of a head_dim: fragments, starts and factors; m, l, o; description
 constexpr size_t prep_bytes(int D) { return (size_t)(D / 16) * 512 + (D / 16) * 64 + kRows * 4; }
 constexpr size_t unit_bytes(int D) { return prep_bytes(D) + (2 * kRows + kRows * D) * 4 + 16; }
-// Query rows of a request from which on the prompt kernel takes a call.
-constexpr int kPromptRows = 48;
+constexpr int kFewRows = 32;            // query rows of a request up to which this file's kernels take every call
+constexpr long long kFewUnits = 4096;   // units up to which they may take one with more (their workspace: 28 MB)
 
 template <int D, int G, int BITS>
 kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
@@ -1146,7 +1146,10 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.num_pages = a.num_pages;
   p.page_shift = a.page_shift;
   p.window = a.window;
-  p.min_tiles = kMinTilesPerCta;
+  // A piece of t tiles takes about t us, joining a unit's n / t pieces about 0.1 n / t: where
+  // there are CTAs to spare, t = sqrt(0.1 n) (one KV head of 256, 16K tokens:
+  // 30.6 us with pieces of 2, 24.7 so).
+  p.min_tiles = std::max(2, (int)std::sqrt(0.1 * std::max(1, (p.max_kv + C::kTile - 1) / C::kTile)));
   const size_t units = (size_t)a.B * a.Hkv * p.rt_max;
   static_assert(C::kPrep <= prep_bytes(D), "workspace");
   p.part = reinterpret_cast<float*>(a.ws);
@@ -1185,16 +1188,50 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
 
 }  // namespace
 
-bool paged_uses_prompt(int Hq, int Hkv, int max_q_len) { return (long long)max_q_len * (Hq / Hkv) >= kPromptRows; }
+namespace {
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+// units of a call: row tiles of `rows` query rows, over heads and requests
+long long units_of(int B, int Hkv, int rows) { return (long long)B * Hkv * ceil_div(rows, kRows); }
+
+// Whether the prompt kernel takes a call, by what both would take (us, fitted to both kernels
+// on 1, 4 and 32 requests of 256, 2048 and 16384 tokens with 1 - 64 query tokens each). Here a
+// tile of 8 rows costs little and every row tile converts the cache again; there up to 256 (128)
+// rows cost about the same. For example 4 requests of 2048 tokens, 4 query heads per KV head:
+// 16 query tokens 29.9 us here and 29.5 there, 32 tokens 47.8 and 30.1; one request of 256
+// tokens: 64 query tokens 16.3 and 22.9; 32 requests: 8 tokens 28.6 and 30.7, 12 tokens 39.4
+// and 31.0.
+bool prefers_prompt(const PagedAttendHost& a) {
+  const int Gq = a.Hq / a.Hkv, q = std::min(a.max_q_len, a.n_q);
+  const long long rows = (long long)q * Gq;
+  if (rows <= kFewRows) return false;
+  const long long units = units_of(a.B, a.Hkv, (int)std::min<long long>(rows, 0x7fffffff - kRows));
+  if (units > kFewUnits) return true;
+  const bool d128 = a.pk->D == 128;
+  const long long all = (long long)a.n_q * Gq, R = d128 ? 256 : 128;
+  const long long cap = std::min<long long>(a.max_kv_len, (long long)a.max_pages << a.page_shift);
+  const long long kv = a.window ? std::min<long long>(cap, (long long)a.window + q) : cap;
+  const long long tiles = std::max(1ll, ceil_div(kv, d128 ? 128 : 64));
+  const double few_tiles = (double)a.Hkv * std::min(a.B * ceil_div(rows, kRows), all / kRows + a.B) * tiles;
+  const double prompt_tiles = (double)a.Hkv * std::min(a.B * ceil_div(rows, R), all / R + a.B) * tiles;
+  const double few = d128 ? 11.0 + 0.0035 * few_tiles + 0.012 * units : 16.0 + 0.004 * few_tiles + 0.02 * units;
+  const double prompt = d128 ? 22.0 + 0.020 * prompt_tiles : 27.0 + 0.035 * prompt_tiles;
+  return prompt < few;
+}
+
+}  // namespace
 
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
-  if (paged_uses_prompt(Hq, Hkv, max_q_len)) return prompt_part_bytes();
-  const size_t rt = ((size_t)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv) + kRows - 1) / kRows;
-  return kPartBytes + (size_t)B * Hkv * rt * unit_bytes(D);
+  const long long rows = (long long)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv);
+  // whatever kernel a call with these sizes, or smaller ones, goes to
+  long long units = units_of(B, Hkv, (int)std::min<long long>(rows, kFewRows));
+  if (rows > kFewRows) units = std::max(units, std::min(kFewUnits, units_of(B, Hkv, (int)std::min<long long>(rows, 0x7fffffff - kRows))));
+  const size_t few = kPartBytes + (size_t)units * unit_bytes(D);
+  return rows > kFewRows ? std::max(few, prompt_part_bytes()) : few;
 }
 
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s) {
-  if (paged_uses_prompt(a.Hq, a.Hkv, a.max_q_len)) return launch_attend_prompt(a, a.ws, s);
+  if (prefers_prompt(a)) return launch_attend_prompt(a, a.ws, s);
   return dispatch_dgb(a.pk->D, a.pk->G, a.pk->bits, [&](auto d, auto g, auto b) {
     return run_paged<decltype(d)::value, decltype(g)::value, decltype(b)::value>(a, s);
   });

@@ -34,6 +34,7 @@
 // maxima and sums are fp32. A token whose V scale is not finite is held as zeros and the
 // rows that attend it (and no others) are set to NaN at the end.
 #include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "kvq_internal.h"
@@ -923,18 +924,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
     const int row = x & 7, k4 = x >> 3;
     const float M = ml[0][row];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += 4) {
-      float4 v[4];
-      float m[4];
+    constexpr int U = 8;  // partials in flight
+    for (int k0 = 0; k0 < np; k0 += U) {
+      float4 v[U];
+      float m[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < U; ++k) {
         if (k0 + k < np) {
           m[k] = __ldcg(slot(k0 + k) + r0 + row);
           v[k] = __ldcg(reinterpret_cast<const float4*>(slot(k0 + k) + 2 * R) + (size_t)k4 * R + r0 + row);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < U; ++k) {
         if (k0 + k < np && m[k] != -INFINITY) {
           const float f = ex2_approx(m[k] - M);
           acc.x = fmaf(f, v[k].x, acc.x);
@@ -1039,7 +1041,10 @@ kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
   p.num_pages = a.num_pages;
   p.page_shift = a.page_shift;
   p.window = a.window;
-  p.min_tiles = 2;
+  // A piece of t tiles takes about 2.6 t us, joining a unit's n / t pieces about 0.4 n / t:
+  // t = sqrt(0.15 n) is best where there are CTAs to spare (one KV head of 256, 16K tokens,
+  // at 64 query tokens 90 us with pieces of 2, 60 with 6).
+  p.min_tiles = std::max(2, (int)std::sqrt(0.15 * std::max(1, (p.max_kv + C::T - 1) / C::T)));
   const long long blocks = ((long long)std::min(a.max_q_len, a.n_q) * p.Gq + C::R - 1) / C::R;
   const long long most = (long long)a.B * a.Hkv * blocks * std::max(1, (p.max_kv + C::T - 1) / C::T);
   const int sms = std::min(kPrMaxCtas, num_sms(a.pk->device));

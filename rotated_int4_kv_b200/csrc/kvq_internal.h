@@ -229,9 +229,7 @@ struct PagedAttendHost {
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len);
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s);
 uint32_t paged_error_flags(bool clear);
-// Rows (query tokens x heads of a KV head's group) of a request above which the prompt kernel
-// (kvq_attend_prompt.cu) takes a call.
-bool paged_uses_prompt(int Hq, int Hkv, int max_q_len);
+// The kernel for many query rows (kvq_attend_prompt.cu); launch_attend_paged chooses.
 size_t prompt_part_bytes();
 kvq_status launch_attend_prompt(const PagedAttendHost& a, void* part, cudaStream_t s);
 uint32_t prompt_error_flags(bool clear);

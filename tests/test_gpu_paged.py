@@ -493,3 +493,144 @@ def test_paged_cache_serves_ragged_requests(kvq, Hq, Hkv, D, P, bits):
                 length[b], texts[b] = 0, []
         taken = int(cache.free_head.item())
         assert taken == sum(-(-n // P) for n in length)
+
+
+# ---------------------------------------------------------------- what a mask hides, and other edges
+@pytest.mark.parametrize("window", [0, 25])
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 4), (256, 32, 8), (256, 32, 4)])
+@pytest.mark.parametrize("q", [5, 90])
+def test_attend_paged_masked_places_may_hold_anything(kvq, q, D, G, bits, window):
+    """NaN and infinite scales reach the queries that attend their tokens, and no others (causal and
+    window masks within the attended range, both kernels)."""
+    kv = 150
+    c = Cache(kvq, [kv, 40], [q, 1], 4, 1, D, G, bits, "srft", 16, seed=8, spoil=False)
+    bad = {"k": (kv - 2, np.nan), "v": (kv - 3, np.nan), "vi": (kv - q + 1, np.inf)}
+    for which, (t, val) in bad.items():
+        page, off = c.table[0][t // 16], t % 16
+        (c.ks if which == "k" else c.vs)[page, 0, off, 0] = val
+    c.dev[1], c.dev[3] = torch.from_numpy(c.ks).cuda(), torch.from_numpy(c.vs).cuda()
+    got = c.run(kvq, max_q_len=q, window=window).cpu().numpy().astype(np.float64)
+    pos = np.arange(kv - q, kv)
+    hit = np.zeros(q, bool)
+    for t, _ in bad.values():
+        hit |= (pos >= t) & ((pos - window < t) if window else True)
+    assert hit.any() and not hit.all()
+    assert np.isnan(got[:q][hit]).all()
+    ok = ~np.concatenate([hit, [False]])
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = c.ref(window)
+    check_rel_l2(got[ok].reshape(-1, D), ref[ok].reshape(-1, D), label="rows beside")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(24, 2, 128), (40, 1, 128), (36, 1, 256), (5, 5, 128)])
+def test_attend_paged_head_groups(kvq, Hq, Hkv, D):
+    """Groups of query heads that do not fill, or do not fit, a tile of rows."""
+    for q in ([1, 1], [3, 2], [50, 7]):
+        c = Cache(kvq, [200, 77], q, Hq, Hkv, D, 32, 4, "srft", 32, seed=6)
+        c.check(c.run(kvq, max_q_len=max(q)), label=f"q {q}")
+
+
+def test_attend_paged_agrees_across_the_choice_of_kernel(kvq):
+    """The same queries, told as longer than they are, go to the other kernel: the same formula."""
+    c = Cache(kvq, [6000, 5800, 6100, 5900], [9, 8, 9, 9], 8, 2, 128, 32, 4, "srft", 16, seed=4)
+    a = c.run(kvq, max_q_len=9).double()
+    b = c.run(kvq, max_q_len=35).double()
+    c.check(a)
+    c.check(b)
+    assert float((a - b).norm() / a.norm()) < 2e-3
+
+
+def test_paged_calls_on_two_streams(kvq):
+    """Calls with workspaces of their own may overlap."""
+    cs = [Cache(kvq, [5000, 300], [1, 1], 8, 1, 128, 32, 4, "srft", 16, seed=1),
+          Cache(kvq, [900, 700], [200, 300], 8, 2, 128, 32, 4, "srft", 16, seed=2)]
+    want = [c.run(kvq, max_q_len=max(c.q_lens)) for c in cs]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [kvq.make_paged_workspace(2, c.q.shape[1], c.kc.shape[1], 128, len(c.q), max(c.q_lens)) for c in cs]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(w) for _ in range(6)] for w in want]
+    for i in range(6):
+        for c, s, w, o in zip(cs, ss, ws, outs):
+            c.run(kvq, max_q_len=max(c.q_lens), workspace=w, out=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
+
+
+def test_paged_cache_past_32_bit_offsets(kvq):
+    """Pages beyond 4 GB of codes: encode, decode and attention reach them."""
+    D, H, P = 128, 8, 128
+    plan, params = make_plan(kvq, D, "k")
+    pages = (5 << 30) // (H * P * D // 2)
+    codes = torch.empty((pages, H, P, D // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((pages, H, P, D // 32), dtype=torch.float16, device="cuda")
+    vcodes, vscales = torch.empty_like(codes), torch.empty_like(scales)
+    n = 300
+    far = np.array([pages - 1, 0, pages - 2, pages // 2], np.int32)
+    t = np.arange(n)
+    slots = (far[t // P] * P + t % P).astype(np.int32)
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((2, n, H, D)).astype(np.float16)
+    xd = torch.from_numpy(x).cuda()
+    kvq.encode_paged([(plan, xd[0], codes, scales), (plan, xd[1], vcodes, vscales)], i32(slots))
+    back = kvq.decode_paged(plan, codes, scales, i32(slots)).cpu().numpy().astype(np.float64)
+    k = [a[torch.from_numpy(far).long().cuda()].cpu().numpy() for a in (codes, scales, vcodes, vscales)]
+    near = np.arange(4, dtype=np.int32)
+    nslots = (near[t // P] * P + t % P).astype(np.int32)
+    check_rel_l2(back.reshape(-1, D), paged_ref.decoded(k[0], k[1], nslots, P, params, 32, "srft", 4).reshape(-1, D))
+    for q in (1, 60):
+        qs = rng.standard_normal((q, H, D)).astype(np.float16)
+        got = kvq.attend_paged(plan, plan, torch.from_numpy(qs).cuda(), codes, scales, vcodes, vscales, i32(far[None]), i32([n]),
+                               i32([0, q]), max_q_len=q).cpu().numpy().astype(np.float64)
+        ref = paged_ref.attend(qs, *k, near[None], [n], [q], params, params, 32, "srft", 4)
+        check_rel_l2(got.reshape(-1, D), ref.reshape(-1, D), label=f"q {q}")
+
+
+def test_paged_cache_step_captured(kvq):
+    """A whole serving step (plan, encode, attention) as a CUDA graph: replays go on from the state
+    that the one before left, as eager steps do."""
+    B, Hkv, Hq, D, P = 3, 2, 8, 128, 16
+    made = []
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(rng.standard_normal((2, B, Hkv, D)).astype(np.float16)).cuda()
+    q = torch.from_numpy(rng.standard_normal((B, Hq, D)).astype(np.float16)).cuda()
+    ones = torch.ones(B, dtype=torch.int32, device="cuda")
+    for graph in (False, True):
+        cache = kvq.PagedInt4KVCache(1, B, Hkv, D, 30, P, 6, kvgen.plan_params(D, seed=2, kind="k"), kvgen.plan_params(D, seed=2, kind="v"))
+        out = torch.zeros_like(q)
+
+        def step():
+            s = cache.begin(ones, B)
+            cache.update(0, x[0], x[1], s)
+            cache.attend(0, q, s, max_q_len=1, out=out)
+        step()
+        torch.cuda.synchronize()
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+        for _ in range(39):
+            g.replay() if graph else step()
+        torch.cuda.synchronize()
+        assert cache.kv_lens.tolist() == [40] * B and int(cache.free_head.item()) == 9
+        made.append((out, cache.block_table, cache.k_codes[0], cache.v_scales[0]))
+    assert all(torch.equal(a, b) for a, b in zip(*made))
+
+
+def test_paged_empty_calls(kvq):
+    plan, _ = make_plan(kvq, 128, "k")
+    z = torch.zeros
+    kc, ks = z(2, 1, 16, 64, dtype=torch.uint8, device="cuda"), z(2, 1, 16, 4, dtype=torch.float16, device="cuda")
+    assert kvq.decode_paged(plan, kc, ks, i32([])).shape == (0, 1, 128)
+    kvq.encode_paged([(plan, z(0, 1, 128, dtype=torch.float16, device="cuda"), kc, ks)], i32([]))
+    kvq.encode_paged([], i32([]))
+    q = z(0, 4, 128, dtype=torch.float16, device="cuda")
+    assert kvq.attend_paged(plan, plan, q, kc, ks, kc, ks, i32(np.zeros((0, 2))), i32([])).shape == (0, 4, 128)
+    # requests without query tokens, and a request without pages
+    q = torch.ones(1, 4, 128, dtype=torch.float16, device="cuda")
+    out = kvq.attend_paged(plan, plan, q, kc, ks, kc, ks, i32([[0], [1], [1]]), i32([3, 0, 5]), i32([0, 0, 1, 1]), max_q_len=1)
+    assert (out == 0).all()
+    plan.close()
+    with pytest.raises(ValueError, match="closed"):
+        kvq.decode_paged(plan, kc, ks, i32([0]))
