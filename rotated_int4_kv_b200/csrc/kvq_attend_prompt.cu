@@ -414,19 +414,36 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         volatile uint32_t* fl = flags + (kt % kFlagRing) * 5;
         const uint32_t flag = fl[0];
         const float f = (flag & 1) ? fac * 256.0f : fac;
-        auto masked = [&](int t, float v) { return t > hi || t <= lo ? -INFINITY : v; };
-        // the row's maximum
+        // The row's maximum. S comes 32 columns at a time, the next ones on their way while these
+        // are used; tiles with masked places take a plain loop of their own.
         float mx = -INFINITY;
+        auto row_max = [&](const float (&x)[32]) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+        };
+        auto mask = [&](int c, float (&x)[32]) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (t0 + c + k > hi || t0 + c + k <= lo) x[k] = -INFINITY;
+        };
+        if (cut) {
 #pragma unroll 1
-        for (int c = 0; c < T; c += 32) {
-          float v[32];
-          tmem_ld32_now(ts + c, v);
-          if (cut) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
+          for (int c = 0; c < T; c += 32) {
+            float v[32];
+            tmem_ld32_now(ts + c, v);
+            mask(c, v);
+            row_max(v);
           }
+        } else {
+          float v[T / 32][32];
+          tmem_ld32(ts, v[0]);
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
+          for (int c = 0; c < T / 32; ++c) {
+            tmem_ld_wait();
+            tmem_regs_fence(v[c]);
+            if (c + 1 < T / 32) tmem_ld32(ts + 32 * (c + 1), v[c + 1 < T / 32 ? c + 1 : c]);
+            row_max(v[c]);
+          }
         }
         mx *= f;
         // the product before this tile's: every phase of odone is waited for, or a parity could
@@ -463,29 +480,41 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         // P, in two halves: the product starts on the first while the second is made
         const float ms = m_run == -INFINITY ? 0.0f : m_run;
         float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < T; c += 32) {
-          float v[32];
-          tmem_ld32_now(ts + c, v);
-          if (cut) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = masked(t0 + c + k, v[k]);
-          }
+        auto weights = [&](int c, const float (&x)[32]) {
           uint32_t h[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float a = ex2_approx(fmaf(v[2 * k], f, -ms)), b = ex2_approx(fmaf(v[2 * k + 1], f, -ms));
+            const float a = ex2_approx(fmaf(x[2 * k], f, -ms)), b = ex2_approx(fmaf(x[2 * k + 1], f, -ms));
             l0 += a;
             l1 += b;
             h[k] = pack_half2(a, b);
           }
-          tmem_st16(ts + c / 2, h);  // over columns that have been read
+          tmem_st16(ts + c / 2, h);  // over columns of S that have been read
           if (c + 32 == T / 2 || c + 32 == T) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             // a barrier per half: a warp may be at its second while another is at its first
             if (lane == 0) mbar_arrive(&pfull[2 * idx + (c + 32 == T)]);
+          }
+        };
+        if (cut) {
+#pragma unroll 1
+          for (int c = 0; c < T; c += 32) {
+            float v[32];
+            tmem_ld32_now(ts + c, v);
+            mask(c, v);
+            weights(c, v);
+          }
+        } else {
+          float v[T / 32][32];
+          tmem_ld32(ts, v[0]);
+#pragma unroll
+          for (int c = 0; c < T / 32; ++c) {
+            tmem_ld_wait();
+            tmem_regs_fence(v[c]);
+            if (c + 1 < T / 32) tmem_ld32(ts + 32 * (c + 1), v[c + 1 < T / 32 ? c + 1 : c]);
+            weights(32 * c, v[c]);
           }
         }
         l_run += l0 + l1;
@@ -685,16 +714,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           copy4(scale_s + (2 * j + 1) * NT, p.vs + at, r[j] >= 0);
         }
       };
-      auto fetch_half = [&](int h, const long long (&r)[NJ]) {
-        const uint8_t* base = (h & 2) ? p.vc : p.kc;
-        uint8_t* dst = ring + (h % NS) * C::kHalf;
+      auto fetch_half = [&](int isv, int half, bool next, int to) {  // into ring slot `to`
+        const uint8_t* base = isv ? p.vc : p.kc;
+        uint8_t* dst = ring + to * C::kHalf;
 #pragma unroll
         for (int x = 0; x < HJ; ++x) {
-          const long long row = (h & 1) ? r[HJ + x] : r[x];
-          const int ch = (h & 1) ? it_chunk(HJ + x) : it_chunk(x);
+          const int j = half * HJ + x;
+          const long long row = next ? rows[1][j] : rows[0][j];
 #pragma unroll
           for (int y = 0; y < C::CW / 4; ++y)
-            copy16(dst + (x * (C::CW / 4) + y) * NT * 16, base + max(row, 0ll) * RB + ch * (4 * BITS) + 16 * y, row >= 0);
+            copy16(dst + (x * (C::CW / 4) + y) * NT * 16, base + max(row, 0ll) * RB + it_chunk(j) * (4 * BITS) + 16 * y, row >= 0);
         }
       };
       // the start: entries of tiles 0 and 1, scales of tile 0, the first halves
@@ -710,9 +739,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       // halves 0 .. NS - 2, a group each
 #pragma unroll
       for (int h = 0; h < NS - 1; ++h) {
-        fetch_half(h, rows[0]);
+        fetch_half(h >> 1, h & 1, false, h);
         commit();
       }
+      int slot = 0;  // of the ring
       asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
       for (int i = 0; i < n; ++i, ++kt, ++kc, ++vc) {
         uint32_t ksc[NJ], vsc[NJ];
@@ -757,36 +787,39 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         asm volatile("bar.sync 1, %0;" ::"n"(ND * 32) : "memory");
         const uint32_t flag = *reinterpret_cast<volatile uint32_t*>(fl);
         if (dtid < 5) flags[((kt + kFlagRing / 2) % kFlagRing) * 5 + dtid] = 0;  // last read four tiles ago
+        // K, then V. Rolled, and softmax' loops as well: the roles' loops together have to stay
+        // within the instruction caches.
+#pragma unroll 1
+        for (int isv = 0; isv < 2; ++isv) {
+          uint8_t* tile = isv ? sV + (vc & 1) * C::kTile : sK + (kc & 1) * C::kTile;
+          const bool big = flag & (isv ? 2u : 1u);
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          const int h = 4 * i + part;
-          // half h has landed; the next one goes to the slot that the half before this left
-          asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
-          Item it[HJ];
+          for (int half = 0; half < 2; ++half) {
+            // this half has landed; the one NS - 1 after it goes to the slot that the half before left
+            asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+            Item it[HJ];
 #pragma unroll
-          for (int x = 0; x < HJ; ++x)
+            for (int x = 0; x < HJ; ++x) {
 #pragma unroll
-            for (int y = 0; y < C::CW / 4; ++y) {
-              const uint4 v = *reinterpret_cast<const uint4*>(ring + (h % NS) * C::kHalf + (x * (C::CW / 4) + y) * NT * 16);
-              it[x].c[4 * y] = v.x;
-              it[x].c[4 * y + 1] = v.y;
-              it[x].c[4 * y + 2] = v.z;
-              it[x].c[4 * y + 3] = v.w;
+              for (int y = 0; y < C::CW / 4; ++y) {
+                const uint4 v = *reinterpret_cast<const uint4*>(ring + slot * C::kHalf + (x * (C::CW / 4) + y) * NT * 16);
+                it[x].c[4 * y] = v.x;
+                it[x].c[4 * y + 1] = v.y;
+                it[x].c[4 * y + 2] = v.z;
+                it[x].c[4 * y + 3] = v.w;
+              }
+              it[x].s = isv ? vsc[half * HJ + x] : ksc[half * HJ + x];
             }
-          if (part + NS - 1 < 4) fetch_half(h + NS - 1, rows[0]);
-          else fetch_half(h + NS - 1, rows[1]);
-          commit();
-          if (part == 0) wait(kempty, kc);
-          if (part == 2) wait(vempty, vc);
-          uint8_t* tile = part < 2 ? sK + (kc & 1) * C::kTile : sV + (vc & 1) * C::kTile;
+            constexpr int kAhead = NS - 1;
+            const int ops = (half + kAhead) / 2;  // operands ahead: 1 or 2, known at compile time
+            fetch_half((isv + ops) & 1, (half + kAhead) & 1, ops == 2 || isv, slot == 0 ? NS - 1 : slot - 1);
+            commit();
+            if (half == 0) wait(isv ? vempty : kempty, isv ? vc : kc);
 #pragma unroll
-          for (int x = 0; x < HJ; ++x) {
-            const int j = (part & 1) * HJ + x;
-            it[x].s = part < 2 ? ksc[j] : vsc[j];
-            convert(tile, j, it[x], part < 2 ? flag & 1 : flag & 2);
+            for (int x = 0; x < HJ; ++x) convert(tile, half * HJ + x, it[x], big);
+            if (half == 1) announce(isv ? &vfull[vc & 1] : &kfull[kc & 1]);
+            slot = slot + 1 == NS ? 0 : slot + 1;
           }
-          if (part == 1) announce(&kfull[kc & 1]);
-          if (part == 3) announce(&vfull[vc & 1]);
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) rows[0][j] = rows[1][j];
