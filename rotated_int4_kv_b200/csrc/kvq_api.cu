@@ -310,10 +310,12 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   // column = channel), one fp16 rounding per entry; the columns of each 16-byte unit in
   // the order the kernel's dequantiser writes the channels (decode_unit_channel)
   std::vector<uint16_t> wdec((size_t)D * D);
+  std::vector<double> basis((size_t)D * D);  // Q, row = channel (also for the paged operands below)
   for (int n = 0; n < D; ++n)
     for (int k = 0; k < D; ++k) {
       const int c = (k & ~7) + kvq::decode_unit_channel(k & 7, bits);
       const double q = hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
+      basis[(size_t)c * D + n] = q;
       wdec[(size_t)n * D + k] = kvq::half_bits((float)((double)signs[n] * q / (double)lambda[c]));
     }
   // paged-attention operands: the query rotation Lambda^-1 Q diag(s) (row = channel) and the
@@ -325,22 +327,24 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   // 16 ks + 2c, + 1 | + 8, + 9)
   std::vector<uint16_t> wpg((size_t)4 * D * D);
   {
-    std::vector<double> m((size_t)D * D);
+    std::vector<double>& m = basis;
     double top = 0.0;
     for (int c = 0; c < D; ++c)
       for (int n = 0; n < D; ++n) {
-        const double q = hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
-        m[(size_t)c * D + n] = (double)signs[n] * q / (double)lambda[c];
-        top = std::max(top, std::fabs(m[(size_t)c * D + n]));
+        double& v = m[(size_t)c * D + n];
+        v = (double)signs[n] * v / (double)lambda[c];
+        top = std::max(top, std::fabs(v));
       }
     int e = 0;
     std::frexp(top, &e);  // top = f 2^e with f in [0.5, 1)
-    for (double& v : m) v = std::ldexp(v, 1 - e);
     p->wq_scale = p->wo_scale = (float)std::ldexp(1.0, e - 1);
+    const double up = std::ldexp(1.0, 1 - e);
+    std::vector<uint16_t> nat((size_t)D * D);  // row = channel, natural order
+    for (size_t x = 0; x < nat.size(); ++x) nat[x] = kvq::half_bits((float)(m[x] * up));
     for (int which = 0; which < 2; ++which) {
       uint16_t* row = wpg.data() + (size_t)which * D * D;
       uint16_t* frag = wpg.data() + (size_t)(2 + which) * D * D;
-      auto entry = [&](int i, int k) { return kvq::half_bits((float)(which ? m[(size_t)k * D + i] : m[(size_t)i * D + k])); };
+      auto entry = [&](int i, int k) { return which ? nat[(size_t)k * D + i] : nat[(size_t)i * D + k]; };
       for (int i = 0; i < D; ++i)
         for (int k = 0; k < D; ++k)
           row[(size_t)i * D + k] = which ? entry(i, kvq::word_channel(k, bits)) : entry(kvq::word_channel(i, bits), k);
