@@ -988,25 +988,41 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
     for (int ks = 0; ks < MT; ++ks) wf[t][ks] = __ldg(p.wo + ((warp + NWARP * t) * MT + ks) * 32 + lane);
   grid_dep_launch();
   grid_dep_wait();
+  // the loads of a step together: request and description; then the first partials' m, l and o
+  const int2 d = __ldcg(p.desc + unit);
   const Request r = request_of<128>(p, b);
   const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
-  if (nrows <= 0) return;
-  const int2 d = __ldcg(p.desc + unit);
+  if (nrows <= 0) return;  // no such unit: nothing was written for it
   const int np = max(1, min(d.y, kMaxCtas));
   // the first CTA's slot, then the first slots of the CTAs after it
   auto part = [&](int k) {
     return d.y == 0 ? p.part_unit + (size_t)unit * PART : p.part + (size_t)(k == 0 ? d.x : (d.x & ~1) + 2 * k) * PART;
   };
+  constexpr int NX = kRows * D / 4 / NT, U = 8;  // float4 values of a thread, partials in flight
+  float4 v[U][NX];
+  auto load_o = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int x = 0; x < NX; ++x)
+        if (k0 + k < np) v[k][x] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + 2 * kRows) + tid + x * NT);
+  };
   {
     const int row = tid & 7, k0 = tid >> 3;
-    float M = -INFINITY, L = 0.0f;
-    for (int k = k0; k < np; k += NT / 8) M = fmaxf(M, __ldcg(part(k) + row));
+    float m0 = -INFINITY, l0 = 0.0f;  // of partial k0
+    if (k0 < np) {
+      m0 = __ldcg(part(k0) + row);
+      l0 = __ldcg(part(k0) + kRows + row);
+    }
+    load_o(0);
+    float M = m0, L = 0.0f;
+    for (int k = k0 + NT / 8; k < np; k += NT / 8) M = fmaxf(M, __ldcg(part(k) + row));
     red[0][k0][row] = M;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < NT / 8; ++k) M = fmaxf(M, red[0][k][row]);
     for (int k = k0; k < np; k += NT / 8) {
-      const float m = __ldcg(part(k) + row), l = __ldcg(part(k) + kRows + row);
+      const float m = k == k0 ? m0 : __ldcg(part(k) + row), l = k == k0 ? l0 : __ldcg(part(k) + kRows + row);
       const float f = m != -INFINITY ? ex2_approx(m - M) : 0.0f;
       L += m != -INFINITY ? l * f : l;
       wts[k * kRows + row] = f;
@@ -1015,17 +1031,11 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
     __syncthreads();
   }
   {
-    constexpr int NX = kRows * D / 4 / NT, U = 8;  // float4 values of a thread, partials in flight
     float4 acc[NX];
 #pragma unroll
     for (int x = 0; x < NX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < np; k0 += U) {
-      float4 v[U][NX];
-#pragma unroll
-      for (int k = 0; k < U; ++k)
-#pragma unroll
-        for (int x = 0; x < NX; ++x)
-          if (k0 + k < np) v[k][x] = __ldcg(reinterpret_cast<const float4*>(part(k0 + k) + 2 * kRows) + tid + x * NT);
+      if (k0) load_o(k0);
 #pragma unroll
       for (int k = 0; k < U; ++k)
 #pragma unroll
