@@ -1157,10 +1157,11 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.num_pages = a.num_pages;
   p.page_shift = a.page_shift;
   p.window = a.window;
+  const double attended = a.window ? std::min<double>(p.max_kv, (double)a.window + std::min(a.max_q_len, a.n_q)) : p.max_kv;  // tokens of a unit
   // A piece of t tiles takes about t us, joining a unit's n / t pieces about 0.1 n / t: where
   // there are CTAs to spare, t = sqrt(0.1 n) (one KV head of 256, 16K tokens:
   // 30.6 us with pieces of 2, 24.7 so).
-  p.min_tiles = std::max(2, (int)std::sqrt(0.1 * std::max(1, (p.max_kv + C::kTile - 1) / C::kTile)));
+  p.min_tiles = std::max(2, (int)std::sqrt(0.1 * attended / C::kTile));
   const size_t units = (size_t)a.B * a.Hkv * p.rt_max;
   static_assert(C::kPrep <= prep_bytes(D), "workspace");
   p.part = reinterpret_cast<float*>(a.ws);

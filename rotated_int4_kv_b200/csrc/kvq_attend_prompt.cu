@@ -1081,10 +1081,11 @@ kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
   p.num_pages = a.num_pages;
   p.page_shift = a.page_shift;
   p.window = a.window;
+  const double attended = a.window ? std::min<double>(p.max_kv, (double)a.window + std::min(a.max_q_len, a.n_q)) : p.max_kv;  // tokens of a unit
   // A piece of t tiles takes about 2.6 t us, joining a unit's n / t pieces about 0.4 n / t:
   // t = sqrt(0.15 n) is best where there are CTAs to spare (one KV head of 256, 16K tokens,
   // at 64 query tokens 90 us with pieces of 2, 60 with 6).
-  p.min_tiles = std::max(2, (int)std::sqrt(0.15 * std::max(1, (p.max_kv + C::T - 1) / C::T)));
+  p.min_tiles = std::max(2, (int)std::sqrt(0.15 * attended / C::T));
   const long long blocks = ((long long)std::min(a.max_q_len, a.n_q) * p.Gq + C::R - 1) / C::R;
   const long long most = (long long)a.B * a.Hkv * blocks * std::max(1, (p.max_kv + C::T - 1) / C::T);
   const int sms = std::min(kPrMaxCtas, num_sms(a.pk->device));
