@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     const uint32_t box = (uint32_t)(bt * (RB < 128 ? RB : 128));
     const uint32_t sbytes = (uint32_t)(bt * NG * 2);
     const uint32_t box_bytes = 2 * ((uint32_t)(bt * RB) + sbytes);
+    const uint64_t pol = p.rt_max == 1 ? l2_evict_first_policy() : l2_normal_policy();
     int s = 0;               // the stage, and the phase of its barriers
     uint32_t phase = 0;
     bool first = true;       // the ring's first round: its stages are free
@@ -506,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
             for (int j = 0; j < (RB + 127) / 128; ++j) {
               uint8_t* kd = st + j * (kTile * 128) + x * box;
-              tma_load_3d(kd, &p.kmap, &full[s], 128 * j, off, ph);
-              tma_load_3d(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph);
+              tma_load_3d_hint(kd, &p.kmap, &full[s], 128 * j, off, ph, pol);
+              tma_load_3d_hint(kd + C::kKBytes, &p.vmap, &full[s], 128 * j, off, ph, pol);
             }
             uint8_t* sd = st + 2 * C::kKBytes + x * sbytes;
             const size_t srow = ((size_t)ph * P + off) * NG;
