@@ -175,7 +175,9 @@ class PagedInt4KVCache:
 
     def begin(self, q_lens: torch.Tensor, n_tokens: int, stream=None) -> PagePlan:
         """Pages, slots and lengths of a step in which request b gets q_lens[b] (int32, device) new
-        tokens, ``n_tokens`` of them at most in all; see :func:`page_plan`. ``kv_lens`` moves on."""
+        tokens, ``n_tokens`` of them at most in all; see :func:`page_plan`. ``kv_lens`` moves on, but not
+        for requests that get no pages (``info[2]`` of them): their tokens have no place in the cache,
+        and what :meth:`attend` gives for them means nothing."""
         step = PagePlan.empty(self.requests, n_tokens, self.device, stream)._replace(kv_lens=self.kv_lens)
         return page_plan(self.kv_lens, q_lens, self.block_table, self.free_pages, self.free_head, self.page_size,
                          out=step, stream=stream)

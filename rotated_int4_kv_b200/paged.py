@@ -104,7 +104,7 @@ def attend_paged(pk: Plan, pv: Plan, q, k_codes, k_scales, v_codes, v_scales, bl
     q fp16 [n, Hq, D] (token and head strides multiples of 8); block_table int32 [B, max_pages];
     kv_lens int32 [B], the new tokens included; q_starts int32 [B + 1] or None for one query token
     per request (n == B). ``max_q_len`` / ``max_kv_len`` bound the lengths, which the host cannot
-    see (defaults: n and the table's capacity); a tight ``max_q_len`` picks the right kernel.
+    see (defaults: n and the table's capacity); tight bounds pick the right kernel.
     ``window`` > 0: each token attends the last ``window`` tokens up to itself. Returns fp16
     [n, Hq, D]; rows of ``out`` that belong to no request are left as they were."""
     return _paged.attend_paged(pk, pv, q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, q_starts, max_q_len,
