@@ -237,8 +237,8 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   }
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(KVQ_ERR_DEVICE, "plan_create: no CUDA device");
-  cudaDeviceProp prop{};
-  if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess || prop.major != 10)
+  int major = 0;  // (one attribute: the whole property block takes milliseconds)
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major != 10)
     return fail(KVQ_ERR_DEVICE, "plan_create: needs a compute capability 10.x (sm_100) device");
 
   kvq_plan* p = new kvq_plan();
@@ -265,6 +265,11 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   // row 256 h + 128 + r = lo of the same channel.
   // SRHT plans: W = H diag(s) exactly (entries +-1; D rows, D columns), the factor
   // lambda_c / sqrt(D) is applied by the kernel's epilogue.
+  std::vector<double> basis((size_t)D * D);  // Q, row = channel: every operand below is made of it
+  for (int c = 0; c < D; ++c)
+    for (int n = 0; n < D; ++n)
+      basis[(size_t)c * D + n] =
+          hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
   std::vector<uint16_t> wt(hadamard ? (size_t)D * D : (size_t)2 * D * D);
   for (int c = 0; c < D; ++c) {
     const int h = c / 128, rr = c % 128;
@@ -273,7 +278,7 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
         wt[(size_t)c * D + n] = kvq::half_bits((float)(kvq::hadamard_value(c, n) * (double)signs[n]));
         continue;
       }
-      const double w = (double)lambda[c] * kvq::basis_value(c, n, D) * (double)signs[n];
+      const double w = (double)lambda[c] * basis[(size_t)c * D + n] * (double)signs[n];
       const uint16_t hi = kvq::half_bits((float)w);
       const uint16_t lo = kvq::half_bits((float)(w - (double)kvq::half_value(hi)));
       wt[(size_t)(256 * h + rr) * D + n] = hi;
@@ -310,12 +315,10 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   // column = channel), one fp16 rounding per entry; the columns of each 16-byte unit in
   // the order the kernel's dequantiser writes the channels (decode_unit_channel)
   std::vector<uint16_t> wdec((size_t)D * D);
-  std::vector<double> basis((size_t)D * D);  // Q, row = channel (also for the paged operands below)
   for (int n = 0; n < D; ++n)
     for (int k = 0; k < D; ++k) {
       const int c = (k & ~7) + kvq::decode_unit_channel(k & 7, bits);
-      const double q = hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
-      basis[(size_t)c * D + n] = q;
+      const double q = basis[(size_t)c * D + n];
       wdec[(size_t)n * D + k] = kvq::half_bits((float)((double)signs[n] * q / (double)lambda[c]));
     }
   // paged-attention operands: the query rotation Lambda^-1 Q diag(s) (row = channel) and the
