@@ -36,10 +36,11 @@
 //
 // Number formats. K and V are fp16 c * scale: exact multiples of 2^-24 below 2^-13 and one
 // rounding (2^-12 on average) elsewhere; a tile with a scale from 2^12 (int8: 2^9) on is held
-// divided by 2^8, so that no product leaves fp16. q~ and O enter their products as one fp16
-// rounding after a power-of-two normalisation per row, P as one fp16 rounding; S, O, the
-// maxima and sums are fp32. A token whose V scale is not finite is held as zeros and the
-// rows that attend it (and no others) are set to NaN at the end.
+// divided by 2^8, so that no product leaves fp16, and O is brought to the power of the tile
+// that is added next. q~ and O enter their products as one fp16 rounding after a
+// power-of-two normalisation per row, P as one fp16 rounding; S, O, the maxima and sums are
+// fp32. A token whose V scale is not finite is held as zeros and the rows that attend it
+// (and no others) are set to NaN at the end.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       const int lo = valid && p.window ? (int)max((long long)hi - p.window, -1ll) : -1;
       const int whi = __reduce_min_sync(0xffffffffu, hi), wlo = __reduce_max_sync(0xffffffffu, lo);
       float m_run = -INFINITY, l_run = 0.0f;
-      int ve = 0;          // O is held divided by 2^ve
+      int ve = 0;          // O is held divided by 2^ve, as V of the tile last added to it
       bool row_nan = false;
       for (int i = 0; i < n; ++i, ++kt) {
         const int idx = NQ == 2 ? qb : (i & 1);
@@ -456,14 +457,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         // the product before this tile's: every phase of odone is waited for, or a parity could
         // stand for the phase before (with one S buffer, S of this tile came after that product)
         if (SB == 2 && i > 0) wait(&odone[qb], (no + i - 1) & 1);
-        const int nve = (flag & 2) ? 8 : ve;
+        const int nve = (flag & 2) ? 8 : 0;
         constexpr float kSlack = 8.0f;
         if (__any_sync(0xffffffffu, mx > m_run + kSlack) || nve != ve) {
           const float m = fmaxf(m_run, mx);
           float g = m == m_run ? 1.0f : ex2_approx(m_run - m);
           l_run *= g;
           if (i > 0) {
-            if (nve != ve) g *= 1.0f / 256.0f;
+            if (nve != ve) g *= nve ? 1.0f / 256.0f : 256.0f;  // exact, and O has fp32's range
             if (SB == 1) wait(&odone[qb], (no + i - 1) & 1);
             if (!ok) continue;
 #pragma unroll 1
