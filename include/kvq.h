@@ -483,7 +483,19 @@ kvq_status kvq_decode_paged(const kvq_plan* plan, const uint8_t* codes, const ui
  * Two kernels serve the call, one for few query rows per request and one for many; which one
  * follows from the sizes and bounds given, so tight bounds are worth giving.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, DEVICE, CUDA.
+ *
+ * kvq_set_attend_paged_path / kvq_get_attend_paged_path -- which of the two it is
+ * (process-wide setting; to test or to time either):
+ *   0  default: by the sizes and bounds given;
+ *   1  the kernel for few query rows;
+ *   2  the kernel for many (prompts).
+ * Both serve every call. kvq_paged_workspace_size follows the setting: a workspace made under
+ * one may be too small under another (the call then answers WORKSPACE). Set it between calls,
+ * not while another thread makes one. Errors: INVALID_ARG for a value other than 0, 1, 2.
  */
+kvq_status kvq_set_attend_paged_path(int path);
+int kvq_get_attend_paged_path(void);
+
 size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int head_dim, int n_q, int max_q_len);
 
 kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,

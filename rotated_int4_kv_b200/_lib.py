@@ -69,6 +69,8 @@ def _load() -> ctypes.CDLL:
         "kvq_page_release": (I, [P, P, P, L, I, I, I, P, I, P, P]),
         "kvq_encode_paged": (I, [ctypes.POINTER(PagedEncodeJob), I, I, I, I, I, P, P]),
         "kvq_decode_paged": (I, [P, P, P, I, I, I, P, I, P, P]),
+        "kvq_set_attend_paged_path": (I, [I]),
+        "kvq_get_attend_paged_path": (I, []),
         "kvq_paged_workspace_size": (S, [I, I, I, I, I, I]),
         "kvq_attend_paged": (I, [P, P, P, L, L, P, P, P, P, I, I, P, I, L, P, P, I, I, I, I, I, I, I, F, P, P, S, P]),
         "kvq_poll_device_errors": (I, [U32P]),

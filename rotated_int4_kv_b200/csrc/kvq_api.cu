@@ -81,6 +81,8 @@ std::atomic<int> g_decode_path{0};
 
 int decode_path() { return g_decode_path.load(); }
 
+std::atomic<int> g_attend_paged_path{0};
+
 // All jobs share head_dim and group (checked by the callers).
 kvq_status dispatch_encode(const kvq_encode_job* jobs, int njobs, cudaStream_t s) {
   const kvq_plan* p = jobs[0].plan;
@@ -827,8 +829,16 @@ kvq_status kvq_decode_paged(const kvq_plan* p, const uint8_t* codes, const uint1
 
 size_t kvq_paged_workspace_size(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 128 && D != 256) || n_q < 0 || max_q_len < 1) return 0;
-  return kvq::paged_workspace_bytes(B, Hq, Hkv, D, n_q, max_q_len);
+  return kvq::paged_workspace_bytes(B, Hq, Hkv, D, n_q, max_q_len, kvq::g_attend_paged_path.load());
 }
+
+kvq_status kvq_set_attend_paged_path(int path) {
+  if (path < 0 || path > 2) return fail(KVQ_ERR_INVALID_ARG, "set_attend_paged_path: path must be 0, 1 or 2");
+  kvq::g_attend_paged_path.store(path);
+  return KVQ_OK;
+}
+
+int kvq_get_attend_paged_path(void) { return kvq::g_attend_paged_path.load(); }
 
 kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16_t* q, int64_t q_token_stride,
                             int64_t q_head_stride, const uint8_t* kc, const uint16_t* ks, const uint8_t* vc,
@@ -861,14 +871,15 @@ kvq_status kvq_attend_paged(const kvq_plan* pk, const kvq_plan* pv, const uint16
       return fail(KVQ_ERR_ALIGNMENT, "attend_paged: query strides must be multiples of 8 elements");
     if ((n_q > 1 && q_token_stride < 0) || (Hq > 1 && q_head_stride < 0))
       return fail(KVQ_ERR_INVALID_ARG, "attend_paged: negative query stride");
-    const size_t need = kvq::paged_workspace_bytes(B, Hq, Hkv, pk->D, n_q, max_q_len);
+    const int path = kvq::g_attend_paged_path.load();
+    const size_t need = kvq::paged_workspace_bytes(B, Hq, Hkv, pk->D, n_q, max_q_len, path);
     if (!ws || ws_bytes < need) return fail(KVQ_ERR_WORKSPACE, "attend_paged: workspace missing or too small");
     if (!kvq::aligned16(ws)) return fail(KVQ_ERR_ALIGNMENT, "attend_paged: workspace must be 16-byte aligned");
     st = kvq::check_plan_device(pk);
     if (st != KVQ_OK) return st;
     const kvq::PagedAttendHost a{pk, pv, q, q_token_stride, q_head_stride, kc, ks, vc, vs, num_pages,
                                  page_shift_of(page_size), table, max_pages, table_stride, kv_lens, q_starts, B, n_q,
-                                 Hq, Hkv, max_q_len, max_kv_len, window, sigma, out, ws, ws_bytes};
+                                 Hq, Hkv, max_q_len, max_kv_len, window, sigma, out, ws, ws_bytes, path};
     return kvq::launch_attend_paged(a, (cudaStream_t)stream);
   });
 }

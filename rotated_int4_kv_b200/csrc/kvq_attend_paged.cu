@@ -1214,6 +1214,7 @@ long long units_of(int B, int Hkv, int rows) { return (long long)B * Hkv * ceil_
 // tokens: 64 query tokens 16.3 and 22.9; 32 requests: 8 tokens 28.6 and 30.7, 12 tokens 39.4
 // and 31.0.
 bool prefers_prompt(const PagedAttendHost& a) {
+  if (a.path) return a.path == 2;
   const int Gq = a.Hq / a.Hkv, q = std::min(a.max_q_len, a.n_q);
   const long long rows = (long long)q * Gq;
   if (rows <= kFewRows) return false;
@@ -1233,8 +1234,10 @@ bool prefers_prompt(const PagedAttendHost& a) {
 
 }  // namespace
 
-size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len) {
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len, int path) {
   const long long rows = (long long)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv);
+  if (path == 1) return kPartBytes + (size_t)(ceil_div(rows, kRows) * B * Hkv) * unit_bytes(D);
+  if (path == 2) return prompt_part_bytes();
   // whatever kernel a call with these sizes, or smaller ones, goes to
   long long units = units_of(B, Hkv, (int)std::min<long long>(rows, kFewRows));
   if (rows > kFewRows) units = std::max(units, std::min(kFewUnits, units_of(B, Hkv, (int)std::min<long long>(rows, 0x7fffffff - kRows))));

@@ -1057,7 +1057,7 @@ kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
   p.ks = a.ks;
   p.vc = a.vc;
   p.vs = a.vs;
-  p.table = a.table;
+  p.table = a.table ? a.table : a.kv_lens;  // no pages: an address for copies of zero bytes
   p.kv_lens = a.kv_lens;
   p.q_starts = a.q_starts;
   p.wq = a.pk->wq_dev;

@@ -225,8 +225,9 @@ struct PagedAttendHost {
   uint16_t* out;
   void* ws;
   size_t ws_bytes;
+  int path;  // 0: either kernel, by what both would take; 1: few query rows; 2: prompts
 };
-size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len);
+size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len, int path);
 kvq_status launch_attend_paged(const PagedAttendHost& a, cudaStream_t s);
 uint32_t paged_error_flags(bool clear);
 // The kernel for many query rows (kvq_attend_prompt.cu); launch_attend_paged chooses.

@@ -21,6 +21,7 @@ from .api import Plan
 
 _paged.set_check(check)
 PAGE_SIZES = (16, 32, 64, 128)
+ATTEND_PAGED_PATHS = {"auto": 0, "few": 1, "prompt": 2}
 
 
 def _new(make, shape, dtype, device, stream):
@@ -94,6 +95,17 @@ def make_paged_workspace(B: int, Hq: int, Hkv: int, head_dim: int, n_tokens: int
     query tokens and ``max_q_len`` of one request. Calls that may overlap need one each."""
     n = max(16, paged_workspace_size(B, Hq, Hkv, head_dim, B if n_tokens is None else n_tokens, max_q_len))
     return _new(torch.empty, n, torch.uint8, device or torch.device("cuda"), stream)
+
+
+def set_attend_paged_path(path: str) -> None:
+    """Select the kernel of :func:`attend_paged`: "auto" (by sizes and bounds), "few" (few query rows per
+    request) or "prompt" (many). Workspaces are sized for the setting."""
+    check(lib.kvq_set_attend_paged_path(ATTEND_PAGED_PATHS[path]), "kvq_set_attend_paged_path")
+
+
+def get_attend_paged_path() -> str:
+    v = int(lib.kvq_get_attend_paged_path())
+    return {n: k for k, n in ATTEND_PAGED_PATHS.items()}[v]
 
 
 def attend_paged(pk: Plan, pv: Plan, q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, q_starts=None,

@@ -1,14 +1,28 @@
-"""Paged attention where its two kernels (few query rows, prompts) differ in how they hold
-numbers: V scales on both sides of the prompt kernel's limit, scales that are not finite, weights
-far below a row's largest. Against the 64-bit form; tolerances as derived in tests/paged_ref.py."""
+"""Both kernels of the paged attention (few query rows, prompts), each chosen by the setting and
+run over the whole range: head_dim 128 and 256, masks, windows, empty rows, bad pages, far pages,
+captured calls, and V scales on both sides of the prompt kernel's limit. Against the 64-bit form;
+tolerances as derived in tests/paged_ref.py."""
 import numpy as np
 import pytest
 
-from tests.parity import rel_l2
-from tests.test_gpu_paged import Cache, kvq, no_device_errors  # noqa: F401  (fixtures)
+import kvgen
+from tests import paged_ref
+from tests.parity import check_rel_l2, rel_l2
+from tests.test_gpu_paged import Cache, i32, kvq, make_plan, no_device_errors  # noqa: F401  (fixtures)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=["few", "prompt"])
+def path(kvq, request):  # noqa: F811
+    kvq.set_attend_paged_path(request.param)
+    yield request.param
+    kvq.set_attend_paged_path("auto")
+
+
+FORMS = [(32, 4, "srft"), (16, 4, "srht"), (32, 8, "srht"), (16, 8, "srft")]
+HEADS = [(12, 2, 128), (32, 8, 128), (8, 1, 128), (4, 1, 256), (3, 3, 128), (2, 2, 256), (40, 1, 128), (36, 1, 256)]
 
 
 def put_scales(c):
@@ -54,3 +68,211 @@ def test_prompt_attention_with_v_scales_across_the_limit(kvq, D, G, bits, big, w
     scale_tokens(c, 0, "v", spots[big], 420.0 if bits == 4 else 520.0)
     put_scales(c)
     check_rows(c, c.run(kvq, max_q_len=m, window=window), window, label=f"{big} window {window}")
+
+
+# ---------------------------------------------------------------- each kernel over the whole range
+@pytest.mark.parametrize("G,bits,xf", FORMS)
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_each_kernel_over_lengths_and_masks(kvq, path, Hq, Hkv, D, G, bits, xf):
+    """Single tokens, several, prompts; tiles, pages and row blocks that end inside; requests without
+    tokens, without queries, with more queries than tokens."""
+    for seed, (P, kv, q, w) in enumerate((
+            (16, [1, 17, 300, 0], [1, 1, 1, 1], 0), (64, [63, 64, 65, 700, 2], [1, 1, 1, 1, 1], 40),
+            (32, [300, 9, 40], [7, 0, 6], 33), (16, [3, 50], [6, 2], 0), (128, [129, 257], [70, 1], 0),
+            (64, [330, 70, 128], [130, 33, 128], 0), (16, [400, 5], [65, 5], 100))):
+        c = Cache(kvq, kv, q, Hq, Hkv, D, G, bits, xf, P, seed=seed, pad=3)
+        out = torch.full((sum(q) + 3, Hq, D), 5.0, dtype=torch.float16, device="cuda")
+        c.check(c.run(kvq, max_q_len=max(q), window=w, out=out), window=w, label=f"kv {kv} q {q} window {w}")
+        assert (out[sum(q):] == 5.0).all()   # rows of no request stay
+
+
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (256, 32, 4), (256, 16, 8)])
+def test_each_kernel_on_long_caches(kvq, path, D, G, bits):
+    """Units cut into pieces that several CTAs share; many of them, and row blocks of several units."""
+    for kv, q, P, w in (([9000, 3, 500], [1, 1, 1], 64, 0), ([5000, 4097], [1, 5], 16, 300), ([3000], [300], 32, 0),
+                        ([2500, 40, 2300], [90, 40, 150], 128, 700)):
+        c = Cache(kvq, kv, q, 4, 1, D, G, bits, "srft", P, seed=21)
+        c.check(c.run(kvq, max_q_len=max(q), window=w), window=w, label=f"kv {kv} q {q}")
+
+
+@pytest.mark.parametrize("B", [300, 1300])
+def test_each_kernel_with_many_requests(kvq, path, B):
+    rng = np.random.default_rng(B)
+    kv, q = rng.integers(0, 40, B), rng.integers(0, 3, B)
+    for q in (q, np.where(rng.random(B) < 0.05, 30, q)):
+        c = Cache(kvq, kv, q, 4, 1, 128, 32, 4, "srft", 16, seed=3)
+        c.check(c.run(kvq, max_q_len=int(q.max())))
+
+
+@pytest.mark.parametrize("window", [0, 25])
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 4), (128, 32, 8), (256, 32, 8), (256, 16, 8), (256, 32, 4)])
+@pytest.mark.parametrize("q", [5, 90])
+def test_each_kernel_keeps_masked_places_apart(kvq, path, q, D, G, bits, window):
+    """NaN scales reach the queries that attend their tokens, and no others, also within a tile."""
+    kv = 150
+    c = Cache(kvq, [kv, 40], [q, 1], 4, 1, D, G, bits, "srft", 16, seed=8, spoil=False)
+    bad = {"k": kv - 2, "v": kv - q + 1}
+    for which, t in bad.items():
+        (c.ks if which == "k" else c.vs)[c.table[0][t // 16], 0, t % 16, -1] = np.nan
+    put_scales(c)
+    got = c.run(kvq, max_q_len=q, window=window).cpu().numpy().astype(np.float64)
+    pos = np.arange(kv - q, kv)
+    hit = np.zeros(q, bool)
+    for t in bad.values():
+        hit |= (pos >= t) & ((pos - window < t) if window else True)
+    assert hit.any() and not hit.all()
+    assert np.isnan(got[:q][hit]).all()
+    ok = ~np.concatenate([hit, [False]])
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = c.ref(window)
+    check_rel_l2(got[ok].reshape(-1, D), ref[ok].reshape(-1, D), label="rows beside")
+
+
+@pytest.mark.parametrize("D,bits", [(128, 4), (128, 8), (256, 4), (256, 8)])
+@pytest.mark.parametrize("q", [1, 90])
+def test_each_kernel_over_the_range_of_scales(kvq, path, q, D, bits):
+    """V and K scales over fp16's whole range, all alike and with large ones in some tokens only."""
+    for vs, ks in ((9000.0, 1.0), (6e-7, 1.0), (1.0, 3e4), (300.0, 40.0)):
+        for where in (slice(0, 300), slice(0, 60), slice(130, 150)):
+            c = Cache(kvq, [300], [q], 4, 1, D, 32, bits, "srft", 16, seed=5, q_size=1.0 / ks)
+            for which, by in (("k", ks), ("v", vs)):
+                scale_tokens(c, 0, which, np.arange(300)[where], by * (7 if which == "v" and by > 1 else 1))
+            put_scales(c)
+            ref = c.ref()
+            got = c.run(kvq, max_q_len=q).cpu().numpy()
+            fits = np.abs(ref) < 6e4
+            big = np.where(fits, ref, 0)
+            # fp16 outputs: half a step is at least 2^-25, whatever the value
+            err = np.abs(np.where(fits, got, 0) - big)
+            assert (err <= 4e-3 * np.abs(big).max(-1, keepdims=True) + 2.0 ** -24).all(), (vs, ks, where)
+
+
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("big", ["front", "middle", "one", "alternate"])
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (256, 32, 8)])
+def test_each_kernel_with_v_scales_across_the_limit(kvq, path, D, G, bits, big, window):
+    """As above, at sizes where one unit holds rows that attend the large tokens and rows that do not."""
+    n, m = 700, 120
+    c = Cache(kvq, [n], [m], 2, 1, D, G, bits, "srft", 32, seed=12, spoil=False)
+    scale_tokens(c, 0, "v", np.arange(n), 20 * 7 if bits == 4 else 2 * 127)
+    spots = {"front": np.arange(0, n - m + 5), "middle": np.arange(n - m + 20, n - m + 40), "one": np.array([n - m - 20]),
+             "alternate": np.arange(0, n, 150)}
+    scale_tokens(c, 0, "v", spots[big], 420.0 if bits == 4 else 520.0)
+    put_scales(c)
+    check_rows(c, c.run(kvq, max_q_len=m, window=window), window, label=f"{big} window {window}")
+
+
+def test_each_kernel_raises_a_flag_for_bad_pages(kvq, path):
+    for D in (128, 256):
+        c = Cache(kvq, [400], [30], 4, 1, D, 32, 4, "srft", 16, spoil=False)
+        for bad in (-1, 10 ** 6):
+            c.tab[0, 3] = bad
+            got = c.run(kvq, max_q_len=30)
+            torch.cuda.synchronize()
+            assert kvq.poll_device_errors() == 8 and torch.isfinite(got).all()
+        c = Cache(kvq, [500], [100], 4, 1, D, 32, 4, "srft", 16)
+        c.tab[0, :20] = -1                       # no attended token lies there
+        c.check(c.run(kvq, max_q_len=100, window=40), window=40)
+        # no pages at all: nothing to attend to
+        q = torch.ones(9, 4, D, dtype=torch.float16, device="cuda")
+        out = kvq.attend_paged(c.pk, c.pv, q, *c.dev, torch.empty((1, 0), dtype=torch.int32, device="cuda"), i32([9]), i32([0, 9]))
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_each_kernel_is_deterministic_and_captures(kvq, path, D):
+    for q in ([1, 1, 1], [40, 1, 25]):
+        c = Cache(kvq, [3000, 41, 777], q, 12, 2, D, 32, 4, "srft", 16)
+        want = c.run(kvq, max_q_len=max(q))
+        ws = kvq.make_paged_workspace(3, 12, 2, D, sum(q), max(q))
+        out = torch.zeros_like(want)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        c.run(kvq, max_q_len=max(q), workspace=ws, out=out, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(kvq, max_q_len=max(q), workspace=ws, out=out)
+            c.run(kvq, max_q_len=max(q), workspace=ws, out=out)
+        for _ in range(3):
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        c.kv[0] = 1500                           # new lengths in place: the captured call follows them
+        c.lens[0] = 1500
+        g.replay()
+        c.check(out)
+
+
+def test_each_kernel_cuts_lengths_to_the_bounds(kvq, path):
+    c = Cache(kvq, [100, 40], [6, 2], 4, 1, 128, 32, 4, "srft", 16)
+    out, full = (torch.full((8, 4, 128), 5.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    c.run(kvq, max_q_len=4, out=out)
+    c.run(kvq, max_q_len=6, out=full)
+    assert (out[4:6] == 5.0).all()
+    assert rel_l2(out[:4].double().cpu(), full[:4].double().cpu()).max() < 2e-3
+    c.lens = i32([250, 40])       # past the table's (7 + 1) pages of 16: cut to max_kv_len
+    c.check(c.run(kvq, max_q_len=6, max_kv_len=100))
+
+
+def test_kernels_agree(kvq):
+    """The same queries through both: the same formula, other roundings."""
+    for D, G, bits in ((128, 32, 4), (128, 16, 8), (256, 32, 4), (256, 16, 8)):
+        c = Cache(kvq, [6000, 580, 61], [9, 80, 2], 8, 2, D, G, bits, "srft", 16, seed=4)
+        got = []
+        try:
+            for path in ("few", "prompt"):
+                kvq.set_attend_paged_path(path)
+                got.append(c.run(kvq, max_q_len=80).double())
+        finally:
+            kvq.set_attend_paged_path("auto")
+        c.check(got[0])
+        c.check(got[1])
+        assert not torch.equal(*got)
+
+
+def test_each_kernel_past_32_bit_offsets(kvq, path):
+    """Pages beyond 4 GB of codes."""
+    H, P = 8, 128
+    for D, bits in ((128, 4), (256, 8)):
+        plan, params = make_plan(kvq, D, "k", bits=bits)
+        row = D * bits // 8
+        pages = (9 << 29) // (H * P * row)
+        far = np.array([pages - 1, 0, pages - 2, pages // 2], np.int32)
+        rng = np.random.default_rng(1)
+        c = Cache(kvq, [300], [1], H, H, D, 32, bits, "srft", P, seed=3, spoil=False)   # random pages to place far away
+        big = []
+        for a in c.dev:
+            t = torch.empty((pages, *a.shape[1:]), dtype=a.dtype, device="cuda")
+            t[torch.from_numpy(far).long().cuda()] = a[:4]
+            big.append(t)
+        near = [a[:4].cpu().numpy() for a in c.dev]
+        for q in (1, 60):
+            qs = rng.standard_normal((q, H, D)).astype(np.float16)
+            got = kvq.attend_paged(plan, plan, torch.from_numpy(qs).cuda(), *big, i32(far[None]), i32([300]), i32([0, q]), max_q_len=q)
+            ref = paged_ref.attend(qs, *near, np.arange(4, dtype=np.int32)[None], [300], [q], params, params, 32, "srft", bits)
+            check_rel_l2(got.cpu().numpy().astype(np.float64).reshape(-1, D), ref.reshape(-1, D), label=f"q {q}")
+        del big
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_cache_class_through_each_kernel(kvq, path, D):
+    """A prompt, then single tokens, through the class; the attention checked on what the pages hold."""
+    B, Hkv, Hq, P, n = 2, 2, 8, 32, 90
+    kp, vp = kvgen.plan_params(D, seed=2, kind="k"), kvgen.plan_params(D, seed=2, kind="v")
+    cache = kvq.PagedInt4KVCache(1, B, Hkv, D, 12, P, 6, kp, vp)
+    rng = np.random.default_rng(5)
+    length = [0, 0]
+    for q in ([n, 40], [1, 1], [0, 3]):
+        t = sum(q)
+        step = cache.begin(i32(q), t)
+        x = torch.from_numpy(rng.standard_normal((2, t, Hkv, D)).astype(np.float16)).cuda()
+        cache.update(0, x[0], x[1], step)
+        qs = rng.standard_normal((t, Hq, D)).astype(np.float16)
+        got = cache.attend(0, torch.from_numpy(qs).cuda(), step, max_q_len=max(q)).cpu().numpy().astype(np.float64)
+        length = [a + b for a, b in zip(length, q)]
+        pages = [a[0].cpu().numpy() for a in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
+        want = paged_ref.attend(qs, *pages, cache.block_table.cpu().numpy(), length, q, kp, vp, 32, "srft", 4)
+        check_rel_l2(got.reshape(-1, D), want.reshape(-1, D), label=f"{q}")
