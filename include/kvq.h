@@ -479,7 +479,8 @@ kvq_status kvq_decode_paged(const kvq_plan* plan, const uint8_t* codes, const ui
  * A table entry outside [0, num_pages) raises device error flag 8 (kvq_poll_device_errors)
  * and page 0 is read in its place; entries of pages with no attended token are not read.
  * Codes and scales behind a request's last token may hold anything; a scale that is not
- * finite makes the outputs of the queries that attend its token NaN, and no others.
+ * finite (NaN or infinite, of K or V) makes the outputs of the queries that attend its token
+ * NaN, and no others.
  * Two kernels serve the call, one for few query rows per request and one for many; which one
  * follows from the sizes and bounds given, so tight bounds are worth giving.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, DEVICE, CUDA.

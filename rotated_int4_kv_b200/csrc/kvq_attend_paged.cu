@@ -704,7 +704,18 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
           }
         }
       }
+      // an infinite K scale can make a score -inf, the mark of a masked place: it becomes NaN (in
+      // tiles without masked places only where the smallest score, mn, says so)
+      auto unmark = [&] {
+#pragma unroll
+        for (int u = 0; u < KS; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (sc[u][e] == -INFINITY) sc[u][e] = __int_as_float(0x7fc00000);
+      };
+      float mn = 0.0f;
       if (cut) {
+        unmark();
 #pragma unroll
         for (int u = 0; u < KS; ++u) {
           const int ta = t0 + 16 * u + g, tb = ta + 8;
@@ -714,6 +725,9 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
             if (tb > hi[e] || tb <= lo[e]) sc[u][2 + e] = -INFINITY;
           }
         }
+      } else {
+#pragma unroll
+        for (int u = 0; u < KS; ++u) mn = fminf(fminf(mn, fminf(sc[u][0], sc[u][1])), fminf(sc[u][2], sc[u][3]));
       }
       // ---- V scales: a token per lane (two lanes where the warp has 16) for the largest of them.
       // Those of tokens that hold no attended data, and those that are not finite, are made
@@ -767,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       }
       mx0 *= rowfac[0];
       mx1 *= rowfac[1];
-      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1] || top >= vlim)) {
+      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1] || top >= vlim || mn == -INFINITY)) {
+        if (mn == -INFINITY) unmark();
         constexpr float kHeadroom = 3.0f;
         float a = mx0, b = mx1;
 #pragma unroll

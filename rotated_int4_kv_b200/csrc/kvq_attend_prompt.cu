@@ -780,6 +780,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             vx = max(vx, max(b & 0xFFFFu, b >> 16));
           }
           if (max(kx, vx) >= kBig) {
+            if (kx >= 0x7C00u) {  // an infinite scale becomes NaN: its score may be -inf, the mark of a masked place
+#pragma unroll
+              for (int j = 0; j < NJ; ++j)
+                if ((ksc[j] & 0x7C00u) == 0x7C00u || (ksc[j] & 0x7C000000u) == 0x7C000000u) ksc[j] = 0x7FFF7FFFu;
+            }
             if (vx >= 0x7C00u) {
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {

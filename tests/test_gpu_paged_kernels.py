@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import kvgen
+import oracle
 from tests import paged_ref
 from tests.parity import check_rel_l2, rel_l2
 from tests.test_gpu_paged import Cache, i32, kvq, make_plan, no_device_errors  # noqa: F401  (fixtures)
@@ -276,3 +277,46 @@ def test_cache_class_through_each_kernel(kvq, path, D):
         pages = [a[0].cpu().numpy() for a in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
         want = paged_ref.attend(qs, *pages, cache.block_table.cpu().numpy(), length, q, kp, vp, 32, "srft", 4)
         check_rel_l2(got.reshape(-1, D), want.reshape(-1, D), label=f"{q}")
+
+
+# ---------------------------------------------------------------- scales that are not finite
+@pytest.mark.parametrize("bad", [np.inf, -np.inf])
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 8), (256, 32, 4), (256, 16, 4), (256, 32, 8)])
+@pytest.mark.parametrize("q", [3, 90])
+def test_each_kernel_makes_infinite_k_scales_nan(kvq, path, q, D, G, bits, bad):
+    """An infinite K scale would give the score -inf, as masked places have, where its group's sum is
+    negative: the queries that attend its token get NaN all the same, and no others."""
+    kv, window = 200, 50
+    for t in (kv - 2, kv - q - 20, kv - q - 60):       # attended by the last queries, by all or the first, by none
+        c = Cache(kvq, [kv, 40], [q, 1], 8, 2, D, G, bits, "srft", 16, seed=9, spoil=False)
+        c.ks[c.table[0][t // 16], :, t % 16, -1] = bad
+        put_scales(c)
+        got = c.run(kvq, max_q_len=q, window=window).cpu().numpy().astype(np.float64)
+        pos = np.arange(kv - q, kv)
+        hit = np.concatenate([(pos >= t) & (pos - window < t), [False]])
+        assert hit.any() == (t != kv - q - 60)
+        assert np.isnan(got[hit]).all()
+        with np.errstate(invalid="ignore", over="ignore"):
+            ref = c.ref(window)
+        check_rel_l2(got[~hit].reshape(-1, D), ref[~hit].reshape(-1, D), label="rows beside")
+
+
+@pytest.mark.parametrize("D,bits", [(128, 4), (256, 8)])
+@pytest.mark.parametrize("q", [2, 90])
+def test_each_kernel_sees_a_score_of_minus_infinity(kvq, path, q, D, bits):
+    """A group of equal codes under an infinite scale, and queries whose rotated form is -1 there and 0
+    elsewhere: every product is -inf or 0 and the token's score exactly that of a masked place."""
+    kv = 150
+    c = Cache(kvq, [kv], [q], 1, 1, D, 32, bits, "srft", 16, seed=10, spoil=False)
+    signs, lam = (np.asarray(a, np.float64) for a in c.kp)
+    basis = np.asarray(oracle.srft_forward(np.eye(D), signs, np.ones(D), "srft"), np.float64)   # [sample, channel]
+    c.q[:] = (basis[:, :32] @ -lam[:32]).astype(np.float16)
+    c.qd.copy_(torch.from_numpy(c.q).cuda())
+    t = kv - 1
+    page = c.table[0][t // 16]
+    c.kc[page, 0, t % 16, : 32 * bits // 8] = 0x11 if bits == 4 else 1
+    c.ks[page, 0, t % 16, 0] = np.inf
+    c.dev[0] = torch.from_numpy(c.kc).cuda()
+    put_scales(c)
+    got = c.run(kvq, max_q_len=q).cpu().numpy()
+    assert np.isnan(got[-1]).all() and np.isfinite(got[:-1]).all()
