@@ -37,7 +37,8 @@
 // Number formats. K and V are fp16 c * scale: exact multiples of 2^-24 below 2^-13 and one
 // rounding (2^-12 on average) elsewhere; a tile with a scale from 2^12 (int8: 2^9) on is held
 // divided by 2^8, so that no product leaves fp16, and O is brought to the power of the tile
-// that is added next. q~ and O enter their products as one fp16 rounding after a
+// that is added next (beside such a scale, V below 2^-6 in the same tile keeps 2^-17 of 1, not
+// its own 11 bits). q~ and O enter their products as one fp16 rounding after a
 // power-of-two normalisation per row, P as one fp16 rounding; S, O, the maxima and sums are
 // fp32. A token whose V scale is not finite is held as zeros and the rows that attend it
 // (and no others) are set to NaN at the end.
@@ -780,21 +781,24 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             vx = max(vx, max(b & 0xFFFFu, b >> 16));
           }
           if (max(kx, vx) >= kBig) {
-            if (kx >= 0x7C00u) {  // an infinite scale becomes NaN: its score may be -inf, the mark of a masked place
-#pragma unroll
-              for (int j = 0; j < NJ; ++j)
-                if ((ksc[j] & 0x7C00u) == 0x7C00u || (ksc[j] & 0x7C000000u) == 0x7C000000u) ksc[j] = 0x7FFF7FFFu;
-            }
-            if (vx >= 0x7C00u) {
+            uint32_t odd = 0;
+            if (max(kx, vx) >= 0x7C00u) {  // scales that are not finite are taken out of the maxima
+              auto not_finite = [](uint32_t s) { return (s & 0x7C00u) == 0x7C00u || (s & 0x7C000000u) == 0x7C000000u; };
+              kx = vx = 0;
 #pragma unroll
               for (int j = 0; j < NJ; ++j) {
-                if ((vsc[j] & 0x7C00u) == 0x7C00u || (vsc[j] & 0x7C000000u) == 0x7C000000u) {
+                // an infinite K scale becomes NaN: its score may be -inf, the mark of a masked place
+                if (not_finite(ksc[j])) ksc[j] = 0x7FFF7FFFu;
+                else kx = max(kx, max(ksc[j] & 0x7FFFu, (ksc[j] >> 16) & 0x7FFFu));
+                if (not_finite(vsc[j])) {
                   vsc[j] = 0;
+                  odd = 4u;
                   atomicOr(&fl[1 + (it_row(j) >> 5)], 1u << (it_row(j) & 31));
                 }
+                vx = max(vx, max(vsc[j] & 0x7FFFu, (vsc[j] >> 16) & 0x7FFFu));
               }
             }
-            atomicOr(&fl[0], (kx >= kBig ? 1u : 0u) | (vx >= kBig ? 2u : 0u) | (vx >= 0x7C00u ? 4u : 0u));
+            atomicOr(&fl[0], (kx >= kBig ? 1u : 0u) | (vx >= kBig ? 2u : 0u) | odd);
           }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(ND * 32) : "memory");

@@ -320,3 +320,22 @@ def test_each_kernel_sees_a_score_of_minus_infinity(kvq, path, q, D, bits):
     put_scales(c)
     got = c.run(kvq, max_q_len=q).cpu().numpy()
     assert np.isnan(got[-1]).all() and np.isfinite(got[:-1]).all()
+
+
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 4), (256, 32, 8), (256, 16, 4)])
+def test_a_scale_that_is_no_number_leaves_its_tile_as_precise(kvq, path, D, G, bits):
+    """Tokens with small scales beside one with a NaN: the queries that do not attend that one are as
+    near the formula as without it."""
+    kv, window, t = 130, 30, 20
+    for which, size in (("v", 5e-4), ("k", 2e-3)):
+        c = Cache(kvq, [kv], [100], 2, 1, D, G, bits, "srft", 16, seed=13, spoil=False, q_size=1.0 if which == "v" else 2.0 ** -3 / size)
+        scale_tokens(c, 0, which, np.arange(kv), size)
+        (c.ks if which == "k" else c.vs)[c.table[0][t // 16], 0, t % 16, 1] = np.nan
+        put_scales(c)
+        got = c.run(kvq, max_q_len=100, window=window).cpu().numpy().astype(np.float64)
+        with np.errstate(invalid="ignore"):
+            ref = c.ref(window)
+        ok = np.arange(kv - 100, kv) - window >= t
+        # fp16 outputs of this size are subnormal: half a step, 2^-25, per element beside the usual 2e-3
+        err = np.linalg.norm((got - ref)[ok], axis=-1)
+        assert (err <= 2e-3 * np.linalg.norm(ref[ok], axis=-1) + 2.0 ** -25 * np.sqrt(D)).all(), which
