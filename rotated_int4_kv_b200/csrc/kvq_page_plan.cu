@@ -77,10 +77,11 @@ __device__ __forceinline__ long long block_scan(long long v, long long* part, lo
 
 template <int NT>
 __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ PagePlanParams p) {
-  extern __shared__ int32_t s_req[];   // [B] start, [B] first entry of the free list (-1: refused), [B] cached tokens
+  // [B] start (its low 32 bits), [B] first entry of the free list (-1: refused), [B] cached tokens
+  extern __shared__ int32_t s_req[];
   __shared__ long long part[32];
   __shared__ long long served_pages;
-  __shared__ int refused;
+  __shared__ int refused, past;  // past: the first request whose start is above 2^31 - 1
   int32_t* s_start = s_req;
   int32_t* s_first = s_req + p.B;
   int32_t* s_kv = s_req + 2 * p.B;
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
   if (tid == 0) {
     served_pages = 0;
     refused = 0;
+    past = p.B;
   }
   grid_dep_launch();
   grid_dep_wait();
@@ -114,7 +116,8 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
     const bool fits = want <= p.max_pages;
     const long long need = fits ? want - ((kv + P - 1) >> p.page_shift) : 0;
     const bool served = fits && (need == 0 || n_at + need <= room);
-    s_start[b] = sat32(q_at);
+    s_start[b] = (int32_t)(uint32_t)q_at;
+    if (q_at > 0x7fffffffll) atomicMin(&past, b);
     s_first[b] = served ? (need ? head + (int)n_at : 0) : -1;
     s_kv[b] = (int32_t)kv;
     if (served) got += need;
@@ -141,11 +144,14 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
     p.info[2] = refused;
     p.info[3] = sat32(wanted);
   }
-  // starts and lengths; the start of b + 1 bounds the new tokens of b, which a served
-  // request has in full (its length fits its table, so it is below the saturation)
-  auto q_of = [&](int b) { return (b + 1 < p.B ? (long long)s_start[b + 1] : (long long)sat32(total)) - s_start[b]; };
+  // starts and lengths; the new tokens of b are the difference of two starts, exact from their
+  // low 32 bits however large the sums are
+  const int first_past = past;
+  auto q_of = [&](int b) {
+    return (long long)((b + 1 < p.B ? (uint32_t)s_start[b + 1] : (uint32_t)total) - (uint32_t)s_start[b]);
+  };
   for (int b = gt; b < p.B; b += nthreads) {
-    if (p.fill) p.q_starts[b] = s_start[b];
+    if (p.fill) p.q_starts[b] = b < first_past ? s_start[b] : 0x7fffffff;
     if (p.move) p.kv_out[b] = s_first[b] >= 0 ? (int32_t)(s_kv[b] + q_of(b)) : s_kv[b];
   }
   if (!p.fill) return;
@@ -188,7 +194,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
   for (long long t = gt; t < p.n_slots; t += nthreads) {
     int slot = -1, pos = -1;
     if (t < total && p.B > 0) {
-      int lo = 0, hi = p.B;  // last request whose start is <= t
+      int lo = 0, hi = first_past;  // last request whose start is <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_start[mid] <= t) lo = mid;
