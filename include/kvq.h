@@ -393,7 +393,8 @@ kvq_status kvq_attend_decode_ref(const uint16_t* q, const uint16_t* k, const uin
  * kvq_page_plan -- the block tables and slot maps of one serving step, built on the GPU:
  * request b has kv_lens[b] cached tokens and gets q_lens[b] new ones (negative lengths
  * count as 0). With have = ceil(kv / P), want = ceil((kv + q) / P), need = want - have:
- *   a request whose `want` exceeds max_pages is refused, and needs nothing; the others are
+ *   a request whose `want` exceeds max_pages, or whose kv + q would pass 2^31 - 1, is refused,
+ *   and needs nothing; the others are
  *   served in order while the running total of their needs (upto) fits the free entries
  *   left, n_free - *free_head; once it does not, every later request with need > 0 is
  *   refused as well (those that fit their last page are served).

@@ -4,7 +4,7 @@
 // For request b with kv cached and q new tokens and pages of P tokens,
 //   have = ceil(kv / P), want = ceil((kv + q) / P), need = want - have (0 when want does
 //   not fit the table), upto = inclusive prefix sum of need,
-//   served = want fits and (need == 0 or upto <= free entries left),
+//   served = want fits, kv + q <= 2^31 - 1 and (need == 0 or upto <= free entries left),
 // the pages of a served request come from the free list at upto - need, and token j goes to
 // position kv + j, slot = page * P + position % P. Integers only; every output is a
 // function of the inputs alone (no atomics), so two calls on the same inputs agree.
@@ -48,6 +48,11 @@ struct PagePlanParams {
 };
 
 __device__ __forceinline__ int32_t sat32(long long v) { return v > 0x7fffffffll ? 0x7fffffff : (int32_t)v; }
+
+// Whether a request of kv + q tokens fits its table row, and its length 32 bits.
+__device__ __forceinline__ bool fits_table(const PagePlanParams& p, long long kv, long long q) {
+  return kv + q <= min((long long)p.max_pages << p.page_shift, 0x7fffffffll);
+}
 
 // Inclusive prefix sum of v over the block of NT threads; total in *sum. `part` holds 32 values.
 template <int NT>
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
     const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
     const long long want = (kv + q + P - 1) >> p.page_shift;
     qs += q;
-    ns += want <= p.max_pages ? want - ((kv + P - 1) >> p.page_shift) : 0;
+    ns += fits_table(p, kv, q) ? want - ((kv + P - 1) >> p.page_shift) : 0;
   }
   long long total, wanted;
   long long q_at = block_scan<NT>(qs, part, &total) - qs;
@@ -113,7 +118,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
   for (int b = b0; b < b1; ++b) {
     const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
     const long long want = (kv + q + P - 1) >> p.page_shift;
-    const bool fits = want <= p.max_pages;
+    const bool fits = fits_table(p, kv, q);
     const long long need = fits ? want - ((kv + P - 1) >> p.page_shift) : 0;
     const bool served = fits && (need == 0 || n_at + need <= room);
     s_start[b] = (int32_t)(uint32_t)q_at;

@@ -46,3 +46,18 @@ def test_requests_behind_sums_past_32_bits_are_served_in_full(kvq, B, n, in_plac
     assert np.array_equal(out.slots.cpu().numpy()[:first], ref["slots"][:first])
     assert (out.slots[first:] == -1).all()
     assert np.array_equal(out.positions.cpu().numpy(), np.concatenate([kv[0] + np.arange(first), kv[1] + np.arange(n - first)]))
+
+
+def test_a_request_whose_length_passes_32_bits_is_refused(kvq):  # noqa: F811
+    """A table wide enough for more than 2^31 - 1 tokens of one request."""
+    P, M = 128, 2 ** 24 + 4
+    table = torch.zeros((1, M), dtype=torch.int32, device="cuda")
+    free = i32(np.arange(10))
+    for kv, q, served in ((TOP - 5, 5, True), (TOP - 5, 6, False), (TOP, 0, True), (TOP - 200, 201, False)):
+        head = i32([0])
+        step = kvq.page_plan(i32([kv]), i32([q]), table, free, head, P, q)
+        assert step.kv_lens.tolist() == [kv + q if served else kv]
+        assert step.info.tolist()[2] == (0 if served else 1)
+        assert served or (int(head.item()) == 0 and (step.slots == -1).all())
+        # positions past 2^31 - 1 saturate
+        assert step.positions.tolist() == [min(kv + j, TOP) for j in range(q)]
