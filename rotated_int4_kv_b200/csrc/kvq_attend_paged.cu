@@ -35,9 +35,13 @@
 //   * q~ is one fp16 rounding per element after a power-of-two normalisation per row
 //     (2^-12 relative on average, so a score's error is about 2^-12 of |q||k|/sqrt(D), below
 //     what the fp16 rounding of the caller's q has put there).
-//   * P is fp16 (2^-12 relative on average; its sum l is in fp32 of the unrounded values),
-//     divided by a power of two that bounds the V scales seen so far, so that its product
-//     with them (one more rounding) stays within fp16 for large and small V.
+//   * P is fp16 (its sum l is in fp32 of the unrounded values), raised to the top of fp16's
+//     range: the largest weight is 2^15, or as much less as V scales from 1 on ask for so that
+//     its product with them (one more rounding) stays within fp16 too. A running maximum's
+//     headroom takes 2^3 of that at most. Weights down to 2^-26 of the largest so have one
+//     rounding of 2^-12 on average (V scales below 1; with scales from 2^15 on: down to 2^-10),
+//     smaller ones an error of at most 2^-37 (2^-21) of the largest; a weight times its scale
+//     is off by as much again, of the largest weight times a scale of 1 (2^16).
 #include <algorithm>
 #include <cmath>
 
@@ -594,14 +598,15 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
       last_lo = p.window ? (int)max((long long)r.kv - r.qn + tok - p.window, -1ll) : -1;
     }
 
-    // ---- (3) the tiles. l and o are held divided by 2^(m + ve)
-    constexpr int kVeMin = -11, kVeMax = 4;
+    // ---- (3) the tiles. l and o are held divided by 2^(m + ve): weights up to 2^-ve, whose product
+    // with a V scale below 2^(ve + 15) stays below 2^15
+    constexpr int kVeMin = -15, kVeMax = 1;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
     float o[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    int ve = kVeMin;                                  // V scales seen so far are below 2^ve, or ve = kVeMax
-    uint32_t vlim = (uint32_t)(kVeMin + 15) << 10;    // the fp16 bits of 2^ve; above every scale from kVeMax on
+    int ve = kVeMin;                                  // V scales seen so far are below 2^(ve + 15)
+    uint32_t vlim = (uint32_t)(kVeMin + 30) << 10;    // the fp16 bits of 2^(ve + 15); above every scale at kVeMax
     bool bad_row = false;                             // column g attends a V scale that is not finite
     float ms0 = 0.0f, ms1 = 0.0f;                     // m + ve, 0 while nothing has been attended
     auto release = [&] {
@@ -792,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         }
         const uint32_t t = __reduce_max_sync(0xffffffffu, top);
         int nve = ve;
-        if (t >= vlim) nve = max(ve, min((int)(t >> 10) - 14, kVeMax));
+        if (t >= vlim) nve = (int)(t >> 10) - 29;
         const float m0 = a > m_run[0] ? a + kHeadroom : m_run[0];
         const float m1 = b > m_run[1] ? b + kHeadroom : m_run[1];
         const float fv = pow2f(ve - nve);
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
         ms0 = m0 == -INFINITY ? 0.0f : m0 + (float)nve;
         ms1 = m1 == -INFINITY ? 0.0f : m1 + (float)nve;
         ve = nve;
-        vlim = ve < kVeMax ? (uint32_t)(ve + 15) << 10 : 0xFFFFu;
+        vlim = ve < kVeMax ? (uint32_t)(ve + 30) << 10 : 0xFFFFu;
       }
       // P as the B operand of the output product: (tokens 2c, 2c + 1 | + 8; column g)
       uint32_t pb[KS][2];

@@ -339,3 +339,48 @@ def test_a_scale_that_is_no_number_leaves_its_tile_as_precise(kvq, path, D, G, b
         # fp16 outputs of this size are subnormal: half a step, 2^-25, per element beside the usual 2e-3
         err = np.linalg.norm((got - ref)[ok], axis=-1)
         assert (err <= 2e-3 * np.linalg.norm(ref[ok], axis=-1) + 2.0 ** -25 * np.sqrt(D)).all(), which
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 8), (256, 32, 4), (256, 32, 8)])
+@pytest.mark.parametrize("vsize", [0.1, 10.0, 30000.0])
+@pytest.mark.parametrize("sink", ["first", "last"])
+@pytest.mark.parametrize("path", ["few"], indirect=True)
+@pytest.mark.parametrize("q", [1, 40])
+def test_each_kernel_weighs_a_tail_below_a_sink(kvq, path, q, sink, vsize, D, G, bits):
+    """One token whose score is 8 to 17.5 above that of thousands, and whose V is 0: the output is the tail's
+    alone, its weights 2^-11 to 2^-25 of the largest. Queries along the sink's K, so that its score has no
+    cancelling terms, and V of one sign, so that lost weights do not average out."""
+    n = 4000
+    for gap in (8.0, 13.3, 16.0, 17.5):
+        if gap > 16 and vsize > 1:
+            continue      # weights below 2^-24 times 30000 are beyond what the few-row kernel's range holds
+        c = Cache(kvq, [n], [q], 1, 1, D, G, bits, "srft", 64, seed=15, spoil=False)
+        t0 = 0 if sink == "first" else n - q
+        at = (c.table[0][t0 // 64], slice(None), t0 % 64)
+        scale_tokens(c, 0, "k", np.arange(n), 0.0)
+        c.ks[at] = 1.0 if bits == 4 else 1.0 / 16
+        signs, lam = (np.asarray(a, np.float64) for a in c.kp)
+        slot = np.array([c.table[0][t0 // 64] * 64 + t0 % 64])
+        y = oracle.srft_forward(paged_ref.decoded(c.kc, c.ks, slot, 64, c.kp, *c.form)[0, 0], signs, lam, "srft")
+        aim = oracle.srft_inverse(lam ** 2 * y, signs, lam, "srft")          # R^T lambda y: q~ = y
+        c.q[:] = (aim * gap * np.sqrt(D) / (y @ y)).astype(np.float16)
+        c.qd.copy_(torch.from_numpy(c.q).cuda())
+        codes = np.abs(oracle.unpack_codes(c.vc, bits)).astype(np.int8)
+        c.vc = oracle.pack_codes(codes, bits).view(np.uint8).reshape(c.vc.shape)
+        c.dev[2] = torch.from_numpy(c.vc).cuda()
+        scale_tokens(c, 0, "v", np.arange(n), vsize * (7 if bits == 4 else 127))
+        c.vs[at] = 0.0
+        put_scales(c)
+        ref = c.ref()
+        if np.abs(ref).max() > 6e4:
+            continue      # the outputs leave fp16
+        # Everything else 2e-3 (tests/paged_ref.py); the score's relative error, sqrt(3) roundings of rms
+        # 2^-11 / sqrt(3) averaged over D like terms, times the score, three standard deviations; and the
+        # kernels' bounds on a weight, relative to the largest: 2^-32 (prompt); 2^-37 for the weight and again, of a
+        # scale of 1, for its product with the scale, both 2^16 larger for scales from 2^15 on.
+        tail = np.exp(gap)
+        tol = 2e-3 + 3 * 2.0 ** -11 * gap / np.sqrt(D)
+        tol += tail * (2.0 ** -32 if path == "prompt" else 2.0 ** -37 * (1 + 2 / vsize) if vsize < 1 else 2.0 ** (-37 + np.log2(vsize) + 2))
+        got = c.run(kvq, max_q_len=q).cpu().numpy().astype(np.float64)
+        check_rel_l2(got.reshape(-1, D), ref.reshape(-1, D), tol=tol, label=f"gap {gap}")
