@@ -39,8 +39,9 @@
 // divided by 2^8, so that no product leaves fp16, and O is brought to the power of the tile
 // that is added next (beside such a scale, V below 2^-6 in the same tile keeps 2^-17 of 1, not
 // its own 11 bits). q~ and O enter their products as one fp16 rounding after a
-// power-of-two normalisation per row, P as one fp16 rounding; S, O, the maxima and sums are
-// fp32. A token whose V scale is not finite is held as zeros and the rows that attend it
+// power-of-two normalisation per row, P as one fp16 rounding, its largest value between 2^7
+// and 2^15: weights down to 2^-21 of the largest keep 2^-12 on average, smaller ones an error of
+// at most 2^-32 of the largest. S, O, the maxima and sums are fp32. A token whose V scale is not finite is held as zeros and the rows that attend it
 // (and no others) are set to NaN at the end.
 #include <algorithm>
 #include <cmath>
@@ -487,7 +488,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
             if (((fl[1 + (t >> 5)] >> (t & 31)) & 1) && t0 + t <= hi && t0 + t > lo) row_nan = true;
         }
         // P, in two halves: the product starts on the first while the second is made
-        const float ms = m_run == -INFINITY ? 0.0f : m_run;
+        // (times 2^kPTop, as l and O then are: with the slack 2^15, within fp16)
+        constexpr float kPTop = 15.0f - kSlack;
+        const float ms = m_run == -INFINITY ? 0.0f : m_run - kPTop;
         float l0 = 0.0f, l1 = 0.0f;
         auto weights = [&](int c, const float (&x)[32]) {
           uint32_t h[16];

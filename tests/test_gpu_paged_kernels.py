@@ -345,7 +345,6 @@ def test_a_scale_that_is_no_number_leaves_its_tile_as_precise(kvq, path, D, G, b
 @pytest.mark.parametrize("D,G,bits", [(128, 32, 4), (128, 16, 8), (256, 32, 4), (256, 32, 8)])
 @pytest.mark.parametrize("vsize", [0.1, 10.0, 30000.0])
 @pytest.mark.parametrize("sink", ["first", "last"])
-@pytest.mark.parametrize("path", ["few"], indirect=True)
 @pytest.mark.parametrize("q", [1, 40])
 def test_each_kernel_weighs_a_tail_below_a_sink(kvq, path, q, sink, vsize, D, G, bits):
     """One token whose score is 8 to 17.5 above that of thousands, and whose V is 0: the output is the tail's
