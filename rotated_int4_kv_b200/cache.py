@@ -13,7 +13,7 @@ import numpy as np
 import torch
 
 from .api import (Plan, attend_decode, attend_decode_append, decode, encode_batch, make_workspace)
-from .paged import (PAGE_SIZES, PagePlan, attend_paged, encode_paged, make_paged_workspace, page_plan, page_release,
+from .paged import (PAGE_SIZES, PagePlan, _new, attend_paged, encode_paged, page_plan, page_release,
                     paged_workspace_size)
 
 
@@ -197,10 +197,10 @@ class PagedInt4KVCache:
         need = paged_workspace_size(self.requests, q_heads, self.kv_heads, self.head_dim, n, longest)
         ws = self._ws.get(q_heads)
         if ws is None or ws.numel() < need:
-            if ws is not None:
-                self._grown.append(ws)  # a captured graph may hold its address
-            ws = self._ws[q_heads] = make_paged_workspace(self.requests, q_heads, self.kv_heads, self.head_dim, n,
-                                                          longest, self.device, stream)
+            if ws is not None:  # a captured graph may hold its address; doubled, so that all kept ones are no more than the new one
+                self._grown.append(ws)
+                need = max(need, 2 * ws.numel())
+            ws = self._ws[q_heads] = _new(torch.empty, max(16, need), torch.uint8, self.device, stream)
         return attend_paged(self.k_plans[layer], self.v_plans[layer], q, self.k_codes[layer], self.k_scales[layer],
                             self.v_codes[layer], self.v_scales[layer], self.block_table, self.kv_lens, step.q_starts,
                             max_q_len=longest, max_kv_len=max_kv_len, window=window, softmax_scale=softmax_scale,

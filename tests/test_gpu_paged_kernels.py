@@ -383,3 +383,26 @@ def test_each_kernel_weighs_a_tail_below_a_sink(kvq, path, q, sink, vsize, D, G,
         tol += tail * (2.0 ** -32 if path == "prompt" else 2.0 ** -37 * (1 + 2 / vsize) if vsize < 1 else 2.0 ** (-37 + np.log2(vsize) + 2))
         got = c.run(kvq, max_q_len=q).cpu().numpy().astype(np.float64)
         check_rel_l2(got.reshape(-1, D), ref.reshape(-1, D), tol=tol, label=f"gap {gap}")
+
+
+def test_cache_class_workspaces_stay_within_twice_the_largest(kvq):
+    """Steps that grow a little each time: the workspaces kept for captured graphs add up to no more
+    than the one in use."""
+    B, Hkv, Hq, D = 64, 1, 8, 256
+    params = kvgen.plan_params(D, seed=2, kind="k")
+    cache = kvq.PagedInt4KVCache(1, B, Hkv, D, 70, 16, 2, params, params)
+    kvq.set_attend_paged_path("few")                       # its workspace grows with the bounds
+    try:
+        for n in range(8, 200, 8):
+            step = cache.begin(i32([1] * B), B)
+            q = torch.ones((n, Hq, D), dtype=torch.float16, device="cuda")
+            cache.attend(0, q, step, max_q_len=n)
+            cache.kv_lens.zero_()
+            cache.free_head.zero_()
+        torch.cuda.synchronize()
+        need = kvq.paged_workspace_size(B, Hq, Hkv, D, n, n)
+    finally:
+        kvq.set_attend_paged_path("auto")
+    now = cache._ws[Hq].numel()
+    kept = sum(w.numel() for w in cache._grown)
+    assert need <= now <= 2 * need and kept <= now
