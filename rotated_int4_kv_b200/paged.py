@@ -15,11 +15,26 @@ from typing import NamedTuple
 
 import torch
 
-from . import _paged
 from ._lib import check, lib
 from .api import Plan
 
-_paged.set_check(check)
+
+class _Binding:
+    """Stands for the compiled binding until a call needs it (the dense calls never do)."""
+
+    def __getattr__(self, name):
+        global _paged
+        try:
+            from . import _paged as binding
+        except ImportError as e:
+            raise ImportError(f"the paged calls' compiled binding does not load ({e}): build it with "
+                              "`python rotated_int4_kv_b200/build.py` (g++, for the installed torch)") from e
+        binding.set_check(check)
+        _paged = binding
+        return getattr(binding, name)
+
+
+_paged = _Binding()
 PAGE_SIZES = (16, 32, 64, 128)
 ATTEND_PAGED_PATHS = {"auto": 0, "few": 1, "prompt": 2}
 
