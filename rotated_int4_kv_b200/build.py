@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -80,9 +81,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def _torch_version() -> str:
+    return importlib.metadata.version("torch")
+
+
 def _build_binding(force: bool) -> None:
+    """Rebuilt for a changed source, header or library, and for another torch or Python than its stamp names."""
     src = os.path.join(CSRC, BINDING)
-    if not force and not _stale(BINDING_LIB, [src, os.path.join(ROOT, "include", "kvq.h"), LIB]):
+    stamp, made_for = os.path.join(BUILD, "paged_binding.stamp"), f"torch {_torch_version()} python {sys.version}"
+    same = os.path.exists(stamp) and open(stamp).read() == made_for
+    if not force and same and not _stale(BINDING_LIB, [src, os.path.join(ROOT, "include", "kvq.h"), LIB]):
         return
     import torch
     t = os.path.dirname(torch.__file__)
@@ -97,6 +105,8 @@ def _build_binding(force: bool) -> None:
         f.write(r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING}:\n{r.stderr[-4000:]}")
+    with open(stamp, "w") as f:
+        f.write(made_for)
 
 
 def main(argv=None) -> int:
