@@ -85,9 +85,10 @@ typedef enum { KVQ_TRANSFORM_SRFT = 0, KVQ_TRANSFORM_SRHT = 1 } kvq_transform;
  *   signs_host  host int8[D], every entry +1 or -1 (the fixed random sign vector s).
  *   lambda_host host float[D], every entry finite and > 0 (per-channel lambda).
  * Allocates one device block on the current device, the plan's device: the
- * per-channel factors and sign masks derived from s and lambda, the tensor-core
- * encode's operand Lambda R as an fp16 hi/lo pair (2 D^2 halves) and the attention
- * kernels' 128-point transform (64 KB).
+ * per-channel factors and sign masks derived from s and lambda (4 KB) and the tensor-core
+ * codec's operands, Lambda R as an fp16 hi/lo pair (2 D^2 halves; D^2 for the SRHT) and
+ * Lambda^-1 R^T (D^2 halves). The attention kernels' transforms depend on D, transform and
+ * code width alone and are shared by the plans that live on a device (64 KB and 4 D^2 halves).
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA, DEVICE.
  */
 kvq_status kvq_plan_create(kvq_plan** out, int head_dim, int group, const int8_t* signs_host,

@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_codec.cu", "kvq_encode_tc.cu", "kvq_decode_tc.cu", "kvq_attend.cu",
-           "kvq_page_plan.cu", "kvq_attend_paged.cu", "kvq_attend_prompt.cu"]
+           "kvq_plan_basis.cu", "kvq_page_plan.cu", "kvq_attend_paged.cu", "kvq_attend_prompt.cu"]
 BINDING = "paged_binding.cpp"   # the Python extension module _paged (torch's C++ interface, linked to libkvq.so)
 BINDING_LIB = os.path.join(PKG, "_paged.so")
 HEADERS = ["kvq_internal.h", "kvq_ptx.cuh", "kvq_quant.cuh", "srft_fft.cuh"]

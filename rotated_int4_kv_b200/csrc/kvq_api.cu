@@ -39,31 +39,6 @@ EncodeTiledFn get_encode_fn() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Per-channel normalisation of the real basis: dg_c = 1/sqrt(D) (DC, Nyquist),
-// sqrt(2/D) (cos rows), -sqrt(2/D) (sin rows: the spectrum slot holds Im X_k and
-// the sin row equals -sqrt(2/D) Im X_k).
-// Row c of the orthonormal real basis in channel order, at sample n: DC, then
-// (cos_k, +sin_k) pairs, then Nyquist; angles from the exact residue k n mod D.
-double basis_value(int c, int n, int D) {
-  const double pi2 = 6.283185307179586476925286766559;
-  if (c == 0) return 1.0 / std::sqrt((double)D);
-  if (c == D - 1) return ((n & 1) ? -1.0 : 1.0) / std::sqrt((double)D);
-  const int k = (c + 1) / 2;
-  const double ang = pi2 * (double)((long)k * n % D) / (double)D;
-  return std::sqrt(2.0 / D) * ((c & 1) ? std::cos(ang) : std::sin(ang));
-}
-
-// Entry (i, j) of the Sylvester Hadamard matrix in natural order: (-1)^popcount(i & j).
-double hadamard_value(int i, int j) { return (__builtin_popcount((unsigned)(i & j)) & 1) ? -1.0 : 1.0; }
-
-uint16_t half_bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
-float half_value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-
-double basis_dg(int c, int D) {
-  if (c == 0 || c == D - 1) return 1.0 / std::sqrt((double)D);
-  return (c & 1) ? std::sqrt(2.0 / D) : -std::sqrt(2.0 / D);
-}
-
 }  // namespace
 
 void set_error(const std::string& msg) { t_last_error = msg; }
@@ -243,7 +218,11 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major != 10)
     return fail(KVQ_ERR_DEVICE, "plan_create: needs a compute capability 10.x (sm_100) device");
 
+  kvq::PlanBasis* basis_dev = nullptr;
+  const kvq_status st = kvq::acquire_basis(dev, D, transform, bits, &basis_dev);
+  if (st != KVQ_OK) return st;
   kvq_plan* p = new kvq_plan();
+  p->basis = basis_dev;
   p->D = D;
   p->G = G;
   p->device = dev;
@@ -287,32 +266,6 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
       wt[(size_t)(256 * h + 128 + rr) * D + n] = lo;
     }
   }
-  // attention operand (both head dims): the unnormalised 128-point real DFT in slot
-  // order, F128 (hi, lo): row 0 = 1, row 1 = (-1)^m, row 2k = cos(2 pi k m / 128),
-  // row 2k+1 = -sin(2 pi k m / 128); for the SRHT the 128-point Hadamard matrix (exact
-  // in fp16, lo = 0). D = 128 applies it directly, D = 256 to the even and odd samples;
-  // the plan's signs and per-channel factors are applied around it.
-  std::vector<uint16_t> rot;
-  {
-    const int M = 128;
-    rot.resize((size_t)2 * M * M);
-    const double pi2 = 6.283185307179586476925286766559;
-    for (int j = 0; j < M; ++j)
-      for (int m = 0; m < M; ++m) {
-        double v;
-        if (hadamard) v = kvq::hadamard_value(j, m);
-        else if (j == 0) v = 1.0;
-        else if (j == 1) v = (m & 1) ? -1.0 : 1.0;
-        else {
-          const double ang = pi2 * (double)((long)(j / 2) * m % M) / (double)M;
-          v = (j & 1) ? -std::sin(ang) : std::cos(ang);
-        }
-        const uint16_t hi = kvq::half_bits((float)v);
-        const uint16_t lo = kvq::half_bits((float)(v - (double)kvq::half_value(hi)));
-        rot[(size_t)j * M + m] = hi;
-        rot[(size_t)(M + j) * M + m] = lo;
-      }
-  }
   // tensor-core decode operand: W_dec = diag(s) Q^T Lambda^-1 (row n = output sample n,
   // column = channel), one fp16 rounding per entry; the columns of each 16-byte unit in
   // the order the kernel's dequantiser writes the channels (decode_unit_channel)
@@ -323,81 +276,32 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
       const double q = basis[(size_t)c * D + n];
       wdec[(size_t)n * D + k] = kvq::half_bits((float)((double)signs[n] * q / (double)lambda[c]));
     }
-  // paged-attention operands: the query rotation Lambda^-1 Q diag(s) (row = channel) and the
-  // output un-rotation diag(s) Q^T Lambda^-1 (row = sample), fp16 times a power of two that
-  // puts the largest entry in [1, 2) (no fp16 range limit applies to lambda). Twice: as
-  // row-major matrices with the channels in the order in which the prompt kernel converts a
-  // word of codes (int4: 0 4 1 5 2 6 3 7 of each eight, int8: 0 2 1 3 4 6 5 7), and in
-  // natural order as A fragments: lane (g, c) of K step ks holds (row g | g + 8, columns
-  // 16 ks + 2c, + 1 | + 8, + 9)
-  std::vector<uint16_t> wpg((size_t)4 * D * D);
-  {
-    std::vector<double>& m = basis;
-    double top = 0.0;
-    for (int c = 0; c < D; ++c)
-      for (int n = 0; n < D; ++n) {
-        double& v = m[(size_t)c * D + n];
-        v = (double)signs[n] * v / (double)lambda[c];
-        top = std::max(top, std::fabs(v));
-      }
-    int e = 0;
-    std::frexp(top, &e);  // top = f 2^e with f in [0.5, 1)
-    p->wq_scale = p->wo_scale = (float)std::ldexp(1.0, e - 1);
-    const double up = std::ldexp(1.0, 1 - e);
-    std::vector<uint16_t> nat((size_t)D * D);  // row = channel, natural order
-    for (size_t x = 0; x < nat.size(); ++x) nat[x] = kvq::half_bits((float)(m[x] * up));
-    for (int which = 0; which < 2; ++which) {
-      uint16_t* row = wpg.data() + (size_t)which * D * D;
-      uint16_t* frag = wpg.data() + (size_t)(2 + which) * D * D;
-      auto entry = [&](int i, int k) { return which ? nat[(size_t)k * D + i] : nat[(size_t)i * D + k]; };
-      for (int i = 0; i < D; ++i)
-        for (int k = 0; k < D; ++k)
-          row[(size_t)i * D + k] = which ? entry(i, kvq::word_channel(k, bits)) : entry(kvq::word_channel(i, bits), k);
-      size_t o = 0;
-      for (int mt = 0; mt < D / 16; ++mt)
-        for (int ks = 0; ks < D / 16; ++ks)
-          for (int lane = 0; lane < 32; ++lane)
-            for (int r = 0; r < 4; ++r)
-              for (int x = 0; x < 2; ++x) {
-                const int i = 16 * mt + (lane >> 2) + 8 * (r & 1), k = 16 * ks + 2 * (lane & 3) + 8 * (r >> 1) + x;
-                frag[o++] = entry(i, k);
-              }
-    }
-  }
   constexpr size_t kWtOff = 4096;  // after the two CodecConsts copies, 16-byte aligned for TMA
   static_assert(2 * sizeof(kvq::CodecConsts) <= kWtOff, "plan block layout");
-  const size_t rot_off = kWtOff + wt.size() * 2;
-  const size_t wdec_off = rot_off + rot.size() * 2;
-  const size_t wpg_off = wdec_off + wdec.size() * 2;
-  const size_t bytes = wpg_off + wpg.size() * 2;
+  const size_t wdec_off = kWtOff + wt.size() * 2;
+  const size_t bytes = wdec_off + wdec.size() * 2;
   void* blk = nullptr;
   if (cudaMalloc(&blk, bytes) != cudaSuccess) {
+    kvq::release_basis(p->basis);
     delete p;
     return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
   }
   if (cudaMemcpy(blk, &p->enc, sizeof(kvq::CodecConsts), cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMemcpy((char*)blk + sizeof(kvq::CodecConsts), &p->dec, sizeof(kvq::CodecConsts), cudaMemcpyHostToDevice) !=
           cudaSuccess ||
-      (!wt.empty() &&
-       cudaMemcpy((char*)blk + kWtOff, wt.data(), wt.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) ||
-      (!rot.empty() &&
-       cudaMemcpy((char*)blk + rot_off, rot.data(), rot.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) ||
-      cudaMemcpy((char*)blk + wdec_off, wdec.data(), wdec.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemcpy((char*)blk + wpg_off, wpg.data(), wpg.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
+      cudaMemcpy((char*)blk + kWtOff, wt.data(), wt.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess ||
+      cudaMemcpy((char*)blk + wdec_off, wdec.data(), wdec.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
     cudaFree(blk);
+    kvq::release_basis(p->basis);
     delete p;
     return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
   }
   p->dblock = blk;
   p->enc_dev = reinterpret_cast<const kvq::CodecConsts*>(blk);
   p->dec_dev = reinterpret_cast<const kvq::CodecConsts*>((char*)blk + sizeof(kvq::CodecConsts));
-  p->wt_dev = wt.empty() ? nullptr : reinterpret_cast<const uint16_t*>((char*)blk + kWtOff);
-  p->rot_dev = reinterpret_cast<const uint16_t*>((char*)blk + rot_off);
+  p->wt_dev = reinterpret_cast<const uint16_t*>((char*)blk + kWtOff);
+  p->rot_dev = p->basis->rot_dev;
   p->wdec_dev = reinterpret_cast<const uint16_t*>((char*)blk + wdec_off);
-  p->wq_dev = reinterpret_cast<const uint16_t*>((char*)blk + wpg_off);
-  p->wo_dev = p->wq_dev + (size_t)D * D;
-  p->wqf_dev = reinterpret_cast<const uint4*>(p->wo_dev + (size_t)D * D);
-  p->wof_dev = reinterpret_cast<const uint4*>(p->wo_dev + (size_t)2 * D * D);
   *out = p;
   return KVQ_OK;
 }
@@ -409,6 +313,7 @@ kvq_status kvq_plan_destroy(kvq_plan* p) {
     cudaGetDevice(&cur);
     if (cur != p->device) cudaSetDevice(p->device);
     cudaFree(p->dblock);
+    kvq::release_basis(p->basis);
     if (cur != p->device && cur >= 0) cudaSetDevice(cur);
   }
   delete p;

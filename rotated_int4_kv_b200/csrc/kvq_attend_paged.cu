@@ -102,15 +102,19 @@ struct PagedParams {
   const int32_t* table;
   const int32_t* kv_lens;
   const int32_t* q_starts;
-  const uint4* wq;
+  const uint4* wq;         // the rotation without signs and factors, as fragments
   const uint4* wo;
+  const float* qchan;      // what its channels are multiplied by, K's and V's
+  const float* ochan;
+  const uint32_t* qsgn;    // sign masks of sample pairs, K's and V's
+  const uint4* osgn;
   uint16_t* out;
   uint8_t* qprep;          // [unit] prepared queries
   float* part;             // [2 CTA + (0, 1)] partials of units that are cut
   float* part_unit;        // [unit] partials of whole units
   int2* desc;              // [unit] the first CTA's slot and the number of partials (0: whole)
   long long q_ts, q_hs, table_stride;
-  float qfac, ofac;        // sigma log2(e) times the query matrix' scale; the output matrix' scale
+  float qfac;              // sigma log2(e)
   int B, n_q, Hq, Hkv, Gq, rt_max, max_q, max_kv, num_pages, page_shift, window, min_tiles;
 };
 
@@ -156,12 +160,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-// The power of two 2^-e that brings a row's largest magnitude into [2^9, 2^10); mx is the
+// The power of two 2^-e that brings a row's largest magnitude into [2^14, 2^15); mx is the
 // largest of this lane's elements of row g, the row's lanes are c = 0 .. 3. Returns e.
 __device__ __forceinline__ int row_exponent(float mx) {
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 9;
+  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 14;
   return mx > 0.0f ? min(max(e, -100), 100) : 0;
 }
 
@@ -273,8 +277,8 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- first kernel: the queries
-// Block u: the 8 query rows of unit u, rotated (a product with the plan's matrix, laid out as
-// fragments when the plan was made) and laid out as the score products' B fragments
+// Block u: the 8 query rows of unit u, rotated (signs, a product with the rotation's fragments,
+// factors) and laid out as the score products' B fragments
 // (column = row of the tile), normalised by 2^-e per row, with per group the start of its sum
 // (minus what the codes' offset adds to it) and per row the factor back to base-2 scores.
 // A block reads the matrix (32 or 128 KB) through L2 before it waits for the kernel in front,
@@ -292,6 +296,18 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
   for (int t = 0; t < TW; ++t)
 #pragma unroll
     for (int ks = 0; ks < MT; ++ks) wf[t][ks] = __ldg(p.wq + ((warp + NWARP * t) * MT + ks) * 32 + lane);
+  float fac[TW][2];            // of channels g and g + 8 of the warp's tiles
+  uint32_t sgn[MT][2];
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    fac[t][0] = __ldg(p.qchan + 16 * (warp + NWARP * t) + g);
+    fac[t][1] = __ldg(p.qchan + 16 * (warp + NWARP * t) + g + 8);
+  }
+#pragma unroll
+  for (int ks = 0; ks < MT; ++ks) {
+    sgn[ks][0] = __ldg(p.qsgn + 8 * ks + c);
+    sgn[ks][1] = __ldg(p.qsgn + 8 * ks + 4 + c);
+  }
   grid_dep_wait();
   grid_dep_launch();  // after the wait: what the main kernel reads before its own wait is complete
   const Request r = request_of<C::kTile>(p, b);
@@ -305,7 +321,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
     for (int ks = 0; ks < MT; ++ks) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) : 0u;
+        bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) ^ sgn[ks][e] : 0u;
     }
   }
 #pragma unroll
@@ -315,10 +331,10 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
     for (int ks = 0; ks < MT; ++ks)
       mma_16816((ks & 1) ? a1 : a0, wf[t][ks].x, wf[t][ks].y, wf[t][ks].z, wf[t][ks].w, bq[ks][0], bq[ks][1]);
     float* o0 = om + (2 * c) * C::kOmStride + 16 * (warp + NWARP * t) + g;
-    o0[0] = a0[0] + a1[0];
-    o0[C::kOmStride] = a0[1] + a1[1];
-    o0[8] = a0[2] + a1[2];
-    o0[C::kOmStride + 8] = a0[3] + a1[3];
+    o0[0] = (a0[0] + a1[0]) * fac[t][0];
+    o0[C::kOmStride] = (a0[1] + a1[1]) * fac[t][0];
+    o0[8] = (a0[2] + a1[2]) * fac[t][1];
+    o0[C::kOmStride + 8] = (a0[3] + a1[3]) * fac[t][1];
   }
   __syncthreads();
   uint4* qf = reinterpret_cast<uint4*>(p.qprep + (size_t)unit * C::kPrep);
@@ -1006,6 +1022,11 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   for (int t = 0; t < TW; ++t)
 #pragma unroll
     for (int ks = 0; ks < MT; ++ks) wf[t][ks] = __ldg(p.wo + ((warp + NWARP * t) * MT + ks) * 32 + lane);
+  constexpr int NX = kRows * D / 4 / NT, U = 8;  // float4 values of a thread, partials in flight
+  float4 fac[NX];                                // of the channels of each
+#pragma unroll
+  for (int x = 0; x < NX; ++x) fac[x] = __ldg(reinterpret_cast<const float4*>(p.ochan) + (tid + x * NT) % (D / 4));
+  const uint4 sgn = __ldg(p.osgn + tid % (D / 8));  // of this thread's 8 samples of every row
   grid_dep_launch();
   grid_dep_wait();
   // the loads of a step together: request and description; then the first partials' m, l and o
@@ -1018,7 +1039,6 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   auto part = [&](int k) {
     return d.y == 0 ? p.part_unit + (size_t)unit * PART : p.part + (size_t)(k == 0 ? d.x : (d.x & ~1) + 2 * k) * PART;
   };
-  constexpr int NX = kRows * D / 4 / NT, U = 8;  // float4 values of a thread, partials in flight
   float4 v[U][NX];
   auto load_o = [&](int k0) {
 #pragma unroll
@@ -1072,6 +1092,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
       const int y = tid + x * NT, row = y / (D / 4);
+      acc[x] = make_float4(acc[x].x * fac[x].x, acc[x].y * fac[x].y, acc[x].z * fac[x].z, acc[x].w * fac[x].w);
       // rows behind the tile's last were not written
       *reinterpret_cast<float4*>(om + row * ST + 4 * (y - row * (D / 4))) = row < nrows ? acc[x] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -1110,7 +1131,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   }
   float fo[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) fo[e] = p.ofac * pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+  for (int e = 0; e < 2; ++e) fo[e] = pow2f(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
 #pragma unroll
   for (int t = 0; t < TW; ++t) {
     __half* x0 = xb + (2 * c) * (D + 8) + 16 * (warp + NWARP * t) + g;
@@ -1123,8 +1144,9 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   for (int x = tid; x < nrows * (D / 8); x += NT) {
     const int row = x / (D / 8), k = x - row * (D / 8);
     const int y = rt * kRows + row, tok = y / p.Gq, head = h * p.Gq + (y - tok * p.Gq);
+    const uint4 v = *reinterpret_cast<const uint4*>(xb + row * (D + 8) + 8 * k);
     *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
-        *reinterpret_cast<const uint4*>(xb + row * (D + 8) + 8 * k);
+        make_uint4(v.x ^ sgn.x, v.y ^ sgn.y, v.z ^ sgn.z, v.w ^ sgn.w);
   }
 }
 
@@ -1157,15 +1179,18 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   p.table = a.table;
   p.kv_lens = a.kv_lens;
   p.q_starts = a.q_starts;
-  p.wq = a.pk->wqf_dev;
-  p.wo = a.pv->wof_dev;
+  p.wq = a.pk->basis->wqf_dev;
+  p.wo = a.pv->basis->wof_dev;
+  p.qchan = a.pk->dec_dev->chan;
+  p.ochan = a.pv->dec_dev->chan;
+  p.qsgn = a.pk->dec_dev->sgn;
+  p.osgn = reinterpret_cast<const uint4*>(a.pv->dec_dev->sgn);
   p.out = a.out;
   p.q_ts = a.q_token_stride;
   p.q_hs = a.q_head_stride;
   p.table_stride = a.table_stride;
   const float sigma = a.sigma > 0.0f ? a.sigma : 1.0f / sqrtf((float)D);
-  p.qfac = sigma * 1.4426950408889634f * a.pk->wq_scale;
-  p.ofac = a.pv->wo_scale;
+  p.qfac = sigma * 1.4426950408889634f;
   p.B = a.B;
   p.n_q = a.n_q;
   p.Hq = a.Hq;

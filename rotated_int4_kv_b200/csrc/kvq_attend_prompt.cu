@@ -85,7 +85,8 @@ struct PrCfg {
   static constexpr int kFlags = kFlagRing * 5 * 4;
   static constexpr int kBars = 256;
   static_assert(kScan <= kTile, "the scan uses the K tiles");
-  static constexpr int kSmem = kQ + 4 * kTile + kRing + kScales + kEnt + kFlags + kBars + 1024;
+  static constexpr int kConst = 2 * (D * 4 + D * 2);  // the plans' factors and sign masks
+  static constexpr int kSmem = kQ + 4 * kTile + kRing + kScales + kEnt + kConst + kFlags + kBars + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // TMEM columns
   static constexpr int kO = 0;                  // O of block q at q * D
@@ -103,12 +104,16 @@ struct PromptParams {
   const int32_t* q_starts;
   const uint16_t* wq;      // [channel][sample], rows in word_channel order
   const uint16_t* wo;      // [sample][channel], columns in word_channel order
-  const uint4* wof;        // the same as fragments, natural order
+  const uint4* wof;        // the same as fragments, natural order (all three without signs and factors)
+  const float* qchan;      // what their channels are multiplied by, K's and V's
+  const float* ochan;
+  const uint4* qsgn;       // sign masks of 8 samples, K's and V's
+  const uint4* osgn;
   uint16_t* out;
   float* part;
   int4* desc;              // [CTA]: the cut unit that starts in it (request, row block, head, partials | slot << 16), 0: none
   long long q_ts, q_hs, table_stride;
-  float qfac, ofac;
+  float qfac;
   int B, n_q, Hq, Hkv, Gq, max_q, max_kv, num_pages, page_shift, window, min_tiles;
 };
 
@@ -121,9 +126,23 @@ __device__ __forceinline__ uint32_t mask_xor(uint32_t a, uint32_t mask, uint32_t
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(mask), "r"(x));
   return d;
 }
-// The exponent e with mx 2^-e in [2^9, 2^10), 0 for mx = 0.
+// Eight fp16 values with the signs flipped that the mask names.
+__device__ __forceinline__ uint4 flip(uint4 v, uint4 m) { return make_uint4(v.x ^ m.x, v.y ^ m.y, v.z ^ m.z, v.w ^ m.w); }
+// 32 channels in word_channel order times their factors (shared memory, natural order).
+template <int BITS>
+__device__ __forceinline__ void times_channels(float (&v)[32], const float* f) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(f + 4 * k);
+    v[word_place(4 * k, BITS)] *= x.x;
+    v[word_place(4 * k + 1, BITS)] *= x.y;
+    v[word_place(4 * k + 2, BITS)] *= x.z;
+    v[word_place(4 * k + 3, BITS)] *= x.w;
+  }
+}
+// The exponent e with mx 2^-e in [2^14, 2^15), 0 for mx = 0.
 __device__ __forceinline__ int row_exp(float mx) {
-  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 9;
+  const int e = (int)((__float_as_uint(mx) >> 23) & 255u) - 127 - 14;
   return mx > 0.0f ? min(max(e, -100), 100) : 0;
 }
 
@@ -285,7 +304,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
   uint32_t* sScale = reinterpret_cast<uint32_t*>(sRing + C::kRing);
   int32_t* sEnt = reinterpret_cast<int32_t*>(sRing + C::kRing + C::kScales);
   long long* scan = reinterpret_cast<long long*>(sK);  // before the first tile
-  uint32_t* flags = reinterpret_cast<uint32_t*>(sRing + C::kRing + C::kScales + C::kEnt);  // [ring][5]
+  float* sQchan = reinterpret_cast<float*>(sRing + C::kRing + C::kScales + C::kEnt);
+  float* sOchan = sQchan + D;
+  uint4* sQsgn = reinterpret_cast<uint4*>(sOchan + D);
+  uint4* sOsgn = sQsgn + D / 8;
+  uint32_t* flags = reinterpret_cast<uint32_t*>(sOsgn + D / 8);  // [ring][5]
   uint64_t* kfull = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(flags) + C::kFlags);
   uint64_t* kempty = kfull + 2;
   uint64_t* vfull = kempty + 2;
@@ -317,6 +340,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
     fence_mbarrier_init();
   }
   for (int x = tid; x < kFlagRing * 5; x += kPrThreads) flags[x] = 0;
+  // factors and signs, used at every unit (read from global memory there, with little L1 left beside
+  // this shared memory: chunks of 2048 tokens 1034 us, so 1027)
+  for (int x = tid; x < D; x += kPrThreads) {
+    sQchan[x] = __ldg(p.qchan + x);
+    sOchan[x] = __ldg(p.ochan + x);
+    if (x < D / 8) {
+      sQsgn[x] = __ldg(p.qsgn + x);
+      sOsgn[x] = __ldg(p.osgn + x);
+    }
+  }
   grid_dep_launch();
   if (warp == kPrWarps - 1) {
     tmem_alloc(tmem_slot, 512);
@@ -373,7 +406,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(w.r.qs + tok) * p.q_ts + (long long)head * p.q_hs);
 #pragma unroll 8
-        for (int u = 0; u < D / 8; ++u) *q_unit(u) = valid ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < D / 8; ++u) *q_unit(u) = valid ? flip(__ldg(src + u), sQsgn[u]) : make_uint4(0, 0, 0, 0);
       }
       announce(&aready[qb]);
       // ---- q~, normalised by a power of two per row
@@ -388,6 +421,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           tmem_ld32(trot + c, v);
           tmem_ld_wait();
           tmem_regs_fence(v);
+          times_channels<BITS>(v, sQchan + c);
 #pragma unroll
           for (int k = 0; k < 32; ++k) mx = fmaxf(mx, fabsf(v[k]));
         }
@@ -400,6 +434,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           tmem_ld32(trot + c, v);
           tmem_ld_wait();
           tmem_regs_fence(v);
+          times_channels<BITS>(v, sQchan + c);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *q_unit(c / 8 + k) = make_uint4(pack_half2(v[8 * k] * f, v[8 * k + 1] * f), pack_half2(v[8 * k + 2] * f, v[8 * k + 3] * f),
@@ -544,6 +579,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           tmem_ld32(to + c, v);
           tmem_ld_wait();
           tmem_regs_fence(v);
+          times_channels<BITS>(v, sOchan + c);
 #pragma unroll
           for (int k = 0; k < 32; ++k) mx = fmaxf(mx, fabsf(v[k]));
         }
@@ -555,6 +591,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           tmem_ld32(to + c, v);
           tmem_ld_wait();
           tmem_regs_fence(v);
+          times_channels<BITS>(v, sOchan + c);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             *q_unit(c / 8 + k) = make_uint4(pack_half2(v[8 * k] * f, v[8 * k + 1] * f), pack_half2(v[8 * k + 2] * f, v[8 * k + 3] * f),
@@ -562,7 +599,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
         }
         announce(&aready[qb]);
         wait(&sfull[s0], ns[s0]++ & 1);
-        const float of = p.ofac * ppow2(ex) * ppow2(ve);
+        const float of = ppow2(ex) * ppow2(ve);
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)(w.r.qs + tok) * p.Hq + head) * D);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -573,8 +610,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
           if (valid && ok) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              dst[c / 8 + k] = make_uint4(pack_half2(v[8 * k] * of, v[8 * k + 1] * of), pack_half2(v[8 * k + 2] * of, v[8 * k + 3] * of),
-                                          pack_half2(v[8 * k + 4] * of, v[8 * k + 5] * of), pack_half2(v[8 * k + 6] * of, v[8 * k + 7] * of));
+              dst[c / 8 + k] = flip(make_uint4(pack_half2(v[8 * k] * of, v[8 * k + 1] * of), pack_half2(v[8 * k + 2] * of, v[8 * k + 3] * of),
+                                               pack_half2(v[8 * k + 4] * of, v[8 * k + 5] * of), pack_half2(v[8 * k + 6] * of, v[8 * k + 7] * of)),
+                                    sOsgn[c / 8 + k]);
           }
         }
       } else {
@@ -949,6 +987,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
   __shared__ __align__(16) __half ob[8 * (D + 8)];
   __shared__ float ml[2][8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint4 sgn = __ldg(p.osgn + tid % (D / 8));  // of this thread's 8 samples of every row
   grid_dep_launch();
   grid_dep_wait();
   const int4 u = __ldcg(p.desc + blockIdx.x);
@@ -1000,10 +1039,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
       }
     }
     float* o = om + row * ST;
-    o[word_channel(4 * k4, BITS)] = acc.x;
-    o[word_channel(4 * k4 + 1, BITS)] = acc.y;
-    o[word_channel(4 * k4 + 2, BITS)] = acc.z;
-    o[word_channel(4 * k4 + 3, BITS)] = acc.w;
+    const float a[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = word_channel(4 * k4 + k, BITS);
+      o[ch] = a[k] * __ldg(p.ochan + ch);
+    }
   }
   __syncthreads();
   const int g = lane >> 2, c = lane & 3;
@@ -1041,7 +1082,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
   }
   float fo[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) fo[e] = p.ofac * ppow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
+  for (int e = 0; e < 2; ++e) fo[e] = ppow2(__shfl_sync(0xffffffffu, ex, 4 * (2 * c + e)));
 #pragma unroll
   for (int t = 0; t < MT / kJoinWarps; ++t) {
     __half* x0 = ob + (2 * c) * (D + 8) + 16 * (warp + kJoinWarps * t) + g;
@@ -1055,7 +1096,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
     const int row = x / (D / 8), k = x - row * (D / 8);
     const int y = u.y * R + r0 + row, tok = y / p.Gq, head = u.z * p.Gq + (y - tok * p.Gq);
     *(reinterpret_cast<uint4*>(p.out + ((size_t)(r.qs + tok) * p.Hq + head) * D) + k) =
-        *reinterpret_cast<const uint4*>(ob + row * (D + 8) + 8 * k);
+        flip(*reinterpret_cast<const uint4*>(ob + row * (D + 8) + 8 * k), sgn);
   }
 }
 
@@ -1072,9 +1113,13 @@ kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
   p.table = a.table ? a.table : a.kv_lens;  // no pages: an address for copies of zero bytes
   p.kv_lens = a.kv_lens;
   p.q_starts = a.q_starts;
-  p.wq = a.pk->wq_dev;
-  p.wo = a.pv->wo_dev;
-  p.wof = a.pv->wof_dev;
+  p.wq = a.pk->basis->wq_dev;
+  p.wo = a.pv->basis->wo_dev;
+  p.wof = a.pv->basis->wof_dev;
+  p.qchan = a.pk->dec_dev->chan;
+  p.ochan = a.pv->dec_dev->chan;
+  p.qsgn = reinterpret_cast<const uint4*>(a.pk->dec_dev->sgn);
+  p.osgn = reinterpret_cast<const uint4*>(a.pv->dec_dev->sgn);
   p.out = a.out;
   p.part = reinterpret_cast<float*>(part);
   p.desc = reinterpret_cast<int4*>(p.part + (size_t)2 * kPrMaxCtas * kPrPart);
@@ -1082,8 +1127,7 @@ kvq_status run_prompt(const PagedAttendHost& a, void* part, cudaStream_t strm) {
   p.q_hs = a.q_head_stride;
   p.table_stride = a.table_stride;
   const float sigma = a.sigma > 0.0f ? a.sigma : 1.0f / sqrtf((float)D);
-  p.qfac = sigma * 1.4426950408889634f * a.pk->wq_scale;
-  p.ofac = a.pv->wo_scale;
+  p.qfac = sigma * 1.4426950408889634f;
   p.B = a.B;
   p.n_q = a.n_q;
   p.Hq = a.Hq;

@@ -24,6 +24,24 @@ struct CodecConsts {
   uint32_t sgn[kMaxD / 2]; // XOR mask per fp16 pair of the original domain (0x8000 per negative s)
 };
 
+// What plans of one device, head_dim, transform and code width share (kvq_plan_basis.cu), held
+// while one of them lives: the rotation without signs and factors.
+struct PlanBasis {
+  int device, D, xform, bits;
+  int users = 0;
+  void* dblock = nullptr;
+  const uint16_t* rot_dev = nullptr;  // F128 (see kvq_plan)
+  // Paged attention, with E = Q, its rows divided by basis_dg (fp16): E (query rotation) and E^T
+  // (output un-rotation), each as row-major [D][D] with the channels in the order of
+  // word_channel, and in natural order as mma.m16n8k16 A fragments (16 bytes per (16-row
+  // tile, K step, lane)). The kernels multiply channel c by basis_dg / lambda_c (dec.chan) and
+  // flip samples by the signs.
+  const uint16_t* wq_dev = nullptr;
+  const uint16_t* wo_dev = nullptr;
+  const uint4* wqf_dev = nullptr;
+  const uint4* wof_dev = nullptr;
+};
+
 }  // namespace kvq
 
 struct kvq_plan {
@@ -42,24 +60,14 @@ struct kvq_plan {
   // Tensor-core encode operand in the same block: W = Lambda F_r diag(s) as fp16
   // hi + lo, per 128-channel half 128 hi rows then 128 lo rows, D columns.
   const uint16_t* wt_dev = nullptr;
-  // Attention operand in the same block: F128, the unnormalised 128-point real DFT in
-  // slot order, fp16 hi rows [128] then lo rows [128] (plan-independent; the attention
-  // kernels apply the plans' signs and per-channel factors around it).
+  // What it shares with other plans, and its F128: the unnormalised 128-point real DFT in
+  // slot order, fp16 hi rows [128] then lo rows [128] (the attention kernels apply the
+  // plans' signs and per-channel factors around it).
+  kvq::PlanBasis* basis = nullptr;
   const uint16_t* rot_dev = nullptr;
   // Tensor-core decode operand in the same block: W_dec = diag(s) Q^T Lambda^-1 as fp16,
   // D rows (output samples) x D columns (channels, in the dequantiser's pair order).
   const uint16_t* wdec_dev = nullptr;
-  // Paged-attention operands in the same block, fp16 times a power of two (one rounding per
-  // entry, the largest entry in [1, 2)): Lambda^-1 Q diag(s) (query rotation) and
-  // diag(s) Q^T Lambda^-1 (output un-rotation), each as row-major [D][D] with the channels in
-  // the order of word_channel, and in natural order as mma.m16n8k16 A fragments (16 bytes per
-  // (16-row tile, K step, lane)).
-  const uint16_t* wq_dev = nullptr;
-  const uint16_t* wo_dev = nullptr;
-  const uint4* wqf_dev = nullptr;
-  const uint4* wof_dev = nullptr;
-  float wq_scale = 1.0f;   // what the stored matrices are multiplied by to give the true ones
-  float wo_scale = 1.0f;
 };
 
 namespace kvq {
@@ -98,12 +106,26 @@ kvq_status encode_tiled_new(CUtensorMap* map, CUtensorMapDataType dt, int rank, 
 
 int num_sms(int device);
 
+// the shared part of a plan on the current device (kvq_plan_basis.cu)
+kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out);
+void release_basis(PlanBasis* b);
+double basis_value(int c, int n, int D);   // the orthonormal real DFT, row = channel
+double basis_dg(int c, int D);             // its rows' normalisation: 1/sqrt(D), sqrt(2/D) (cos), -sqrt(2/D) (sin)
+double hadamard_value(int i, int j);
+uint16_t half_bits(float f);
+float half_value(uint16_t b);
+
 kvq_status check_plan_device(const kvq_plan* p);
 
 // The channel at place p of a row when every 32-bit word of its codes is converted to fp16
 // pairs by masks: int4 pairs (0, 4) (1, 5) (2, 6) (3, 7), int8 pairs (0, 2) (1, 3).
 constexpr int word_channel(int p, int bits) {
   return bits == 4 ? (p & ~7) + ((p & 7) >> 1) + 4 * (p & 1) : (p & ~3) + ((p & 3) >> 1) + 2 * (p & 1);
+}
+
+// The place of channel c: word_channel(word_place(c)) = c.
+constexpr int word_place(int c, int bits) {
+  return bits == 4 ? (c & ~7) + 2 * (c & 3) + ((c >> 2) & 1) : (c & ~3) + 2 * (c & 1) + ((c >> 1) & 1);
 }
 
 // Lets a kernel use `bytes` of dynamic shared memory on `device` (an attribute of the

@@ -1,0 +1,140 @@
+// kvq_plan_basis.cu -- what plans of the same head_dim, transform and code width share: the
+// rotation without signs and factors, as the attention kernels' operands. Signs and factors
+// are a plan's own few KB, which the kernels apply around these (an exact change of sign, one
+// fp32 product per element), so a plan holds no matrix of its own for them.
+#include <cmath>
+#include <map>
+#include <memory>
+#include <mutex>
+#include <tuple>
+#include <vector>
+
+#include "kvq_internal.h"
+
+namespace kvq {
+
+// Row c of the orthonormal real basis in channel order, at sample n: DC, then
+// (cos_k, +sin_k) pairs, then Nyquist; angles from the exact residue k n mod D.
+double basis_value(int c, int n, int D) {
+  const double pi2 = 6.283185307179586476925286766559;
+  if (c == 0) return 1.0 / std::sqrt((double)D);
+  if (c == D - 1) return ((n & 1) ? -1.0 : 1.0) / std::sqrt((double)D);
+  const int k = (c + 1) / 2;
+  const double ang = pi2 * (double)((long)k * n % D) / (double)D;
+  return std::sqrt(2.0 / D) * ((c & 1) ? std::cos(ang) : std::sin(ang));
+}
+
+// Entry (i, j) of the Sylvester Hadamard matrix in natural order: (-1)^popcount(i & j).
+double hadamard_value(int i, int j) { return (__builtin_popcount((unsigned)(i & j)) & 1) ? -1.0 : 1.0; }
+
+double basis_dg(int c, int D) {
+  if (c == 0 || c == D - 1) return 1.0 / std::sqrt((double)D);
+  return (c & 1) ? std::sqrt(2.0 / D) : -std::sqrt(2.0 / D);
+}
+
+uint16_t half_bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
+float half_value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+
+namespace {
+
+constexpr int kF = 128;  // points of the dense attention's transform
+
+// A basis' device block as the host makes it: F128 hi and lo, then four D x D matrices.
+size_t rot_halves() { return (size_t)2 * kF * kF; }
+size_t block_halves(int D) { return rot_halves() + (size_t)4 * D * D; }
+
+std::vector<uint16_t> make_block(int D, bool hadamard, int bits) {
+  std::vector<uint16_t> blk(block_halves(D));
+  // dense attention (both head dims): the unnormalised 128-point real DFT in slot order, F128
+  // (hi, lo): row 0 = 1, row 1 = (-1)^m, row 2k = cos(2 pi k m / 128), row 2k+1 =
+  // -sin(2 pi k m / 128); for the SRHT the 128-point Hadamard matrix (exact in fp16, lo = 0).
+  // D = 128 applies it directly, D = 256 to the even and odd samples.
+  const double pi2 = 6.283185307179586476925286766559;
+  for (int j = 0; j < kF; ++j)
+    for (int m = 0; m < kF; ++m) {
+      double v;
+      if (hadamard) v = hadamard_value(j, m);
+      else if (j == 0) v = 1.0;
+      else if (j == 1) v = (m & 1) ? -1.0 : 1.0;
+      else {
+        const double ang = pi2 * (double)((long)(j / 2) * m % kF) / (double)kF;
+        v = (j & 1) ? -std::sin(ang) : std::cos(ang);
+      }
+      const uint16_t hi = half_bits((float)v);
+      blk[(size_t)j * kF + m] = hi;
+      blk[(size_t)(kF + j) * kF + m] = half_bits((float)(v - (double)half_value(hi)));
+    }
+  // paged attention: the basis with rows divided by basis_dg (entries cos, -sin, +-1: one fp16
+  // rounding each, none for the SRHT), as query rotation (row = channel) and output
+  // un-rotation (row = sample). Twice: as row-major matrices with the channels in the order in
+  // which the prompt kernel converts a word of codes (word_channel), and in natural order as A
+  // fragments: lane (g, c) of K step ks holds (row g | g + 8, columns 16 ks + 2c, + 1 | + 8, + 9)
+  std::vector<uint16_t> nat((size_t)D * D);  // row = channel, natural order
+  for (int c = 0; c < D; ++c)
+    for (int n = 0; n < D; ++n)
+      nat[(size_t)c * D + n] =
+          half_bits((float)(hadamard ? hadamard_value(c, n) : basis_value(c, n, D) / basis_dg(c, D)));
+  for (int which = 0; which < 2; ++which) {
+    uint16_t* row = blk.data() + rot_halves() + (size_t)which * D * D;
+    uint16_t* frag = row + (size_t)2 * D * D;
+    auto entry = [&](int i, int k) { return which ? nat[(size_t)k * D + i] : nat[(size_t)i * D + k]; };
+    for (int i = 0; i < D; ++i)
+      for (int k = 0; k < D; ++k)
+        row[(size_t)i * D + k] = which ? entry(i, word_channel(k, bits)) : entry(word_channel(i, bits), k);
+    size_t o = 0;
+    for (int mt = 0; mt < D / 16; ++mt)
+      for (int ks = 0; ks < D / 16; ++ks)
+        for (int lane = 0; lane < 32; ++lane)
+          for (int r = 0; r < 4; ++r)
+            for (int x = 0; x < 2; ++x) {
+              const int i = 16 * mt + (lane >> 2) + 8 * (r & 1), k = 16 * ks + 2 * (lane & 3) + 8 * (r >> 1) + x;
+              frag[o++] = entry(i, k);
+            }
+  }
+  return blk;
+}
+
+std::mutex g_mu;
+// the host's tables, kept: constants of mathematics
+std::map<std::tuple<int, int, int>, std::vector<uint16_t>> g_host;
+// the device's, as long as a plan uses them
+std::map<std::tuple<int, int, int, int>, std::unique_ptr<PlanBasis>> g_bases;
+
+}  // namespace
+
+kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto& slot = g_bases[{device, D, xform, bits}];
+  if (!slot) {
+    auto& blk = g_host[{D, xform, bits}];
+    if (blk.empty()) blk = make_block(D, xform == 1, bits);
+    auto b = std::make_unique<PlanBasis>();
+    b->device = device;
+    b->D = D;
+    b->xform = xform;
+    b->bits = bits;
+    if (cudaMalloc(&b->dblock, blk.size() * 2) != cudaSuccess) return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
+    if (cudaMemcpy(b->dblock, blk.data(), blk.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
+      cudaFree(b->dblock);
+      return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
+    }
+    b->rot_dev = static_cast<const uint16_t*>(b->dblock);
+    b->wq_dev = b->rot_dev + rot_halves();
+    b->wo_dev = b->wq_dev + (size_t)D * D;
+    b->wqf_dev = reinterpret_cast<const uint4*>(b->wo_dev + (size_t)D * D);
+    b->wof_dev = reinterpret_cast<const uint4*>(b->wo_dev + (size_t)2 * D * D);
+    slot = std::move(b);
+  }
+  ++slot->users;
+  *out = slot.get();
+  return KVQ_OK;
+}
+
+void release_basis(PlanBasis* b) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (--b->users > 0) return;
+  cudaFree(b->dblock);
+  g_bases.erase({b->device, b->D, b->xform, b->bits});
+}
+
+}  // namespace kvq

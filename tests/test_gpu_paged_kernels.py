@@ -406,3 +406,42 @@ def test_cache_class_workspaces_stay_within_twice_the_largest(kvq):
     now = cache._ws[Hq].numel()
     kept = sum(w.numel() for w in cache._grown)
     assert need <= now <= 2 * need and kept <= now
+
+
+# ---------------------------------------------------------------- factors
+@pytest.mark.parametrize("D,G,bits,xf", [(128, 32, 4, "srft"), (128, 16, 8, "srht"), (256, 32, 4, "srht"), (256, 16, 8, "srft")])
+@pytest.mark.parametrize("q", [1, 70])
+def test_each_kernel_with_factors_of_seven_decades(kvq, path, q, D, G, bits, xf):
+    """Factors from 3e-4 to 3e3, a group of channels each, and scales in proportion, as an encode would
+    give: every channel counts alike in the scores and in the output."""
+    n = 300
+    c = Cache(kvq, [n, 40], [q, 2], 4, 1, D, G, bits, xf, 32, seed=16, spoil=False)
+    lam = np.repeat(np.random.default_rng(1).permutation(np.logspace(-3.5, 3.5, D // G)), G)
+    for which in "kv":
+        signs = kvgen.plan_params(D, seed=17, kind=which)[0]
+        params = (signs, lam.astype(np.float32))
+        plan = kvq.Plan(*params, G, xf, bits)
+        s = c.ks if which == "k" else c.vs
+        s[:] = (s.astype(np.float64) * lam[::G]).astype(np.float16)
+        if which == "k":
+            c.pk, c.kp = plan, params
+        else:
+            c.pv, c.vp = plan, params
+    # scales of 3e-4 / 127 keep 2 to 7 bits in fp16: the reference reads the same ones
+    put_scales(c)
+    c.check(c.run(kvq, max_q_len=max(q, 2)))
+
+
+def test_plans_hold_no_matrices_for_paged_calls(kvq):
+    """What plans hold on the device: the codec's own operands (2 D^2 halves to encode, D^2 to decode) and
+    4 KB, the rest shared."""
+    D, n = 256, 64
+    first = make_plan(kvq, D, "k")[0]
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0]
+    plans = [make_plan(kvq, D, "k", seed=s)[0] for s in range(n)]
+    used = before - torch.cuda.mem_get_info()[0]
+    own = 3 * D * D * 2 + 4096
+    # the allocator hands out 2 MB blocks
+    assert used <= n * own * 1.4 + (4 << 20), used / n
+    del first, plans
