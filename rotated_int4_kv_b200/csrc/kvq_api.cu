@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <memory>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -166,6 +167,24 @@ kvq_status check_plan_device(const kvq_plan* p) {
 
 using kvq::fail;
 
+namespace {
+
+// No C++ exception leaves a C entry point.
+template <typename F>
+kvq_status guarded(const char* who, F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    try {
+      return fail(KVQ_ERR_CUDA, std::string(who) + ": out of host memory");
+    } catch (...) {
+      return KVQ_ERR_CUDA;
+    }
+  }
+}
+
+}  // namespace
+
 extern "C" {
 
 const char* kvq_status_string(kvq_status s) {
@@ -199,123 +218,94 @@ kvq_status kvq_plan_create_transform(kvq_plan** out, int D, int G, const int8_t*
 
 kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs, const float* lambda, int transform,
                               int bits) {
-  if (!out || !signs || !lambda) return fail(KVQ_ERR_INVALID_ARG, "plan_create: null argument");
-  *out = nullptr;
-  if (bits != 4 && bits != 8) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: bits must be 4 or 8");
-  if (transform != KVQ_TRANSFORM_SRFT && transform != KVQ_TRANSFORM_SRHT)
-    return fail(KVQ_ERR_UNSUPPORTED, "plan_create: transform must be KVQ_TRANSFORM_SRFT or KVQ_TRANSFORM_SRHT");
-  const bool hadamard = transform == KVQ_TRANSFORM_SRHT;
-  if (D != 128 && D != 256) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: head_dim must be 128 or 256");
-  if (G != 32 && G != 16) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: group must be 32 or 16");
-  for (int i = 0; i < D; ++i) {
-    if (signs[i] != 1 && signs[i] != -1) return fail(KVQ_ERR_INVALID_ARG, "plan_create: signs must be +1/-1");
-    if (!(std::isfinite(lambda[i]) && lambda[i] > 0.0f))
-      return fail(KVQ_ERR_INVALID_ARG, "plan_create: lambda must be finite and > 0");
-  }
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return fail(KVQ_ERR_DEVICE, "plan_create: no CUDA device");
-  int major = 0;  // (one attribute: the whole property block takes milliseconds)
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major != 10)
-    return fail(KVQ_ERR_DEVICE, "plan_create: needs a compute capability 10.x (sm_100) device");
+  return guarded("plan_create", [&]() -> kvq_status {
+    if (!out || !signs || !lambda) return fail(KVQ_ERR_INVALID_ARG, "plan_create: null argument");
+    *out = nullptr;
+    if (bits != 4 && bits != 8) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: bits must be 4 or 8");
+    if (transform != KVQ_TRANSFORM_SRFT && transform != KVQ_TRANSFORM_SRHT)
+      return fail(KVQ_ERR_UNSUPPORTED, "plan_create: transform must be KVQ_TRANSFORM_SRFT or KVQ_TRANSFORM_SRHT");
+    const bool hadamard = transform == KVQ_TRANSFORM_SRHT;
+    if (D != 128 && D != 256) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: head_dim must be 128 or 256");
+    if (G != 32 && G != 16) return fail(KVQ_ERR_UNSUPPORTED, "plan_create: group must be 32 or 16");
+    for (int i = 0; i < D; ++i) {
+      if (signs[i] != 1 && signs[i] != -1) return fail(KVQ_ERR_INVALID_ARG, "plan_create: signs must be +1/-1");
+      if (!(std::isfinite(lambda[i]) && lambda[i] > 0.0f))
+        return fail(KVQ_ERR_INVALID_ARG, "plan_create: lambda must be finite and > 0");
+    }
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(KVQ_ERR_DEVICE, "plan_create: no CUDA device");
+    int major = 0;  // (one attribute: the whole property block takes milliseconds)
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess || major != 10)
+      return fail(KVQ_ERR_DEVICE, "plan_create: needs a compute capability 10.x (sm_100) device");
 
-  kvq::PlanBasis* basis_dev = nullptr;
-  const kvq_status st = kvq::acquire_basis(dev, D, transform, bits, &basis_dev);
-  if (st != KVQ_OK) return st;
-  kvq_plan* p = new kvq_plan();
-  p->basis = basis_dev;
-  p->D = D;
-  p->G = G;
-  p->device = dev;
-  p->xform = transform;
-  p->bits = bits;
-  // per-channel factor of the rotation's unnormalised rows: the real DFT's dg_c, or
-  // 1/sqrt(D) for every Hadamard row
-  for (int c = 0; c < D; ++c) {
-    const double dg = hadamard ? 1.0 / std::sqrt((double)D) : kvq::basis_dg(c, D);
-    p->enc.chan[c] = (float)((double)lambda[c] * dg);
-    p->dec.chan[c] = (float)(dg / (double)lambda[c]);
-  }
-  for (int w = 0; w < D / 2; ++w) {
-    const uint32_t m = (signs[2 * w] < 0 ? 0x8000u : 0u) | (signs[2 * w + 1] < 0 ? 0x80000000u : 0u);
-    p->enc.sgn[w] = m;
-    p->dec.sgn[w] = m;
-  }
-  // tensor-core encode operand: W = Lambda F_r diag(s) (channel rows, D columns) as an
-  // fp16 pair (value = hi + lo to ~2^-22 |W|), laid out per 128-channel half h as
-  // 128 hi rows then 128 lo rows: row 256 h + r = hi of channel 128 h + r,
-  // row 256 h + 128 + r = lo of the same channel.
-  // SRHT plans: W = H diag(s) exactly (entries +-1; D rows, D columns), the factor
-  // lambda_c / sqrt(D) is applied by the kernel's epilogue.
-  std::vector<double> basis((size_t)D * D);  // Q, row = channel: every operand below is made of it
-  for (int c = 0; c < D; ++c)
-    for (int n = 0; n < D; ++n)
-      basis[(size_t)c * D + n] =
-          hadamard ? kvq::hadamard_value(c, n) / std::sqrt((double)D) : kvq::basis_value(c, n, D);
-  std::vector<uint16_t> wt(hadamard ? (size_t)D * D : (size_t)2 * D * D);
-  for (int c = 0; c < D; ++c) {
-    const int h = c / 128, rr = c % 128;
-    for (int n = 0; n < D; ++n) {
-      if (hadamard) {
-        wt[(size_t)c * D + n] = kvq::half_bits((float)(kvq::hadamard_value(c, n) * (double)signs[n]));
-        continue;
-      }
-      const double w = (double)lambda[c] * basis[(size_t)c * D + n] * (double)signs[n];
-      const uint16_t hi = kvq::half_bits((float)w);
-      const uint16_t lo = kvq::half_bits((float)(w - (double)kvq::half_value(hi)));
-      wt[(size_t)(256 * h + rr) * D + n] = hi;
-      wt[(size_t)(256 * h + 128 + rr) * D + n] = lo;
+    std::unique_ptr<kvq_plan> made(new kvq_plan());
+    kvq_plan* p = made.get();
+    kvq_status st = kvq::acquire_basis(dev, D, transform, bits, &p->basis);
+    if (st != KVQ_OK) return st;
+    p->D = D;
+    p->G = G;
+    p->device = dev;
+    p->xform = transform;
+    p->bits = bits;
+    // per-channel factor of the rotation's unnormalised rows: the real DFT's dg_c, or
+    // 1/sqrt(D) for every Hadamard row
+    for (int c = 0; c < D; ++c) {
+      const double dg = hadamard ? 1.0 / std::sqrt((double)D) : kvq::basis_dg(c, D);
+      p->enc.chan[c] = (float)((double)lambda[c] * dg);
+      p->dec.chan[c] = (float)(dg / (double)lambda[c]);
     }
-  }
-  // tensor-core decode operand: W_dec = diag(s) Q^T Lambda^-1 (row n = output sample n,
-  // column = channel), one fp16 rounding per entry; the columns of each 16-byte unit in
-  // the order the kernel's dequantiser writes the channels (decode_unit_channel)
-  std::vector<uint16_t> wdec((size_t)D * D);
-  for (int n = 0; n < D; ++n)
-    for (int k = 0; k < D; ++k) {
-      const int c = (k & ~7) + kvq::decode_unit_channel(k & 7, bits);
-      const double q = basis[(size_t)c * D + n];
-      wdec[(size_t)n * D + k] = kvq::half_bits((float)((double)signs[n] * q / (double)lambda[c]));
+    for (int w = 0; w < D / 2; ++w) {
+      const uint32_t m = (signs[2 * w] < 0 ? 0x8000u : 0u) | (signs[2 * w + 1] < 0 ? 0x80000000u : 0u);
+      p->enc.sgn[w] = m;
+      p->dec.sgn[w] = m;
     }
-  constexpr size_t kWtOff = 4096;  // after the two CodecConsts copies, 16-byte aligned for TMA
-  static_assert(2 * sizeof(kvq::CodecConsts) <= kWtOff, "plan block layout");
-  const size_t wdec_off = kWtOff + wt.size() * 2;
-  const size_t bytes = wdec_off + wdec.size() * 2;
-  void* blk = nullptr;
-  if (cudaMalloc(&blk, bytes) != cudaSuccess) {
-    kvq::release_basis(p->basis);
-    delete p;
-    return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
-  }
-  if (cudaMemcpy(blk, &p->enc, sizeof(kvq::CodecConsts), cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemcpy((char*)blk + sizeof(kvq::CodecConsts), &p->dec, sizeof(kvq::CodecConsts), cudaMemcpyHostToDevice) !=
-          cudaSuccess ||
-      cudaMemcpy((char*)blk + kWtOff, wt.data(), wt.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess ||
-      cudaMemcpy((char*)blk + wdec_off, wdec.data(), wdec.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
-    cudaFree(blk);
-    kvq::release_basis(p->basis);
-    delete p;
-    return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
-  }
-  p->dblock = blk;
-  p->enc_dev = reinterpret_cast<const kvq::CodecConsts*>(blk);
-  p->dec_dev = reinterpret_cast<const kvq::CodecConsts*>((char*)blk + sizeof(kvq::CodecConsts));
-  p->wt_dev = reinterpret_cast<const uint16_t*>((char*)blk + kWtOff);
-  p->rot_dev = p->basis->rot_dev;
-  p->wdec_dev = reinterpret_cast<const uint16_t*>((char*)blk + wdec_off);
-  *out = p;
-  return KVQ_OK;
+    // Device block: the header, then
+    //  * the tensor-core encode's operand W = Lambda F_r diag(s) (channel rows, D columns) as an
+    //    fp16 pair (value = hi + lo to ~2^-22 |W|), laid out per 128-channel half h as 128 hi
+    //    rows then 128 lo rows: row 256 h + r = hi of channel 128 h + r, row 256 h + 128 + r = lo
+    //    of the same channel. SRHT plans: W = H diag(s) exactly (entries +-1; D rows, D
+    //    columns), the factor lambda_c / sqrt(D) is applied by the kernel's epilogue;
+    //  * the tensor-core decode's W_dec = diag(s) Q^T Lambda^-1 (row n = output sample n, column
+    //    = channel), one fp16 rounding per entry; the columns of each 16-byte unit in the
+    //    order the kernel's dequantiser writes the channels (word_place).
+    static_assert(sizeof(kvq::PlanHeader) % 1024 == 0, "TMA operands behind the header");
+    kvq::PlanHeader head{p->enc, p->dec, {}};
+    std::copy(lambda, lambda + D, head.lambda);
+    const size_t n_wt = (size_t)(hadamard ? 1 : 2) * D * D, n_wdec = (size_t)D * D;
+    if (cudaMalloc(&p->dblock, sizeof(head) + (n_wt + n_wdec) * 2) != cudaSuccess) {
+      p->dblock = nullptr;
+      kvq_plan_destroy(made.release());
+      return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
+    }
+    char* blk = static_cast<char*>(p->dblock);
+    const kvq::PlanHeader* head_dev = reinterpret_cast<const kvq::PlanHeader*>(blk);
+    uint16_t* wt = reinterpret_cast<uint16_t*>(blk + sizeof(head));
+    p->enc_dev = &head_dev->enc;
+    p->dec_dev = &head_dev->dec;
+    p->wt_dev = wt;
+    p->wdec_dev = wt + n_wt;
+    p->rot_dev = p->basis->rot_dev;
+    if (cudaMemcpy(blk, &head, sizeof(head), cudaMemcpyHostToDevice) != cudaSuccess)
+      st = fail(KVQ_ERR_CUDA, "plan_create: upload failed");
+    else
+      st = kvq::form_plan(p->basis, head_dev, wt, wt + n_wt);
+    if (st != KVQ_OK) {
+      kvq_plan_destroy(made.release());
+      return st;
+    }
+    *out = made.release();
+    return KVQ_OK;
+  });
 }
 
 kvq_status kvq_plan_destroy(kvq_plan* p) {
   if (!p) return KVQ_OK;
-  if (p->dblock) {
-    int cur = -1;
-    cudaGetDevice(&cur);
-    if (cur != p->device) cudaSetDevice(p->device);
-    cudaFree(p->dblock);
-    kvq::release_basis(p->basis);
-    if (cur != p->device && cur >= 0) cudaSetDevice(cur);
-  }
+  int cur = -1;
+  cudaGetDevice(&cur);
+  if (cur != p->device) cudaSetDevice(p->device);
+  if (p->dblock) cudaFree(p->dblock);
+  kvq::release_basis(p->basis);
+  if (cur != p->device && cur >= 0) cudaSetDevice(cur);
   delete p;
   return KVQ_OK;
 }
@@ -620,20 +610,6 @@ kvq_status check_pages(const char* who, int num_pages, int page_size, int Hkv) {
   if ((long long)num_pages * page_size > 0x7fffffffll || (long long)num_pages * Hkv > 0x7fffffffll)
     return fail(KVQ_ERR_UNSUPPORTED, w + "num_pages * page_size and num_pages * Hkv must be below 2^31");
   return KVQ_OK;
-}
-
-// No C++ exception leaves a C entry point.
-template <typename F>
-kvq_status guarded(const char* who, F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    try {
-      return fail(KVQ_ERR_CUDA, std::string(who) + ": out of host memory");
-    } catch (...) {
-      return KVQ_ERR_CUDA;
-    }
-  }
 }
 
 bool same_form(const kvq_plan* a, const kvq_plan* b) {

@@ -24,12 +24,19 @@ struct CodecConsts {
   uint32_t sgn[kMaxD / 2]; // XOR mask per fp16 pair of the original domain (0x8000 per negative s)
 };
 
+// The front of a plan's device block.
+struct PlanHeader {
+  CodecConsts enc, dec;
+  float lambda[kMaxD];
+};
+
 // What plans of one device, head_dim, transform and code width share (kvq_plan_basis.cu), held
 // while one of them lives: the rotation without signs and factors.
 struct PlanBasis {
   int device, D, xform, bits;
   int users = 0;
   void* dblock = nullptr;
+  const double* q_dev = nullptr;      // Q, row = channel
   const uint16_t* rot_dev = nullptr;  // F128 (see kvq_plan)
   // Paged attention, with E = Q, its rows divided by basis_dg (fp16): E (query rotation) and E^T
   // (output un-rotation), each as row-major [D][D] with the channels in the order of
@@ -109,11 +116,9 @@ int num_sms(int device);
 // the shared part of a plan on the current device (kvq_plan_basis.cu)
 kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out);
 void release_basis(PlanBasis* b);
-double basis_value(int c, int n, int D);   // the orthonormal real DFT, row = channel
-double basis_dg(int c, int D);             // its rows' normalisation: 1/sqrt(D), sqrt(2/D) (cos), -sqrt(2/D) (sin)
-double hadamard_value(int i, int j);
-uint16_t half_bits(float f);
-float half_value(uint16_t b);
+double basis_dg(int c, int D);  // the real DFT's rows' normalisation: 1/sqrt(D), sqrt(2/D) (cos), -sqrt(2/D) (sin)
+// a plan's codec operands from its header, both on the device; returns when they are there
+kvq_status form_plan(const PlanBasis* b, const PlanHeader* head_dev, uint16_t* wt, uint16_t* wdec);
 
 kvq_status check_plan_device(const kvq_plan* p);
 
@@ -157,13 +162,6 @@ kvq_status launch_decode_tc(const kvq_plan* p, const uint8_t* codes, const uint1
 uint32_t decode_tc_error_flags(bool clear);
 // decode path: 0 = tensor cores (default), 1 = register FFT
 int decode_path();
-// K position p (0..7) of a 16-byte unit of the tensor-core decode's fp16 operand -> the
-// channel offset within the unit's eight channels (the dequantiser's pair order)
-inline int decode_unit_channel(int p, int bits) {
-  if (bits == 4) return (p & 1) ? (p >> 1) + 4 : (p >> 1);  // pairs (j, j + 4) of one 32-bit word
-  static const int k8[8] = {0, 2, 1, 3, 4, 6, 5, 7};       // pairs (0, 2), (1, 3) of each word
-  return k8[p];
-}
 
 // codec launchers (kvq_codec.cu)
 kvq_status launch_encode_jobs(const kvq_encode_job* jobs, int njobs, cudaStream_t s);

@@ -1,7 +1,8 @@
 // kvq_plan_basis.cu -- what plans of the same head_dim, transform and code width share: the
 // rotation without signs and factors, as the attention kernels' operands. Signs and factors
 // are a plan's own few KB, which the kernels apply around these (an exact change of sign, one
-// fp32 product per element), so a plan holds no matrix of its own for them.
+// fp32 product per element), so a plan holds no matrix of its own for them. And the codec's
+// matrices of a plan, formed on the GPU from the shared rotation in 64 bits.
 #include <cmath>
 #include <map>
 #include <memory>
@@ -13,17 +14,6 @@
 
 namespace kvq {
 
-// Row c of the orthonormal real basis in channel order, at sample n: DC, then
-// (cos_k, +sin_k) pairs, then Nyquist; angles from the exact residue k n mod D.
-double basis_value(int c, int n, int D) {
-  const double pi2 = 6.283185307179586476925286766559;
-  if (c == 0) return 1.0 / std::sqrt((double)D);
-  if (c == D - 1) return ((n & 1) ? -1.0 : 1.0) / std::sqrt((double)D);
-  const int k = (c + 1) / 2;
-  const double ang = pi2 * (double)((long)k * n % D) / (double)D;
-  return std::sqrt(2.0 / D) * ((c & 1) ? std::cos(ang) : std::sin(ang));
-}
-
 // Entry (i, j) of the Sylvester Hadamard matrix in natural order: (-1)^popcount(i & j).
 double hadamard_value(int i, int j) { return (__builtin_popcount((unsigned)(i & j)) & 1) ? -1.0 : 1.0; }
 
@@ -32,10 +22,40 @@ double basis_dg(int c, int D) {
   return (c & 1) ? std::sqrt(2.0 / D) : -std::sqrt(2.0 / D);
 }
 
+namespace {
+
 uint16_t half_bits(float f) { return __half_as_ushort(__float2half_rn(f)); }
 float half_value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 
-namespace {
+// cos and sin of 2 pi r / M for r < M: every angle of an M-point transform, by its residue.
+struct Circle {
+  std::vector<double> c, s;
+  explicit Circle(int M) : c(M), s(M) {
+    for (int r = 0; r < M; ++r) {
+      const double ang = 6.283185307179586476925286766559 * (double)r / (double)M;
+      c[r] = std::cos(ang);
+      s[r] = std::sin(ang);
+    }
+  }
+};
+
+// Q, row = channel. The orthonormal real basis in channel order: DC, then (cos_k, +sin_k)
+// pairs, then Nyquist; or the normalised Hadamard matrix.
+std::vector<double> make_basis(int D, bool hadamard) {
+  std::vector<double> q((size_t)D * D);
+  const Circle w(D);
+  const double one = 1.0 / std::sqrt((double)D), two = std::sqrt(2.0 / D);
+  for (int c = 0; c < D; ++c)
+    for (int n = 0; n < D; ++n) {
+      double& v = q[(size_t)c * D + n];
+      const int r = (c + 1) / 2 * n % D;
+      if (hadamard) v = hadamard_value(c, n) / std::sqrt((double)D);
+      else if (c == 0) v = one;
+      else if (c == D - 1) v = (n & 1) ? -one : one;
+      else v = two * ((c & 1) ? w.c[r] : w.s[r]);
+    }
+  return q;
+}
 
 constexpr int kF = 128;  // points of the dense attention's transform
 
@@ -43,23 +63,21 @@ constexpr int kF = 128;  // points of the dense attention's transform
 size_t rot_halves() { return (size_t)2 * kF * kF; }
 size_t block_halves(int D) { return rot_halves() + (size_t)4 * D * D; }
 
-std::vector<uint16_t> make_block(int D, bool hadamard, int bits) {
+std::vector<uint16_t> make_block(int D, bool hadamard, int bits, const std::vector<double>& basis) {
   std::vector<uint16_t> blk(block_halves(D));
   // dense attention (both head dims): the unnormalised 128-point real DFT in slot order, F128
   // (hi, lo): row 0 = 1, row 1 = (-1)^m, row 2k = cos(2 pi k m / 128), row 2k+1 =
   // -sin(2 pi k m / 128); for the SRHT the 128-point Hadamard matrix (exact in fp16, lo = 0).
   // D = 128 applies it directly, D = 256 to the even and odd samples.
-  const double pi2 = 6.283185307179586476925286766559;
+  const Circle w(kF);
   for (int j = 0; j < kF; ++j)
     for (int m = 0; m < kF; ++m) {
+      const int r = j / 2 * m % kF;
       double v;
       if (hadamard) v = hadamard_value(j, m);
       else if (j == 0) v = 1.0;
       else if (j == 1) v = (m & 1) ? -1.0 : 1.0;
-      else {
-        const double ang = pi2 * (double)((long)(j / 2) * m % kF) / (double)kF;
-        v = (j & 1) ? -std::sin(ang) : std::cos(ang);
-      }
+      else v = (j & 1) ? -w.s[r] : w.c[r];
       const uint16_t hi = half_bits((float)v);
       blk[(size_t)j * kF + m] = hi;
       blk[(size_t)(kF + j) * kF + m] = half_bits((float)(v - (double)half_value(hi)));
@@ -73,7 +91,7 @@ std::vector<uint16_t> make_block(int D, bool hadamard, int bits) {
   for (int c = 0; c < D; ++c)
     for (int n = 0; n < D; ++n)
       nat[(size_t)c * D + n] =
-          half_bits((float)(hadamard ? hadamard_value(c, n) : basis_value(c, n, D) / basis_dg(c, D)));
+          half_bits((float)(hadamard ? hadamard_value(c, n) : basis[(size_t)c * D + n] / basis_dg(c, D)));
   for (int which = 0; which < 2; ++which) {
     uint16_t* row = blk.data() + rot_halves() + (size_t)which * D * D;
     uint16_t* frag = row + (size_t)2 * D * D;
@@ -96,7 +114,11 @@ std::vector<uint16_t> make_block(int D, bool hadamard, int bits) {
 
 std::mutex g_mu;
 // the host's tables, kept: constants of mathematics
-std::map<std::tuple<int, int, int>, std::vector<uint16_t>> g_host;
+struct HostBasis {
+  std::vector<uint16_t> blk;
+  std::vector<double> q;
+};
+std::map<std::tuple<int, int, int>, HostBasis> g_host;
 // the device's, as long as a plan uses them
 std::map<std::tuple<int, int, int, int>, std::unique_ptr<PlanBasis>> g_bases;
 
@@ -106,19 +128,25 @@ kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out
   std::lock_guard<std::mutex> lk(g_mu);
   auto& slot = g_bases[{device, D, xform, bits}];
   if (!slot) {
-    auto& blk = g_host[{D, xform, bits}];
-    if (blk.empty()) blk = make_block(D, xform == 1, bits);
+    HostBasis& h = g_host[{D, xform, bits}];
+    if (h.blk.empty()) {
+      h.q = make_basis(D, xform == 1);
+      h.blk = make_block(D, xform == 1, bits, h.q);
+    }
     auto b = std::make_unique<PlanBasis>();
     b->device = device;
     b->D = D;
     b->xform = xform;
     b->bits = bits;
-    if (cudaMalloc(&b->dblock, blk.size() * 2) != cudaSuccess) return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
-    if (cudaMemcpy(b->dblock, blk.data(), blk.size() * 2, cudaMemcpyHostToDevice) != cudaSuccess) {
+    const size_t nq = h.q.size() * 8, nblk = h.blk.size() * 2;
+    if (cudaMalloc(&b->dblock, nq + nblk) != cudaSuccess) return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
+    if (cudaMemcpy(b->dblock, h.q.data(), nq, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaMemcpy(static_cast<char*>(b->dblock) + nq, h.blk.data(), nblk, cudaMemcpyHostToDevice) != cudaSuccess) {
       cudaFree(b->dblock);
       return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
     }
-    b->rot_dev = static_cast<const uint16_t*>(b->dblock);
+    b->q_dev = static_cast<const double*>(b->dblock);
+    b->rot_dev = reinterpret_cast<const uint16_t*>(b->q_dev + h.q.size());
     b->wq_dev = b->rot_dev + rot_halves();
     b->wo_dev = b->wq_dev + (size_t)D * D;
     b->wqf_dev = reinterpret_cast<const uint4*>(b->wo_dev + (size_t)D * D);
@@ -135,6 +163,38 @@ void release_basis(PlanBasis* b) {
   if (--b->users > 0) return;
   cudaFree(b->dblock);
   g_bases.erase({b->device, b->D, b->xform, b->bits});
+}
+
+namespace {
+
+// Block c, thread n: the entries of channel c and sample n. Every operation in 64 bits, rounded
+// as written, so that the bits are those of the same formulas on a host.
+__global__ void __launch_bounds__(kMaxD) form_plan_kernel(const double* q, const PlanHeader* head, int D, bool hadamard,
+                                                          int bits, uint16_t* wt, uint16_t* wdec) {
+  const int c = blockIdx.x, n = threadIdx.x;
+  const double v = q[(size_t)c * D + n], lam = (double)head->lambda[c];
+  const double s = (head->enc.sgn[n >> 1] >> (n & 1 ? 31 : 15)) & 1 ? -1.0 : 1.0;
+  auto bits16 = [](double x) { return __half_as_ushort(__float2half_rn(__double2float_rn(x))); };
+  if (hadamard) {
+    wt[(size_t)c * D + n] = bits16(v < 0.0 ? -s : s);
+  } else {
+    const double w = __dmul_rn(__dmul_rn(lam, v), s);
+    const uint16_t hi = bits16(w);
+    const size_t row = 256 * (c >> 7) + (c & 127);
+    wt[row * D + n] = hi;
+    wt[(row + 128) * D + n] = bits16(__dsub_rn(w, (double)__half2float(__ushort_as_half(hi))));
+  }
+  wdec[(size_t)n * D + word_place(c, bits)] = bits16(__ddiv_rn(__dmul_rn(s, v), lam));
+}
+
+}  // namespace
+
+kvq_status form_plan(const PlanBasis* b, const PlanHeader* head_dev, uint16_t* wt, uint16_t* wdec) {
+  form_plan_kernel<<<b->D, b->D>>>(b->q_dev, head_dev, b->D, b->xform == 1, b->bits, wt, wdec);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("plan_create: ") + cudaGetErrorString(e));
+  return KVQ_OK;
 }
 
 }  // namespace kvq
