@@ -116,6 +116,7 @@ struct PagedParams {
   long long q_ts, q_hs, table_stride;
   float qfac;              // sigma log2(e)
   int B, n_q, Hq, Hkv, Gq, rt_max, max_q, max_kv, num_pages, page_shift, window, min_tiles;
+  bool packed;             // units numbered by where the queries lie (see unit_base)
 };
 
 // ---------------------------------------------------------------- small helpers
@@ -226,6 +227,36 @@ __device__ __forceinline__ Request request_of(const PagedParams& p, int b) {
   return r;
 }
 
+// The numbers of units: (row tile of all requests, KV head). A request's row tiles start at
+// b rt_max, rt_max being what the longest may have; or packed, where the bound on the longest is
+// loose, at floor(first query row / 8) + b: at least ceil(rows / 8) further on for every request,
+// as floor(x + y) + 1 >= floor(x) + ceil(y), and n_q Gq / 8 + B of them in all.
+__device__ __forceinline__ int unit_base(const PagedParams& p, int b, int qs) {
+  return p.packed ? qs * p.Gq / kRows + b : b * p.rt_max;
+}
+
+// The request and row tile of row tile x of all requests (rt < 0: none). Packed: the last request
+// that starts at or in front of x, by a warp's 32 probes at a time.
+__device__ __forceinline__ void request_at(const PagedParams& p, int x, int& b, int& rt) {
+  if (!p.packed) {
+    b = x / p.rt_max;
+    rt = x - b * p.rt_max;
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  auto base = [&](int i) { return unit_base(p, i, min(max(__ldg(p.q_starts + i), 0), p.n_q)); };
+  int lo = 0, n = p.B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, lane * step < n && base(i) <= x);
+    const int k = at ? 31 - __clz(at) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  b = lo;
+  rt = x - base(lo);
+}
+
 __device__ __forceinline__ long long tiles_of(const PagedParams& p, const Request& r) {
   return (long long)p.Hkv * r.rt * r.nt;
 }
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
   constexpr int NC = C::NC, MT = C::MT, NWARP = kUnitWarps<D>, TW = MT / NWARP;
   __shared__ __align__(16) float om[kRows * C::kOmStride];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int unit = blockIdx.x, x = unit / p.Hkv, h = unit - x * p.Hkv;
   uint4 wf[TW][MT];
 #pragma unroll
   for (int t = 0; t < TW; ++t)
@@ -310,9 +341,11 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
   }
   grid_dep_wait();
   grid_dep_launch();  // after the wait: what the main kernel reads before its own wait is complete
+  int b, rt;
+  request_at(p, x, b, rt);
   const Request r = request_of<C::kTile>(p, b);
   const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
-  if (nrows <= 0) return;
+  if (nrows <= 0 || rt < 0) return;
   uint32_t bq[MT][2];
   {
     const int y = rt * kRows + (g < nrows ? g : 0), tok = y / p.Gq, head = h * p.Gq + (y - tok * p.Gq);
@@ -570,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
     const Request& r = w.r;
     const int h = w.u / r.rt, rt = w.u - h * r.rt;
     const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
-    const size_t unit = ((size_t)w.b * p.Hkv + h) * p.rt_max + rt;
+    const size_t unit = (size_t)(unit_base(p, w.b, r.qs) + rt) * p.Hkv + h;
     // row x of the tile: query token (rt * 8 + x) / Gq, head of the group the remainder
     auto q_row = [&](int x, int& tok, int& head) {
       const int y = rt * kRows + x;
@@ -1016,7 +1049,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   __shared__ __align__(16) __half xb[kRows * (D + 8)];
   __shared__ float red[2][NT / 8][kRows], wts[kMaxCtas * kRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int unit = blockIdx.x, rt = unit % p.rt_max, bh = unit / p.rt_max, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int unit = blockIdx.x, xt = unit / p.Hkv, h = unit - xt * p.Hkv;
   uint4 wf[TW][MT];
 #pragma unroll
   for (int t = 0; t < TW; ++t)
@@ -1031,9 +1064,11 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   grid_dep_wait();
   // the loads of a step together: request and description; then the first partials' m, l and o
   const int2 d = __ldcg(p.desc + unit);
+  int b, rt;
+  request_at(p, xt, b, rt);
   const Request r = request_of<128>(p, b);
   const int nrows = min(kRows, min(r.qn, p.max_q) * p.Gq - rt * kRows);
-  if (nrows <= 0) return;  // no such unit: nothing was written for it
+  if (nrows <= 0 || rt < 0) return;  // no such unit: nothing was written for it
   const int np = max(1, min(d.y, kMaxCtas));
   // the first CTA's slot, then the first slots of the CTAs after it
   auto part = [&](int k) {
@@ -1160,6 +1195,13 @@ constexpr size_t unit_bytes(int D) { return prep_bytes(D) + (2 * kRows + kRows *
 constexpr int kFewRows = 32;            // query rows of a request up to which this file's kernels take every call
 constexpr long long kFewUnits = 4096;   // units up to which they may take one with more (their workspace: 28 MB)
 
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+// units of a call with n_q query tokens, at most `rows` query rows of a request: the smaller of
+// the two ways to number them (unit_base)
+long long units_of(int B, int Hkv, int Gq, int n_q, long long rows) {
+  return (long long)Hkv * std::min(B * ceil_div(rows, kRows), (long long)n_q * Gq / kRows + B);
+}
+
 template <int D, int G, int BITS>
 kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   using C = PCfg<D, G, BITS>;
@@ -1207,7 +1249,9 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
   // there are CTAs to spare, t = sqrt(0.1 n) (one KV head of 256, 16K tokens:
   // 30.6 us with pieces of 2, 24.7 so).
   p.min_tiles = std::max(2, (int)std::sqrt(0.1 * attended / C::kTile));
-  const size_t units = (size_t)a.B * a.Hkv * p.rt_max;
+  const long long rows_max = (long long)std::min(a.max_q_len, a.n_q) * p.Gq;
+  const size_t units = (size_t)units_of(a.B, a.Hkv, p.Gq, a.n_q, rows_max);
+  p.packed = units < (size_t)a.B * a.Hkv * p.rt_max;  // (then there are q_starts: without, a request has one token)
   static_assert(C::kPrep <= prep_bytes(D), "workspace");
   p.part = reinterpret_cast<float*>(a.ws);
   p.part_unit = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) + kPartBytes);
@@ -1247,10 +1291,6 @@ kvq_status run_paged(const PagedAttendHost& a, cudaStream_t strm) {
 
 namespace {
 
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
-// units of a call: row tiles of `rows` query rows, over heads and requests
-long long units_of(int B, int Hkv, int rows) { return (long long)B * Hkv * ceil_div(rows, kRows); }
-
 // Whether the prompt kernel takes a call, by what both would take (us, fitted to both kernels
 // on 1, 4 and 32 requests of 256, 2048 and 16384 tokens with 1 - 64 query tokens each). Here a
 // tile of 8 rows costs little and every row tile converts the cache again; there up to 256 (128)
@@ -1263,7 +1303,7 @@ bool prefers_prompt(const PagedAttendHost& a) {
   const int Gq = a.Hq / a.Hkv, q = std::min(a.max_q_len, a.n_q);
   const long long rows = (long long)q * Gq;
   if (rows <= kFewRows) return false;
-  const long long units = units_of(a.B, a.Hkv, (int)std::min<long long>(rows, 0x7fffffff - kRows));
+  const long long units = units_of(a.B, a.Hkv, Gq, a.n_q, rows);
   if (units > kFewUnits) return true;
   const bool d128 = a.pk->D == 128;
   const long long all = (long long)a.n_q * Gq, R = d128 ? 256 : 128;
@@ -1280,12 +1320,13 @@ bool prefers_prompt(const PagedAttendHost& a) {
 }  // namespace
 
 size_t paged_workspace_bytes(int B, int Hq, int Hkv, int D, int n_q, int max_q_len, int path) {
-  const long long rows = (long long)std::min(max_q_len, std::max(n_q, 1)) * (Hq / Hkv);
-  if (path == 1) return kPartBytes + (size_t)(ceil_div(rows, kRows) * B * Hkv) * unit_bytes(D);
+  const int Gq = Hq / Hkv;
+  const long long rows = (long long)std::min(max_q_len, std::max(n_q, 1)) * Gq;
+  if (path == 1) return kPartBytes + (size_t)units_of(B, Hkv, Gq, n_q, rows) * unit_bytes(D);
   if (path == 2) return prompt_part_bytes();
   // whatever kernel a call with these sizes, or smaller ones, goes to
-  long long units = units_of(B, Hkv, (int)std::min<long long>(rows, kFewRows));
-  if (rows > kFewRows) units = std::max(units, std::min(kFewUnits, units_of(B, Hkv, (int)std::min<long long>(rows, 0x7fffffff - kRows))));
+  long long units = units_of(B, Hkv, Gq, n_q, std::min<long long>(rows, kFewRows));
+  if (rows > kFewRows) units = std::max(units, std::min(kFewUnits, units_of(B, Hkv, Gq, n_q, rows)));
   const size_t few = kPartBytes + (size_t)units * unit_bytes(D);
   return rows > kFewRows ? std::max(few, prompt_part_bytes()) : few;
 }

@@ -445,3 +445,40 @@ def test_plans_hold_no_matrices_for_paged_calls(kvq):
     # the allocator hands out 2 MB blocks
     assert used <= n * own * 1.4 + (4 << 20), used / n
     del first, plans
+
+
+# ---------------------------------------------------------------- loose bounds
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (5, 1, 128), (24, 2, 128), (4, 1, 256)])
+@pytest.mark.parametrize("B", [1, 3, 40, 70, 1100])
+def test_bounds_need_not_be_tight(kvq, path, B, Hq, Hkv, D):
+    """Without max_q_len (so n, as if one request had every token): single tokens, idle requests, a
+    longer one among them, padding; the same values as with the tight bound."""
+    rng = np.random.default_rng(B)
+    kv = rng.integers(1, 60, B)
+    for q in (np.ones(B, int), rng.integers(0, 3, B), np.where(rng.random(B) < 0.1, 37, rng.integers(0, 2, B))):
+        q[rng.integers(B)] = 1
+        c = Cache(kvq, kv, q, Hq, Hkv, D, 32, 4, "srft", 16, seed=B, pad=2)
+        out = torch.full((int(q.sum()) + 2, Hq, D), 5.0, dtype=torch.float16, device="cuda")
+        c.run(kvq, out=out)
+        assert (out[q.sum():] == 5.0).all()
+        tight = c.run(kvq, max_q_len=int(q.max()))[: q.sum()]
+        assert torch.equal(out[: q.sum()], tight) or rel_l2(out[: q.sum()].double().cpu(), tight.double().cpu()).max() < 2e-3
+        if B < 1000:
+            c.check(out)
+
+
+def test_a_loose_bound_keeps_the_workspace_and_the_kernel(kvq):
+    """A decode batch whose longest query is not told: the workspace is that of its tokens, and the few-row
+    kernel takes it (bit for bit the values that it gives)."""
+    B, Hq, Hkv = 64, 32, 8
+    need = kvq.paged_workspace_size(B, Hq, Hkv, 128, B, B)
+    kvq.set_attend_paged_path("few")
+    try:
+        few = kvq.paged_workspace_size(B, Hq, Hkv, 128, B, B)
+        assert few < 1.2 * kvq.paged_workspace_size(B, Hq, Hkv, 128, B, 1) + (4 << 20)
+        c = Cache(kvq, [300] * B, [1] * B, Hq, Hkv, 128, 32, 4, "srft", 64, seed=2, spoil=False)
+        want = c.run(kvq)
+    finally:
+        kvq.set_attend_paged_path("auto")
+    assert few <= need
+    assert torch.equal(c.run(kvq), want)
