@@ -215,10 +215,10 @@ __device__ __forceinline__ Request request_of(const PagedParams& p, int b) {
   r.qs = b;
   r.qn = 1;
   if (p.q_starts) {
-    r.qs = min(max(__ldg(p.q_starts + b), 0), p.n_q);
-    r.qn = min(max(__ldg(p.q_starts + b + 1), r.qs), p.n_q) - r.qs;
+    r.qs = min(max(ld_fresh(p.q_starts + b), 0), p.n_q);
+    r.qn = min(max(ld_fresh(p.q_starts + b + 1), r.qs), p.n_q) - r.qs;
   }
-  r.kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+  r.kv = min(max(ld_fresh(p.kv_lens + b), 0), p.max_kv);
   const long long lo = p.window ? (long long)r.kv - r.qn + 1 - p.window : 0;
   r.t_lo = (int)min(max(lo, 0ll), (long long)r.kv);
   r.tile0 = r.t_lo / kTile;
@@ -244,7 +244,7 @@ __device__ __forceinline__ void request_at(const PagedParams& p, int x, int& b, 
     return;
   }
   const int lane = threadIdx.x & 31;
-  auto base = [&](int i) { return unit_base(p, i, min(max(__ldg(p.q_starts + i), 0), p.n_q)); };
+  auto base = [&](int i) { return unit_base(p, i, min(max(ld_fresh(p.q_starts + i), 0), p.n_q)); };
   int lo = 0, n = p.B;
   while (n > 1) {
     const int step = (n + 31) / 32, i = lo + lane * step;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) rotate_paged_kernel(const 
     for (int ks = 0; ks < MT; ++ks) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        bq[ks][e] = g < nrows ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) ^ sgn[ks][e] : 0u;
+        bq[ks][e] = g < nrows ? ld_fresh(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8 * e + 2 * c)) ^ sgn[ks][e] : 0u;
     }
   }
 #pragma unroll
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, (PCfg<D, G, BITS>::kCtas))
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int x = tid + k * kWarps * 32;
-        if (x < C::kPrep / 16) v[k] = __ldcg(src + x);
+        if (x < C::kPrep / 16) v[k] = ld_fresh(src + x);
       }
       consumers_sync();  // the segment before has been read to its end
 #pragma unroll
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(kUnitWarps<D> * 32) join_paged_kernel(const __
   grid_dep_launch();
   grid_dep_wait();
   // the loads of a step together: request and description; then the first partials' m, l and o
-  const int2 d = __ldcg(p.desc + unit);
+  const int2 d = ld_fresh(p.desc + unit);
   int b, rt;
   request_at(p, xt, b, rt);
   const Request r = request_of<128>(p, b);

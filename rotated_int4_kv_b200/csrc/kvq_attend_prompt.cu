@@ -154,10 +154,10 @@ struct PrRequest {
     qs = b;
     qn = 1;
     if (p.q_starts) {
-      qs = min(max(__ldg(p.q_starts + b), 0), p.n_q);
-      qn = min(max(__ldg(p.q_starts + b + 1), qs), p.n_q) - qs;
+      qs = min(max(ld_fresh(p.q_starts + b), 0), p.n_q);
+      qn = min(max(ld_fresh(p.q_starts + b + 1), qs), p.n_q) - qs;
     }
-    kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+    kv = min(max(ld_fresh(p.kv_lens + b), 0), p.max_kv);
     rows = min(qn, p.max_q) * p.Gq;
     nrt = (rows + R - 1) / R;
   }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (long long)(w.r.qs + tok) * p.q_ts + (long long)head * p.q_hs);
 #pragma unroll 8
-        for (int u = 0; u < D / 8; ++u) *q_unit(u) = valid ? flip(__ldg(src + u), sQsgn[u]) : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < D / 8; ++u) *q_unit(u) = valid ? flip(ld_fresh(src + u), sQsgn[u]) : make_uint4(0, 0, 0, 0);
       }
       announce(&aready[qb]);
       // ---- q~, normalised by a power of two per row
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) attend_prompt_kernel(const __gr
       // the start: entries of tiles 0 and 1, scales of tile 0, the first halves
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        rows[0][j] = cache_row(0, j, live(0, j) ? __ldg(trow + (token(0, j) >> p.page_shift)) : -1);
+        rows[0][j] = cache_row(0, j, live(0, j) ? ld_fresh(trow + (token(0, j) >> p.page_shift)) : -1);
         rows[1][j] = -1;
       }
       fetch_entries(1);
@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_prompt_kernel(const __gr
   const uint4 sgn = __ldg(p.osgn + tid % (D / 8));  // of this thread's 8 samples of every row
   grid_dep_launch();
   grid_dep_wait();
-  const int4 u = __ldcg(p.desc + blockIdx.x);
+  const int4 u = ld_fresh(p.desc + blockIdx.x);
   if (u.w == 0) return;
   PrRequest<R, T> r;
   r.load(p, u.x);

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
       uint32_t sc[NS];
       if constexpr (PG) {
         cur.start(P, t_begin * kDtRows + row);
-        crow = cur.cache_row(P, cur.t < P.n ? __ldg(P.slots + cur.tok) : -1);
+        crow = cur.cache_row(P, cur.t < P.n ? ld_fresh(P.slots + cur.tok) : -1);
         cp_async_codes<D, BITS>(sC, warp - 2, lane, P, crow);
         cur.next(P);
         fetch_slot(cur);
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kDtThreads, 1) decode_tc_kernel(const __grid_c
     // pages: the next tile's cache row is a slot-map entry away, which is read a tile early
     DtCursor cur;
     int nslot = -1;
-    auto slot_of = [&](const DtCursor& k) { return k.t < P.n ? __ldg(P.slots + k.tok) : -1; };
+    auto slot_of = [&](const DtCursor& k) { return k.t < P.n ? ld_fresh(P.slots + k.tok) : -1; };
     if (ntile > 0) {
       uint32_t sc[NS];
       if constexpr (PG) {

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int slot = -1;
       if constexpr (PG) {
         const int tok = (t - J.tile0) * pg.tok + ptok;
-        if (ptok < pg.tok && tok < pg.n) slot = __ldg(pg.slots + tok);
+        if (ptok < pg.tok && tok < pg.n) slot = ld_fresh(pg.slots + tok);
       }
       // warp-uniform outcome: the tcgen05.ld below needs the whole warp
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[a], (i >> 1) & 1))) {

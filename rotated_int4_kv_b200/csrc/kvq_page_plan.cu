@@ -99,13 +99,15 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
   }
   grid_dep_launch();
   grid_dep_wait();
-  const int head = min(max(__ldcg(p.free_head), 0), p.n_free);
+  const int32_t *kv_lens = behind_wait(p.kv_lens), *q_lens = behind_wait(p.q_lens), *free_pages = behind_wait(p.free_pages);
+  const int32_t* table = behind_wait(p.table);
+  const int head = min(max(ld_fresh(p.free_head), 0), p.n_free);
   const long long room = p.n_free - head;
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long qs = 0, ns = 0;
   for (int b = b0; b < b1; ++b) {
-    const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
+    const long long kv = max(__ldcg(kv_lens + b), 0), q = max(__ldcg(q_lens + b), 0);
     const long long want = (kv + q + P - 1) >> p.page_shift;
     qs += q;
     ns += fits_table(p, kv, q) ? want - ((kv + P - 1) >> p.page_shift) : 0;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
   long long got = 0;
   int ref = 0;
   for (int b = b0; b < b1; ++b) {
-    const long long kv = max(__ldcg(p.kv_lens + b), 0), q = max(__ldcg(p.q_lens + b), 0);
+    const long long kv = max(__ldcg(kv_lens + b), 0), q = max(__ldcg(q_lens + b), 0);
     const long long want = (kv + q + P - 1) >> p.page_shift;
     const bool fits = fits_table(p, kv, q);
     const long long need = fits ? want - ((kv + P - 1) >> p.page_shift) : 0;
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
       const int first = s_first[b], have = (int)((kv + P - 1) >> p.page_shift);
       const int want = (int)((kv + q_of(b) + P - 1) >> p.page_shift);
       for (int e = have + lane; e < want; e += 32)
-        p.table[(long long)b * p.table_stride + e] = __ldg(p.free_pages + first + e - have);
+        p.table[(long long)b * p.table_stride + e] = free_pages[first + e - have];
     }
   } else for (int b0 = (gt >> 5) * 32; b0 < p.B; b0 += nthreads) {
     const int b = b0 + lane;
@@ -185,20 +187,29 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
       want = (int)((kv + q_of(b) + P - 1) >> p.page_shift);
     }
     for (int e = have; e < min(want, have + kFirst); ++e)
-      p.table[(long long)b * p.table_stride + e] = __ldg(p.free_pages + first + e - have);
+      p.table[(long long)b * p.table_stride + e] = free_pages[first + e - have];
     uint32_t more = __ballot_sync(0xffffffffu, want - have > kFirst);
     while (more) {
       const int l = __ffs(more) - 1;
       more &= more - 1;
       const int f = __shfl_sync(0xffffffffu, first, l), h = __shfl_sync(0xffffffffu, have, l), w = __shfl_sync(0xffffffffu, want, l);
       for (int e = h + kFirst + lane; e < w; e += 32)
-        p.table[(long long)(b0 + l) * p.table_stride + e] = __ldg(p.free_pages + f + e - h);
+        p.table[(long long)(b0 + l) * p.table_stride + e] = free_pages[f + e - h];
     }
   }
-  // slots and positions, one token per thread; behind the last token both are -1
-  for (long long t = gt; t < p.n_slots; t += nthreads) {
-    int slot = -1, pos = -1;
-    if (t < total && p.B > 0) {
+  // slots and positions; behind the last token both are -1. Four tokens of a thread at a time, so
+  // that their loads overlap: 190 thousand tokens 8.4 us a pass, 12.5 one by one (when, at 32
+  // registers a thread, two passes' CTAs also share an SM)
+  constexpr int U = NT == kPlanThreads ? 4 : 1;
+  for (long long t0 = gt; t0 < p.n_slots; t0 += (long long)U * nthreads) {
+    const int32_t* entry[U];
+    int slot[U], pos[U], page[U], place[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long t = t0 + (long long)u * nthreads;
+      entry[u] = nullptr;
+      slot[u] = pos[u] = -1;
+      if (t >= min(total, (long long)p.n_slots) || p.B == 0) continue;
       int lo = 0, hi = first_past;  // last request whose start is <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -206,18 +217,26 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(const __grid_constant__ P
         else hi = mid;
       }
       const long long kv = s_kv[lo], at = kv + (t - s_start[lo]);
-      pos = sat32(at);
+      pos[u] = sat32(at);
       const int first = s_first[lo];
-      if (first >= 0) {
-        const int blk = (int)(at >> p.page_shift), have = (int)((kv + P - 1) >> p.page_shift);
-        const int page = blk < have ? __ldcg(p.table + (long long)lo * p.table_stride + blk)
-                                    : __ldg(p.free_pages + first + blk - have);
-        // a page whose slots would not fit 32 bits is no page of a cache
-        slot = page < 0 || page > (0x7fffffff >> p.page_shift) ? -1 : page * P + (int)(at & (P - 1));
+      if (first < 0) continue;
+      const int blk = (int)(at >> p.page_shift), have = (int)((kv + P - 1) >> p.page_shift);
+      place[u] = (int)(at & (P - 1));
+      entry[u] = blk < have ? table + (long long)lo * p.table_stride + blk : free_pages + first + blk - have;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (entry[u]) page[u] = ld_fresh(entry[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a page whose slots would not fit 32 bits is no page of a cache
+      if (entry[u] && page[u] >= 0 && page[u] <= (0x7fffffff >> p.page_shift)) slot[u] = page[u] * P + place[u];
+      const long long t = t0 + (long long)u * nthreads;
+      if (t < p.n_slots) {
+        p.slots[t] = slot[u];
+        p.positions[t] = pos[u];
       }
     }
-    p.slots[t] = slot;
-    p.positions[t] = pos;
   }
 }
 
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_release_kernel(const uint8_
   const int tid = threadIdx.x, P = 1 << page_shift;
   grid_dep_launch();
   grid_dep_wait();
-  const int head = min(max(__ldcg(free_head), 0), n_free);
+  const int head = min(max(ld_fresh(free_head), 0), n_free);
   long long before = 0;  // pages returned by earlier chunks
   for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
     const int b = c0 + tid;

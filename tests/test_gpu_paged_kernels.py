@@ -482,3 +482,39 @@ def test_a_loose_bound_keeps_the_workspace_and_the_kernel(kvq):
         kvq.set_attend_paged_path("auto")
     assert few <= need
     assert torch.equal(c.run(kvq), want)
+
+
+# ---------------------------------------------------------------- calls that follow one another closely
+@pytest.mark.parametrize("q_hi", [1, 40])
+def test_steps_in_a_row_read_what_the_call_before_wrote(kvq, path, q_hi):
+    """Release, planning, encode and attention start early, while the call in front still runs: many steps
+    without a wait on the host leave the same state and outputs as steps that wait after every call."""
+    B, Hkv, Hq, D, P, M = 24, 2, 8, 128, 16, 12
+    params = kvgen.plan_params(D, seed=2, kind="k"), kvgen.plan_params(D, seed=2, kind="v")
+    made = []
+    for wait in (True, False):
+        rng = np.random.default_rng(9)
+        cache = kvq.PagedInt4KVCache(1, B, Hkv, D, 200, P, M, *params)
+        steps, outs = [], []
+        for _ in range(60):
+            q = rng.integers(0, q_hi + 1, B)
+            n = B * q_hi
+            x = torch.from_numpy(rng.standard_normal((2, n, Hkv, D)).astype(np.float16)).cuda()
+            qs = torch.from_numpy(rng.standard_normal((n, Hq, D)).astype(np.float16)).cuda()
+            steps.append((i32(q), torch.from_numpy(rng.random(B) < 0.15).cuda(), x, qs, torch.zeros((n, Hq, D), dtype=torch.float16, device="cuda")))
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        torch.cuda.synchronize()
+        for q, done, x, qs, out in steps:
+            step = cache.begin(q, x.shape[1])
+            sync()
+            cache.update(0, x[0], x[1], step)
+            sync()
+            outs.append(cache.attend(0, qs, step, max_q_len=q_hi, out=out))
+            sync()
+            outs.append(kvq.decode_paged(cache.k_plans[0], cache.k_codes[0], cache.k_scales[0], step.slots))
+            sync()
+            cache.release(done)
+            sync()
+        torch.cuda.synchronize()
+        made.append((*outs, cache.kv_lens, cache.free_head, cache.free_pages, cache.block_table, cache.k_codes[0], cache.v_scales[0]))
+    assert all(torch.equal(a, b) for a, b in zip(*made))
