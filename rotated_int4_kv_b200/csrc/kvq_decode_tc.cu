@@ -154,11 +154,11 @@ __device__ __forceinline__ void load_scales(const DtParams& P, long long crow, u
   if (crow >= 0) {
     const uint16_t* sp = P.scales + crow * (2 * NS);
     if constexpr (NS == 2) {
-      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "l"(sp));
+      asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "l"(sp));
     } else {
 #pragma unroll
       for (int i = 0; i < NS / 4; ++i)
-        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(s[4 * i]), "=r"(s[4 * i + 1]), "=r"(s[4 * i + 2]), "=r"(s[4 * i + 3])
                      : "l"(sp + 8 * i));
     }

@@ -518,3 +518,29 @@ def test_steps_in_a_row_read_what_the_call_before_wrote(kvq, path, q_hi):
         torch.cuda.synchronize()
         made.append((*outs, cache.kv_lens, cache.free_head, cache.free_pages, cache.block_table, cache.k_codes[0], cache.v_scales[0]))
     assert all(torch.equal(a, b) for a, b in zip(*made))
+
+
+@pytest.mark.parametrize("D,G,bits,n", [(128, 32, 4, 40), (256, 16, 8, 40), (256, 16, 4, 700), (128, 32, 8, 3000)])
+def test_decode_reads_what_the_encode_before_wrote(kvq, D, G, bits, n):
+    """The same slots encoded and decoded over and over without a wait: every decode gives the rows of
+    the encode in front of it, none of the one before."""
+    plan, _ = make_plan(kvq, D, "k", G=G, bits=bits)
+    pages = n // 16 + 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    xs = torch.randn(2, n, 1, D, generator=g, device="cuda").half()
+    slots = torch.randperm(pages * 16, generator=g, device="cuda")[:n].int()
+    codes = torch.zeros((pages, 1, 16, D * bits // 8), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((pages, 1, 16, D // G), dtype=torch.float16, device="cuda")
+    want = []
+    for x in xs:
+        kvq.encode_paged([(plan, x, codes, scales)], slots)
+        torch.cuda.synchronize()
+        want.append(kvq.decode_paged(plan, codes, scales, slots))
+        torch.cuda.synchronize()
+    outs = [torch.empty_like(want[0]) for _ in range(100)]
+    for i, out in enumerate(outs):
+        kvq.encode_paged([(plan, xs[i % 2], codes, scales)], slots)
+        kvq.decode_paged(plan, codes, scales, slots, out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want[i % 2]) for i, out in enumerate(outs))
