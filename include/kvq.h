@@ -88,7 +88,8 @@ typedef enum { KVQ_TRANSFORM_SRFT = 0, KVQ_TRANSFORM_SRHT = 1 } kvq_transform;
  * per-channel factors and sign masks derived from s and lambda (4 KB) and the tensor-core
  * codec's operands, Lambda R as an fp16 hi/lo pair (2 D^2 halves; D^2 for the SRHT) and
  * Lambda^-1 R^T (D^2 halves). The attention kernels' transforms depend on D, transform and
- * code width alone and are shared by the plans that live on a device (64 KB and 4 D^2 halves).
+ * code width alone: made with a device's first plan of a form (0.3 to 1.1 MB), kept for the
+ * process and shared.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA, DEVICE.
  */
 kvq_status kvq_plan_create(kvq_plan** out, int head_dim, int group, const int8_t* signs_host,

@@ -240,7 +240,7 @@ kvq_status kvq_plan_create_ex(kvq_plan** out, int D, int G, const int8_t* signs,
 
     std::unique_ptr<kvq_plan> made(new kvq_plan());
     kvq_plan* p = made.get();
-    kvq_status st = kvq::acquire_basis(dev, D, transform, bits, &p->basis);
+    kvq_status st = kvq::basis_of(D, transform, bits, &p->basis);
     if (st != KVQ_OK) return st;
     p->D = D;
     p->G = G;
@@ -304,7 +304,6 @@ kvq_status kvq_plan_destroy(kvq_plan* p) {
   cudaGetDevice(&cur);
   if (cur != p->device) cudaSetDevice(p->device);
   if (p->dblock) cudaFree(p->dblock);
-  kvq::release_basis(p->basis);
   if (cur != p->device && cur >= 0) cudaSetDevice(cur);
   delete p;
   return KVQ_OK;

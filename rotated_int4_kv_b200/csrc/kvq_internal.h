@@ -30,12 +30,10 @@ struct PlanHeader {
   float lambda[kMaxD];
 };
 
-// What plans of one device, head_dim, transform and code width share (kvq_plan_basis.cu), held
-// while one of them lives: the rotation without signs and factors.
+// What plans of one device, head_dim, transform and code width share (kvq_plan_basis.cu): the
+// rotation without signs and factors.
 struct PlanBasis {
-  int device, D, xform, bits;
-  int users = 0;
-  void* dblock = nullptr;
+  int D, xform, bits;
   const double* q_dev = nullptr;      // Q, row = channel
   const uint16_t* rot_dev = nullptr;  // F128 (see kvq_plan)
   // Paged attention, with E = Q, its rows divided by basis_dg (fp16): E (query rotation) and E^T
@@ -70,7 +68,7 @@ struct kvq_plan {
   // What it shares with other plans, and its F128: the unnormalised 128-point real DFT in
   // slot order, fp16 hi rows [128] then lo rows [128] (the attention kernels apply the
   // plans' signs and per-channel factors around it).
-  kvq::PlanBasis* basis = nullptr;
+  const kvq::PlanBasis* basis = nullptr;
   const uint16_t* rot_dev = nullptr;
   // Tensor-core decode operand in the same block: W_dec = diag(s) Q^T Lambda^-1 as fp16,
   // D rows (output samples) x D columns (channels, in the dequantiser's pair order).
@@ -114,8 +112,7 @@ kvq_status encode_tiled_new(CUtensorMap* map, CUtensorMapDataType dt, int rank, 
 int num_sms(int device);
 
 // the shared part of a plan on the current device (kvq_plan_basis.cu)
-kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out);
-void release_basis(PlanBasis* b);
+kvq_status basis_of(int D, int xform, int bits, const PlanBasis** out);
 double basis_dg(int c, int D);  // the real DFT's rows' normalisation: 1/sqrt(D), sqrt(2/D) (cos), -sqrt(2/D) (sin)
 // a plan's codec operands from its header, both on the device; returns when they are there
 kvq_status form_plan(const PlanBasis* b, const PlanHeader* head_dev, uint16_t* wt, uint16_t* wdec);

@@ -113,56 +113,54 @@ std::vector<uint16_t> make_block(int D, bool hadamard, int bits, const std::vect
 }
 
 std::mutex g_mu;
-// the host's tables, kept: constants of mathematics
-struct HostBasis {
-  std::vector<uint16_t> blk;
-  std::vector<double> q;
-};
-std::map<std::tuple<int, int, int>, HostBasis> g_host;
-// the device's, as long as a plan uses them
-std::map<std::tuple<int, int, int, int>, std::unique_ptr<PlanBasis>> g_bases;
+// Kept for the process: constants of mathematics, at most eight forms of 0.3 to 1.1 MB a context.
+// By the context's number, which no later context has: after a device reset they are made anew.
+std::map<std::tuple<unsigned long long, int, int, int>, std::unique_ptr<PlanBasis>> g_bases;
+
+// The number of the current device's context; false where there is none.
+bool context_id(unsigned long long* id) {
+  using Fn = CUresult (*)(CUcontext, unsigned long long*);
+  static const Fn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const bool ok = cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<Fn>(p) : nullptr;
+  }();
+  return fn && cudaFree(nullptr) == cudaSuccess && fn(nullptr, id) == CUDA_SUCCESS;  // (cudaFree makes the context)
+}
 
 }  // namespace
 
-kvq_status acquire_basis(int device, int D, int xform, int bits, PlanBasis** out) {
+kvq_status basis_of(int D, int xform, int bits, const PlanBasis** out) {
+  unsigned long long id = 0;
+  if (!context_id(&id)) return fail(KVQ_ERR_CUDA, "plan_create: no CUDA context");
   std::lock_guard<std::mutex> lk(g_mu);
-  auto& slot = g_bases[{device, D, xform, bits}];
+  auto& slot = g_bases[{id, D, xform, bits}];
   if (!slot) {
-    HostBasis& h = g_host[{D, xform, bits}];
-    if (h.blk.empty()) {
-      h.q = make_basis(D, xform == 1);
-      h.blk = make_block(D, xform == 1, bits, h.q);
-    }
-    auto b = std::make_unique<PlanBasis>();
-    b->device = device;
-    b->D = D;
-    b->xform = xform;
-    b->bits = bits;
-    const size_t nq = h.q.size() * 8, nblk = h.blk.size() * 2;
-    if (cudaMalloc(&b->dblock, nq + nblk) != cudaSuccess) return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
-    if (cudaMemcpy(b->dblock, h.q.data(), nq, cudaMemcpyHostToDevice) != cudaSuccess ||
-        cudaMemcpy(static_cast<char*>(b->dblock) + nq, h.blk.data(), nblk, cudaMemcpyHostToDevice) != cudaSuccess) {
-      cudaFree(b->dblock);
+    const std::vector<double> q = make_basis(D, xform == 1);
+    const std::vector<uint16_t> blk = make_block(D, xform == 1, bits, q);
+    const size_t nq = q.size() * 8, nblk = blk.size() * 2;
+    void* dev = nullptr;
+    if (cudaMalloc(&dev, nq + nblk) != cudaSuccess) return fail(KVQ_ERR_CUDA, "plan_create: cudaMalloc failed");
+    if (cudaMemcpy(dev, q.data(), nq, cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaMemcpy(static_cast<char*>(dev) + nq, blk.data(), nblk, cudaMemcpyHostToDevice) != cudaSuccess) {
+      cudaFree(dev);
       return fail(KVQ_ERR_CUDA, "plan_create: upload failed");
     }
-    b->q_dev = static_cast<const double*>(b->dblock);
-    b->rot_dev = reinterpret_cast<const uint16_t*>(b->q_dev + h.q.size());
-    b->wq_dev = b->rot_dev + rot_halves();
-    b->wo_dev = b->wq_dev + (size_t)D * D;
-    b->wqf_dev = reinterpret_cast<const uint4*>(b->wo_dev + (size_t)D * D);
-    b->wof_dev = reinterpret_cast<const uint4*>(b->wo_dev + (size_t)2 * D * D);
-    slot = std::move(b);
+    slot = std::make_unique<PlanBasis>();
+    slot->D = D;
+    slot->xform = xform;
+    slot->bits = bits;
+    slot->q_dev = static_cast<const double*>(dev);
+    slot->rot_dev = reinterpret_cast<const uint16_t*>(slot->q_dev + q.size());
+    slot->wq_dev = slot->rot_dev + rot_halves();
+    slot->wo_dev = slot->wq_dev + (size_t)D * D;
+    slot->wqf_dev = reinterpret_cast<const uint4*>(slot->wo_dev + (size_t)D * D);
+    slot->wof_dev = reinterpret_cast<const uint4*>(slot->wo_dev + (size_t)2 * D * D);
   }
-  ++slot->users;
   *out = slot.get();
   return KVQ_OK;
-}
-
-void release_basis(PlanBasis* b) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (--b->users > 0) return;
-  cudaFree(b->dblock);
-  g_bases.erase({b->device, b->D, b->xform, b->bits});
 }
 
 namespace {
