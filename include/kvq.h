@@ -437,9 +437,9 @@ kvq_status kvq_page_release(const uint8_t* done, int32_t* kv_lens, const int32_t
  * other slots are left as they were. Slots must be distinct: two tokens with the same slot
  * leave a mixture of the two.
  *   x      fp16, token i and head h at x + i * token_stride + h * head_stride elements, D
- *          contiguous (strides multiples of 8, e.g. a part of a fused projection); the
- *          strides of a dimension of size one are ignored.
- * The jobs (e.g. K and V) share n, Hkv <= 128, the slots and the page geometry, and the
+ *          contiguous (strides multiples of 8 and at least D, e.g. a part of a fused projection);
+ *          the strides of a dimension of size one are ignored.
+ * The jobs (e.g. K and V) write pages of their own and share n, Hkv <= 128, the slots, the page geometry and the
  * plans' head_dim, group, transform, code width and device; two share a launch. Always the
  * dense tensor-core encode (kvq_set_encode_path does not apply).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, DEVICE, CUDA.

@@ -17,7 +17,8 @@
 // pieces took 24 us beside the loads instead of 16: 64 ragged requests 88 -> 66 us, 4 x 128K
 // tokens 137 -> 125 us, one request of 700 tokens 13.0 -> 11.5 us.
 //
-// A CTA of attend is one producer warp and four consumer warps. The producer streams a tile's
+// A CTA of attend is one producer warp and four consumer warps; at 128 registers, for three CTAs
+// per SM, every form spills some (52 to 180 bytes a thread). The producer streams a tile's
 // pages into a ring of stages: per page one TMA box of K codes and one of V codes (swizzled for
 // ldmatrix), and the scale rows as plain bulk copies. Consumer warp w takes the w-th quarter of
 // a tile's tokens, all channels, and keeps its own softmax state and output; the warps are
@@ -32,9 +33,12 @@
 //     an fp16 word, or 16 times that in the next four): one logical operation per pair. The
 //     offset is taken out by the accumulators' start in the scores and by a product with a
 //     constant in the output, the powers of two by the query's fragments and at the end.
-//   * q~ is one fp16 rounding per element after a power-of-two normalisation per row
-//     (2^-12 relative on average, so a score's error is about 2^-12 of |q||k|/sqrt(D), below
-//     what the fp16 rounding of the caller's q has put there).
+//   * The rotation's entries are fp16, one rounding each (none for the SRHT), and q~ is one fp16
+//     rounding per element after a power-of-two normalisation per row: 2^-12 relative each on
+//     average, so a score's error is about 2^-12 of |q||k|/sqrt(D), as much as the fp16 rounding
+//     of the caller's q has put there already. hi + lo pairs would double the score products (8
+//     of 24 per 16 tokens) and the 32 or 128 KB of matrix per unit. The output's rotation takes o
+//     as hi + lo: a few products more per unit, beside latencies that hide them.
 //   * P is fp16 (its sum l is in fp32 of the unrounded values), raised to the top of fp16's
 //     range: the largest weight is 2^15, or as much less as V scales from 1 on ask for so that
 //     its product with them (one more rounding) stays within fp16 too. A running maximum's
@@ -1193,7 +1197,7 @@ constexpr size_t kPartBytes = (size_t)2 * kMaxCtas * (2 * kRows + kRows * kMaxD)
 constexpr size_t prep_bytes(int D) { return (size_t)(D / 16) * 512 + (D / 16) * 64 + kRows * 4; }
 constexpr size_t unit_bytes(int D) { return prep_bytes(D) + (2 * kRows + kRows * D) * 4 + 16; }
 constexpr int kFewRows = 32;            // query rows of a request up to which this file's kernels take every call
-constexpr long long kFewUnits = 4096;   // units up to which they may take one with more (their workspace: 28 MB)
+constexpr long long kFewUnits = 4096;   // units up to which they may take one with more (their workspace: 36 MB, 72 at D = 256)
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // units of a call with n_q query tokens, at most `rows` query rows of a request: the smaller of

@@ -27,22 +27,29 @@
 // The query's rotation and the output's un-rotation are products of the same kind: the
 // plan's matrix passes through the K tiles' ring, and each row normalises its own result.
 //
-// Chunks of 2048 tokens on 16K caches (32 / 8 heads of 128): 0.93 ms in single calls, 1.0 back
-// to back under the power cap (793 TFLOP/s, 58 % of the sustained matrix rate); 8 rows at a
-// time with register products it was 15.2 ms. A tile of 256 x 128 takes about 4500 cycles, of
-// which the products 2048; a softmax warp spends 1000 on the maxima, 2000 on P (the exponential
-// unit serves two such warps per scheduler). Bound by that chain and by the instruction caches:
-// longer (more unrolled) forms of any role slowed all of them.
+// Chunks of 2048 tokens on 16K caches (32 / 8 heads of 128): 1.03 ms back to back under the
+// power cap (785 TFLOP/s, 57 % of the sustained matrix rate), 8-bit codes 1.08 ms, 4 / 1 heads of
+// 256 0.41 ms (495 TFLOP/s); 8 rows at a time with register products the first was 15.2 ms. A
+// tile of 256 x 128 takes about 4500 cycles, of which the products 2048; a softmax warp spends
+// 1000 on the maxima, 2000 on P (the exponential unit serves two such warps per scheduler). Bound
+// by that chain and by the instruction caches: longer (more unrolled) forms of any role slowed
+// all of them.
 //
-// Number formats. K and V are fp16 c * scale: exact multiples of 2^-24 below 2^-13 and one
-// rounding (2^-12 on average) elsewhere; a tile with a scale from 2^12 (int8: 2^9) on is held
-// divided by 2^8, so that no product leaves fp16, and O is brought to the power of the tile
-// that is added next (beside such a scale, V below 2^-6 in the same tile keeps 2^-17 of 1, not
-// its own 11 bits). q~ and O enter their products as one fp16 rounding after a
-// power-of-two normalisation per row, P as one fp16 rounding, its largest value between 2^7
-// and 2^15: weights down to 2^-21 of the largest keep 2^-12 on average, smaller ones an error of
-// at most 2^-32 of the largest. S, O, the maxima and sums are fp32. A token whose V scale is not finite is held as zeros and the rows that attend it
-// (and no others) are set to NaN at the end.
+// Number formats, each chosen for products of one fp16 tile per operand (a hi + lo pair would
+// double their number and the shared memory they wait for):
+//   * K and V are fp16 c * scale: exact multiples of 2^-24 below 2^-13 and one rounding (2^-12
+//     on average) elsewhere. A tile with a scale from 2^12 (int8: 2^9) on is held divided by 2^8,
+//     so that no product leaves fp16, and O is brought to the power of the tile that is added
+//     next (beside such a scale, V below 2^-6 in the same tile keeps 2^-17 of 1, not its own 11
+//     bits).
+//   * The rotation's entries are one fp16 rounding each (none for the SRHT); q~ is one after a
+//     power-of-two normalisation per row, as is o before the output's rotation. The join of cut
+//     units takes o as hi + lo, which costs nothing beside reading the partials; whole units would
+//     pay about 2 us each for it, so a row may be 10 % nearer the formula where its unit is cut.
+//   * P is one fp16 rounding, its largest value between 2^7 and 2^15: weights down to 2^-21 of
+//     the largest keep 2^-12 on average, smaller ones an error of at most 2^-32 of the largest.
+//   * S, O, the maxima and sums are fp32. A token whose V scale is not finite is held as zeros and
+//     the rows that attend it (and no others) are set to NaN at the end.
 #include <algorithm>
 #include <cmath>
 #include <string>

@@ -88,7 +88,7 @@ def page_release(done, kv_lens, block_table, free_pages, free_head, page_size: i
 
 def encode_paged(jobs, slots, stream=None) -> None:
     """Encode tokens into pages: ``jobs`` is a sequence of (plan, x, codes, scales), x fp16
-    [n, Hkv, D] (any token and head strides that are multiples of 8, e.g. a slice of a fused
+    [n, Hkv, D] (any token and head strides from D on that are multiples of 8, e.g. a slice of a fused
     projection), ``slots`` int32 [n] shared by all jobs; a slot outside the pages (-1) skips its
     token. Two jobs (K and V) share a launch. See kvq_encode_paged."""
     _paged.encode_paged(jobs, slots, None if stream is None else stream.cuda_stream)
@@ -131,9 +131,11 @@ def attend_paged(pk: Plan, pv: Plan, q, k_codes, k_scales, v_codes, v_scales, bl
     q fp16 [n, Hq, D] (token and head strides multiples of 8); block_table int32 [B, max_pages];
     kv_lens int32 [B], the new tokens included; q_starts int32 [B + 1] or None for one query token
     per request (n == B). ``max_q_len`` / ``max_kv_len`` bound the lengths, which the host cannot
-    see (defaults: n and the table's capacity); tight bounds pick the right kernel.
+    see (defaults: n and the table's capacity); tight bounds choose the kernel best and save a few
+    microseconds.
     ``window`` > 0: each token attends the last ``window`` tokens up to itself. Returns fp16
-    [n, Hq, D]; rows of ``out`` that belong to no request are left as they were."""
+    [n, Hq, D]; rows of ``out`` that belong to no request are left as they were (without ``out``:
+    with any contents)."""
     return _paged.attend_paged(pk, pv, q, k_codes, k_scales, v_codes, v_scales, block_table, kv_lens, q_starts, max_q_len,
                                max_kv_len, window, softmax_scale, out, workspace,
                                None if stream is None else stream.cuda_stream)
