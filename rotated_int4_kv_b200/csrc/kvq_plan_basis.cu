@@ -188,8 +188,10 @@ __global__ void __launch_bounds__(kMaxD) form_plan_kernel(const double* q, const
 }  // namespace
 
 kvq_status form_plan(const PlanBasis* b, const PlanHeader* head_dev, uint16_t* wt, uint16_t* wdec) {
-  form_plan_kernel<<<b->D, b->D>>>(b->q_dev, head_dev, b->D, b->xform == 1, b->bits, wt, wdec);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(b->D);
+  cfg.blockDim = dim3(b->D);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, form_plan_kernel, b->q_dev, head_dev, b->D, b->xform == 1, b->bits, wt, wdec);
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, std::string("plan_create: ") + cudaGetErrorString(e));
   return KVQ_OK;
